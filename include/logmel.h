@@ -365,6 +365,163 @@ int logmel_resample(const logmel_resampler* r, const void* d_samples, int sample
                     const int64_t* d_sample_offsets, const int64_t* d_out_offsets,
                     int64_t n_clips, int64_t total_out, float* d_out, void* hip_stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators over packed rows, for the layers that take the front end's rows:
+ * a gated recurrence along each sequence, and the norms around a block. The
+ * rows are those of logmel_compute (clip i's frames are rows
+ * [frame_offsets[i], frame_offsets[i+1])) or of a push (stream j's new frames
+ * are rows [fo[j], fo[j+1])), of any width.
+ *
+ * Conventions beside those above:
+ *  - A row operand is [rows][channels] of `type` (LOGMEL_F32, LOGMEL_F16 or
+ *    LOGMEL_BF16, one type for all row operands of a call), each row
+ *    contiguous, row r at element r * stride of its pointer (stride >=
+ *    channels, so the column slices of one wider product are operands as
+ *    they are). Any element alignment is accepted. Arithmetic, sums and
+ *    states are fp32; a row output is rounded once, to nearest even.
+ *  - Parameters, states and their gradients are contiguous fp32.
+ *  - An output may not overlap another operand (INVALID_ARGUMENT), except
+ *    where a call says so.
+ *  - The work is split by the sizes alone and every sum is taken in a fixed
+ *    order: the same call gives the same bits.
+ * --------------------------------------------------------------------------- */
+#define LOGMEL_BF16 3 /* bfloat16, of these operators' rows only */
+
+/* The gated scan. For each sequence and channel, with a_t = sigmoid(gate_t +
+ * bias) and u_t = 1 - a_t = sigmoid(-(gate_t + bias)),
+ *     h_t = a_t h_{t-1} + u_t x_t,
+ * h_{-1} the sequence's row of d_state (zero if d_state is NULL).
+ * Products are plain IEEE: a NaN or infinity in x or gate stays in its
+ * sequence and channel, from its row on. */
+typedef struct logmel_scan_input {
+  int32_t type;
+  int64_t rows;                 /* rows of the row operands */
+  int64_t channels;             /* >= 1 */
+  int64_t n_seq;                /* sequence i is rows [d_seq_offsets[i], d_seq_offsets[i+1]) */
+  const int64_t* d_seq_offsets; /* int64[n_seq + 1], non-decreasing, the first 0, the last at most
+                                   rows; rows from the last on belong to no sequence: they are not
+                                   read and their outputs are not written. A precondition that is
+                                   not read back: other offsets give wrong rows, but no access
+                                   outside the operands (LOGMEL_VALIDATE=1 checks them, with one
+                                   synchronisation) */
+  int64_t max_frames;           /* rows of the longest sequence, or 0 if not known: chooses how the
+                                   work is split, never what is computed */
+  const void* d_x;
+  int64_t x_stride;
+  const void* d_gate;
+  int64_t gate_stride;
+  const float* d_bias;          /* [channels] or NULL (0) */
+  const float* d_state;         /* [n_seq][channels] or NULL (0) */
+} logmel_scan_input;
+
+/* Rows of the checkpoint array for `rows` rows: ceil(rows / 128); -1 for a
+ * negative count. */
+#define LOGMEL_SCAN_CHECKPOINT 128
+int64_t logmel_gated_scan_checkpoint_rows(int64_t rows);
+
+/* Bytes of device workspace a call needs (0: none, d_workspace may be NULL);
+ * -1 for bad arguments. backward: 0 for logmel_gated_scan, 1 for its
+ * gradient. The workspace must be 16-byte aligned; its contents mean nothing
+ * before or after a call, and calls that may overlap on the device need one
+ * each. */
+int64_t logmel_gated_scan_workspace(const logmel_plan* plan, const logmel_scan_input* in,
+                                    int backward);
+
+/* Writes d_h (row operand), and where not NULL
+ *   d_state_out    [n_seq][channels]: each sequence's last h (its initial
+ *                  state if it is empty); may be d_state itself
+ *   d_checkpoints  [logmel_gated_scan_checkpoint_rows(rows)][channels]: row k
+ *                  is h before row 128 k, where row 128 k continues a sequence
+ *                  (other rows are unspecified); what the gradient reads.
+ * INPUT_TOO_LONG if rows * stride or n_seq * channels overflows. */
+int logmel_gated_scan(const logmel_plan* plan, const logmel_scan_input* in, void* d_h,
+                      int64_t h_stride, float* d_state_out, float* d_checkpoints,
+                      void* d_workspace, int64_t workspace_bytes, void* hip_stream);
+
+/* Gradient of logmel_gated_scan for the same inputs. With dh the gradient of
+ * h and D_t = dh_t + a_{t+1} D_{t+1} (after a sequence's last row its row of
+ * d_dstate_out, zero if NULL):
+ *     dx = u D,  dgate = a u (h_{t-1} - x) D,  dbias = sum of dgate over the
+ *     rows,  dstate = a_0 D_0 (of an empty sequence: its row of dstate_out).
+ *   d_checkpoints  what the forward call wrote; the states between are
+ *                  formed anew from x and gate
+ *   d_dx, d_dgate  row outputs; d_dbias [channels] and d_dstate
+ *                  [n_seq][channels] may be NULL. */
+typedef struct logmel_scan_grad {
+  const void* d_dh;
+  int64_t dh_stride;
+  const float* d_dstate_out;
+  void* d_dx;
+  int64_t dx_stride;
+  void* d_dgate;
+  int64_t dgate_stride;
+  float* d_dbias;
+  float* d_dstate;
+} logmel_scan_grad;
+int logmel_gated_scan_backward(const logmel_plan* plan, const logmel_scan_input* in,
+                               const float* d_checkpoints, const logmel_scan_grad* grad,
+                               void* d_workspace, int64_t workspace_bytes, void* hip_stream);
+
+/* The block norm: what stands between one block's product and the next
+ * block's. For each row, with rms(v) = sqrt(mean(v^2) + eps),
+ *     t = h / rms(h) * w_post * silu(gate),   silu(g) = g sigmoid(g)
+ *     y = res + scale * t
+ *     z = y / rms(y) * w_pre      (of y before it is rounded)
+ * d_h NULL: y = res (the norm before a first block, as of log-mel rows).
+ * d_gate NULL: no silu factor. d_w_post, d_scale, d_w_pre NULL: 1. gate,
+ * w_post and scale without h are INVALID_ARGUMENT. channels 1..8192
+ * (UNSUPPORTED beyond); eps a finite number >= 0 (a row of zeros with eps 0
+ * gives NaN). */
+#define LOGMEL_NORM_MAX_CHANNELS 8192
+typedef struct logmel_norm_input {
+  int32_t type;
+  int64_t rows;
+  int64_t channels;
+  const void* d_res;
+  int64_t res_stride;
+  const void* d_h;
+  int64_t h_stride;
+  const void* d_gate;
+  int64_t gate_stride;
+  const float* d_w_post; /* [channels], as the next two */
+  const float* d_scale;
+  const float* d_w_pre;
+  float eps;
+} logmel_norm_input;
+
+/* Writes y and z (row outputs; either may be NULL, not both; y without h is
+ * INVALID_ARGUMENT: it would be a copy). */
+int logmel_block_norm(const logmel_plan* plan, const logmel_norm_input* in, void* d_y,
+                      int64_t y_stride, void* d_z, int64_t z_stride, void* hip_stream);
+
+/* Gradient of logmel_block_norm: from d_dy and d_dz (NULL: zero; not both
+ * NULL) the gradients of res, h and gate (row outputs; dh and dgate exactly
+ * where h and gate are given, else INVALID_ARGUMENT) and of the parameters
+ * ([channels]; each may be NULL, and must be where its factor is absent: no h
+ * for dw_post and dscale, no dz for dw_pre). Parameter sums are fp32 over
+ * fixed parts of the rows, joined in order. */
+typedef struct logmel_norm_grad {
+  const void* d_dy;
+  int64_t dy_stride;
+  const void* d_dz;
+  int64_t dz_stride;
+  void* d_dres;
+  int64_t dres_stride;
+  void* d_dh;
+  int64_t dh_stride;
+  void* d_dgate;
+  int64_t dgate_stride;
+  float* d_dw_post;
+  float* d_dscale;
+  float* d_dw_pre;
+} logmel_norm_grad;
+/* Bytes of device workspace the gradient needs, as
+ * logmel_gated_scan_workspace. */
+int64_t logmel_block_norm_workspace(const logmel_plan* plan, const logmel_norm_input* in);
+int logmel_block_norm_backward(const logmel_plan* plan, const logmel_norm_input* in,
+                               const logmel_norm_grad* grad, void* d_workspace,
+                               int64_t workspace_bytes, void* hip_stream);
+
 /* Names a status code (a static string; "unknown status" for codes this
  * library does not return). Every failure is an explicit negative code and
  * over-long input is an error, never a silent truncation: the convention

@@ -36,6 +36,9 @@ CHUNK_FRAMES = 3000   # LOGMEL_CHUNK_FRAMES
 LOGMEL_F32 = 0
 LOGMEL_I16 = 1
 LOGMEL_F16 = 2
+LOGMEL_BF16 = 3       # rows of the row operators only
+SCAN_CHECKPOINT = 128   # LOGMEL_SCAN_CHECKPOINT
+NORM_MAX_CHANNELS = 8192   # LOGMEL_NORM_MAX_CHANNELS
 N_FFT = 400
 HOP = 160
 SAMPLE_RATE = 16000
@@ -50,6 +53,32 @@ class logmel_config(ctypes.Structure):
                 ("hop", ctypes.c_int32), ("n_mels", ctypes.c_int32),
                 ("f_min", ctypes.c_double), ("f_max", ctypes.c_double),
                 ("log_floor", ctypes.c_double), ("device", ctypes.c_int32)]
+
+
+class logmel_scan_input(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("rows", _i64), ("channels", _i64), ("n_seq", _i64),
+                ("d_seq_offsets", _p), ("max_frames", _i64), ("d_x", _p), ("x_stride", _i64),
+                ("d_gate", _p), ("gate_stride", _i64), ("d_bias", _p), ("d_state", _p)]
+
+
+class logmel_scan_grad(ctypes.Structure):
+    _fields_ = [("d_dh", _p), ("dh_stride", _i64), ("d_dstate_out", _p), ("d_dx", _p),
+                ("dx_stride", _i64), ("d_dgate", _p), ("dgate_stride", _i64), ("d_dbias", _p),
+                ("d_dstate", _p)]
+
+
+class logmel_norm_input(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("rows", _i64), ("channels", _i64), ("d_res", _p),
+                ("res_stride", _i64), ("d_h", _p), ("h_stride", _i64), ("d_gate", _p),
+                ("gate_stride", _i64), ("d_w_post", _p), ("d_scale", _p), ("d_w_pre", _p),
+                ("eps", ctypes.c_float)]
+
+
+class logmel_norm_grad(ctypes.Structure):
+    _fields_ = [("d_dy", _p), ("dy_stride", _i64), ("d_dz", _p), ("dz_stride", _i64),
+                ("d_dres", _p), ("dres_stride", _i64), ("d_dh", _p), ("dh_stride", _i64),
+                ("d_dgate", _p), ("dgate_stride", _i64), ("d_dw_post", _p), ("d_dscale", _p),
+                ("d_dw_pre", _p)]
 
 
 def _sig(name, res, *args):
@@ -100,6 +129,18 @@ _resampler_destroy = _sig("logmel_resampler_destroy", None, _p)
 _resampler_info = _sig("logmel_resampler_info", ctypes.c_int, _p, _i64p, _i64p)
 _resample = _sig("logmel_resample", ctypes.c_int, _p, _p, ctypes.c_int, _p, _p, _i64, _i64, _p,
                  _p)
+_scan_in_p = ctypes.POINTER(logmel_scan_input)
+_norm_in_p = ctypes.POINTER(logmel_norm_input)
+_gated_scan_checkpoint_rows = _sig("logmel_gated_scan_checkpoint_rows", _i64, _i64)
+_gated_scan_workspace = _sig("logmel_gated_scan_workspace", _i64, _p, _scan_in_p, ctypes.c_int)
+_gated_scan = _sig("logmel_gated_scan", ctypes.c_int, _p, _scan_in_p, _p, _i64, _p, _p, _p, _i64,
+                   _p)
+_gated_scan_backward = _sig("logmel_gated_scan_backward", ctypes.c_int, _p, _scan_in_p, _p,
+                            ctypes.POINTER(logmel_scan_grad), _p, _i64, _p)
+_block_norm = _sig("logmel_block_norm", ctypes.c_int, _p, _norm_in_p, _p, _i64, _p, _i64, _p)
+_block_norm_workspace = _sig("logmel_block_norm_workspace", _i64, _p, _norm_in_p)
+_block_norm_backward = _sig("logmel_block_norm_backward", ctypes.c_int, _p, _norm_in_p,
+                            ctypes.POINTER(logmel_norm_grad), _p, _i64, _p)
 
 EXPORTED = [
     "logmel_default_config", "logmel_abi_version", "logmel_status_string",
@@ -112,6 +153,9 @@ EXPORTED = [
     "logmel_stream_get_state", "logmel_stream_set_state", "logmel_resample_length",
     "logmel_resample_offsets", "logmel_resampler_create", "logmel_resampler_destroy",
     "logmel_resampler_info", "logmel_resample", "logmel_stream_push_static",
+    "logmel_gated_scan_checkpoint_rows", "logmel_gated_scan_workspace", "logmel_gated_scan",
+    "logmel_gated_scan_backward", "logmel_block_norm", "logmel_block_norm_workspace",
+    "logmel_block_norm_backward",
 ]
 
 STATIC_MAX_STREAMS = 512   # LOGMEL_STATIC_MAX_STREAMS
@@ -625,3 +669,230 @@ def resample(r: Resampler, samples, sample_offsets_host, stream=None):
     y = logmel_resample(r, samples, torch.from_numpy(so).to(dev), torch.from_numpy(oo).to(dev),
                         int(oo[-1]), stream=stream)
     return y, oo
+
+
+# ----------------------------------------------- operators over packed rows
+
+_ROW_TYPES: dict = {}
+
+
+def _row_type(dtype):
+    if not _ROW_TYPES:
+        torch = _torch()
+        _ROW_TYPES.update({torch.float32: LOGMEL_F32, torch.float16: LOGMEL_F16,
+                           torch.bfloat16: LOGMEL_BF16})
+    t = _ROW_TYPES.get(dtype)
+    if t is None:
+        raise TypeError(f"rows must be float32, float16 or bfloat16, got {dtype}")
+    return t
+
+
+def _rows(t, what, like, plan):
+    """(address, row stride) of a row operand [rows, channels] like ``like``;
+    (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a torch tensor on a ROCm device")
+    if t.device.index != plan.device:
+        raise ValueError(f"{what} must be on the plan's device {plan.device}, got {t.device}")
+    if t.dtype != like.dtype:
+        raise TypeError(f"{what} must be {like.dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape != like.shape:
+        raise ValueError(f"{what} must be [rows, channels] = {list(like.shape)}, "
+                         f"got {list(t.shape)}")
+    rows, channels = t.shape
+    if channels > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have contiguous rows")
+    stride = t.stride(0)
+    if rows <= 1:
+        stride = max(stride, channels)
+    if stride < channels:
+        raise ValueError(f"{what} must not repeat or overlap rows")
+    # an empty operand has no address; any aligned one stands for it
+    return (t.data_ptr() or 16), stride
+
+
+def _params(t, what, shape, plan):
+    """Address of a contiguous fp32 tensor of that shape; None for None."""
+    if t is None:
+        return None
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a torch tensor on a ROCm device")
+    if t.device.index != plan.device:
+        raise ValueError(f"{what} must be on the plan's device {plan.device}, got {t.device}")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{what} must be torch.float32, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr() or None
+
+
+def _empty(shape, dtype, device, stream):
+    """A tensor the call writes on ``stream``: from that stream's memory, so
+    that neither its last use nor its next one can run beside the call."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace(need, device, stream, what):
+    """(tensor, address) of ``need`` bytes of workspace for one call."""
+    if need < 0:
+        raise LogmelError(LOGMEL_ERR_INVALID_ARGUMENT, what)
+    if need == 0:
+        return None, None
+    ws = _empty((need,), _torch().uint8, device, stream)
+    return ws, ws.data_ptr()
+
+
+def _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames):
+    torch = _torch()
+    ty = _row_type(x.dtype)
+    px, sx = _rows(x, "x", x, plan)
+    pg, sg = _rows(gate, "gate", x, plan)
+    rows, channels = x.shape
+    n_seq = int(seq_offsets.numel()) - 1
+    if seq_offsets.dim() != 1 or n_seq < 0:
+        raise ValueError("seq_offsets must have n_seq + 1 entries")
+    if seq_offsets.device != x.device:
+        raise ValueError("seq_offsets must be on the device of x")
+    po = _dev_ptr(seq_offsets, torch.int64, "seq_offsets").value
+    return logmel_scan_input(ty, rows, channels, n_seq, po, int(max_frames), px, sx, pg, sg,
+                             _params(bias, "bias", (channels,), plan),
+                             _params(state, "state", (n_seq, channels), plan))
+
+
+def logmel_gated_scan_checkpoint_rows(rows: int) -> int:
+    """Rows of the checkpoint array [.., channels] for ``rows`` rows."""
+    return int(_gated_scan_checkpoint_rows(int(rows)))
+
+
+def logmel_gated_scan(plan: Plan, x, gate, seq_offsets, bias=None, state=None, out=None,
+                      state_out=None, checkpoints=None, max_frames: int = 0, stream=None):
+    """h_t = a_t h_{t-1} + (1 - a_t) x_t with a = sigmoid(gate + bias), along
+    each packed sequence; returns h [rows, channels].
+
+    x, gate (and out): [rows, channels] float32, float16 or bfloat16 with
+    contiguous rows at any row stride; sequence i is rows
+    [seq_offsets[i], seq_offsets[i + 1]) (int64 [n_seq + 1] on the device; rows
+    from the last offset on stay as they are in out). bias [channels], state
+    [n_seq, channels] (h before each sequence, default 0) and state_out (h
+    after it; may be state) are fp32. checkpoints, fp32
+    [logmel_gated_scan_checkpoint_rows(rows), channels], receives what
+    logmel_gated_scan_backward needs. max_frames (the longest sequence's rows,
+    0: not known) only chooses how the work is split."""
+    inp = _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames)
+    if out is None:
+        out = _empty(x.shape, x.dtype, x.device, stream)
+    po, so = _rows(out, "out", x, plan)
+    pso = _params(state_out, "state_out", (inp.n_seq, inp.channels), plan)
+    pck = _params(checkpoints, "checkpoints",
+                  (_gated_scan_checkpoint_rows(inp.rows), inp.channels), plan)
+    need = _gated_scan_workspace(plan.handle, inp, 0)
+    ws, pws = _workspace(need, x.device, stream, "logmel_gated_scan")
+    _check(_gated_scan(plan.handle, inp, po, so, pso, pck, pws, need,
+                       _stream_handle(stream, x.device)), "logmel_gated_scan")
+    return out
+
+
+def logmel_gated_scan_backward(plan: Plan, dh, x, gate, seq_offsets, checkpoints, bias=None,
+                               state=None, dstate_out=None, dx=None, dgate=None,
+                               max_frames: int = 0, stream=None):
+    """Gradient of logmel_gated_scan for the same x, gate, seq_offsets, bias
+    and state, from dh and dstate_out (None: 0), with the checkpoints the
+    forward call wrote; returns (dx, dgate, dbias or None, dstate or None):
+    dbias where bias is given, dstate where state is. Rows from the last
+    offset on stay as they are in dx and dgate."""
+    inp = _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames)
+    dx = _empty(x.shape, x.dtype, x.device, stream) if dx is None else dx
+    dgate = _empty(x.shape, x.dtype, x.device, stream) if dgate is None else dgate
+    dbias = None if bias is None else _empty(bias.shape, bias.dtype, x.device, stream)
+    dstate = None if state is None else _empty(state.shape, state.dtype, x.device, stream)
+    states = (inp.n_seq, inp.channels)
+    pd, sd = _rows(dh, "dh", x, plan)
+    px, sx = _rows(dx, "dx", x, plan)
+    pg, sg = _rows(dgate, "dgate", x, plan)
+    grad = logmel_scan_grad(pd, sd, _params(dstate_out, "dstate_out", states, plan), px, sx, pg,
+                            sg, _params(dbias, "dbias", (inp.channels,), plan),
+                            _params(dstate, "dstate", states, plan))
+    pck = _params(checkpoints, "checkpoints",
+                  (_gated_scan_checkpoint_rows(inp.rows), inp.channels), plan)
+    need = _gated_scan_workspace(plan.handle, inp, 1)
+    ws, pws = _workspace(need, x.device, stream, "logmel_gated_scan_backward")
+    _check(_gated_scan_backward(plan.handle, inp, pck, grad, pws, need,
+                                _stream_handle(stream, x.device)), "logmel_gated_scan_backward")
+    return dx, dgate, dbias, dstate
+
+
+def _norm_input(plan, res, h, gate, w_post, scale, w_pre, eps):
+    ty = _row_type(res.dtype)
+    pr, sr = _rows(res, "res", res, plan)
+    rows, channels = res.shape
+    ph, sh = _rows(h, "h", res, plan)
+    pg, sg = _rows(gate, "gate", res, plan)
+    return logmel_norm_input(ty, rows, channels, pr, sr, ph, sh, pg, sg,
+                             _params(w_post, "w_post", (channels,), plan),
+                             _params(scale, "scale", (channels,), plan),
+                             _params(w_pre, "w_pre", (channels,), plan), float(eps))
+
+
+def logmel_block_norm(plan: Plan, res, h=None, gate=None, w_post=None, scale=None, w_pre=None,
+                      eps: float = 1e-6, y=None, z=None, want_y: bool = True,
+                      want_z: bool = True, stream=None):
+    """y = res + scale * (h / rms(h) * w_post * silu(gate)) and
+    z = y / rms(y) * w_pre, row by row; returns (y, z).
+
+    res, h, gate (and y, z): [rows, channels] float32, float16 or bfloat16 with
+    contiguous rows at any row stride; w_post, scale, w_pre: fp32 [channels];
+    what is None drops out. Without h, y is res and only z is formed. want_y
+    and want_z False leave that output out (None)."""
+    inp = _norm_input(plan, res, h, gate, w_post, scale, w_pre, eps)
+    if y is None and want_y and h is not None:
+        y = _empty(res.shape, res.dtype, res.device, stream)
+    if z is None and want_z:
+        z = _empty(res.shape, res.dtype, res.device, stream)
+    py, sy = _rows(y, "y", res, plan)
+    pz, sz = _rows(z, "z", res, plan)
+    _check(_block_norm(plan.handle, inp, py, sy, pz, sz, _stream_handle(stream, res.device)),
+           "logmel_block_norm")
+    return y, z
+
+
+def logmel_block_norm_backward(plan: Plan, res, h=None, gate=None, w_post=None, scale=None,
+                               w_pre=None, eps: float = 1e-6, dy=None, dz=None, dres=None,
+                               dh=None, dgate=None, stream=None):
+    """Gradient of logmel_block_norm for the same operands, from dy and dz
+    (None: 0, not both); returns a dict with dres, dh, dgate, dw_post, dscale
+    and dw_pre, each None where its operand is (dw_pre also where dz is)."""
+    inp = _norm_input(plan, res, h, gate, w_post, scale, w_pre, eps)
+
+    def rows(t, of):
+        if t is not None or of is None:
+            return t
+        return _empty(res.shape, res.dtype, res.device, stream)
+
+    def param(of):
+        return None if of is None else _empty(of.shape, of.dtype, res.device, stream)
+
+    out = dict(dres=rows(dres, res), dh=rows(dh, h), dgate=rows(dgate, gate),
+               dw_post=param(w_post), dscale=param(scale),
+               dw_pre=None if dz is None else param(w_pre))
+    ptrs = []
+    for t, what in ((dy, "dy"), (dz, "dz"), (out["dres"], "dres"), (out["dh"], "dh"),
+                    (out["dgate"], "dgate")):
+        ptrs.extend(_rows(t, what, res, plan))
+    for k in ("dw_post", "dscale", "dw_pre"):
+        ptrs.append(_params(out[k], k, (inp.channels,), plan))
+    grad = logmel_norm_grad(*ptrs)
+    need = _block_norm_workspace(plan.handle, inp)
+    ws, pws = _workspace(need, res.device, stream, "logmel_block_norm_backward")
+    _check(_block_norm_backward(plan.handle, inp, grad, pws, need,
+                                _stream_handle(stream, res.device)),
+           "logmel_block_norm_backward")
+    return out

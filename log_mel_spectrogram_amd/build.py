@@ -37,6 +37,8 @@ def build(verbose: bool = False) -> str:
            os.path.join(CSRC, "logmel_kernels.hip"), os.path.join(CSRC, "logmel_resample.hip"),
            os.path.join(CSRC, "logmel_stream.hip"),
            os.path.join(CSRC, "logmel_static.hip"),
+           os.path.join(CSRC, "logmel_scan.hip"), os.path.join(CSRC, "logmel_norm.hip"),
+           os.path.join(CSRC, "logmel_rows_api.cpp"),
            os.path.join(CSRC, "logmel_api.cpp"),
            "-o", tmp]
     if verbose:

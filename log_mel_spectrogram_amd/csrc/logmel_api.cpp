@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "logmel_launch.h"
+#include "logmel_plan.h"
 #include "logmel_resample_launch.h"
 #include "logmel_slots.h"
 
@@ -23,24 +24,6 @@ constexpr int kMels = 128;
 constexpr int64_t kChunkFrames = LOGMEL_CHUNK_FRAMES;   // 30 s of 10 ms frames
 constexpr int kRing = 400;  // carry capacity in front of each workspace row
 
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) { ok = false; return; }
-    if (prev != dev && hipSetDevice(dev) != hipSuccess) ok = false;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
-
-bool env_validate() {
-  const char* v = std::getenv("LOGMEL_VALIDATE");
-  return v && v[0] && v[0] != '0';
-}
-
 int64_t frames_of(int64_t n) { return n < kNFFT ? 0 : (n - kNFFT) / kHop + 1; }
 
 }  // namespace
@@ -51,12 +34,6 @@ static const double kHostWindow[200] = {
 };
 static const double kHostRot400[200] = {
 #include "logmel_rot400.inc"
-};
-
-struct logmel_plan {
-  logmel_config cfg;
-  double* tables = nullptr;  // device, kTabBytes
-  int resident_waves = 0;    // wavefronts of the transform kernel resident at once: one per SIMD
 };
 
 // ---------------------------------------------------------------------------
