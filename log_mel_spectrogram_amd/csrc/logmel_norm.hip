@@ -36,7 +36,7 @@ struct NormGradArgs {
   int64_t dhs;
   T* dgate;
   int64_t dgates;
-  float* part;   // [workgroups][3][channels]: dw_post, dscale, dw_pre
+  double* part;   // [workgroups][3][channels]: dw_post, dscale, dw_pre
 };
 
 // Sum over the workgroup's 4 wavefronts, in every lane.
@@ -63,7 +63,7 @@ struct Cell {
     if (p.o) {
       const float o = (float)p.o[r * p.os + c];
       float a, u;
-      gate_pair<T>(o, a, u);
+      Gate<T>::pair(o, 0.0f, a, u);
       act = o * a;
       slope = a * __builtin_fmaf(o, u, 1.0f);
     }
@@ -103,9 +103,9 @@ __global__ __launch_bounds__(256) void logmel_norm_simple_kernel(NormArgs<T> p, 
 template <typename T>
 __global__ __launch_bounds__(256) void logmel_norm_backward_simple_kernel(NormArgs<T> p,
                                                                           NormGradArgs<T> q) {
-  float* part = q.part + (int64_t)blockIdx.x * 3 * p.channels;
+  double* part = q.part + (int64_t)blockIdx.x * 3 * p.channels;
   for (int64_t c = threadIdx.x; c < p.channels; c += 256)
-    part[c] = part[p.channels + c] = part[2 * p.channels + c] = 0.0f;
+    part[c] = part[p.channels + c] = part[2 * p.channels + c] = 0.0;
   const float inv = 1.0f / (float)p.channels;
   for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
     float r1 = 0.0f;
@@ -202,7 +202,7 @@ hipError_t launch_norm_backward(const logmel_norm_input& in, const logmel_norm_g
                     g.dh_stride,
                     static_cast<T*>(g.d_dgate),
                     g.dgate_stride,
-                    static_cast<float*>(ws)};
+                    static_cast<double*>(ws)};
   const int64_t parts = norm_parts(in.rows, cus);
   if (parts)
     logmel_norm_backward_simple_kernel<T>
@@ -220,7 +220,7 @@ hipError_t launch_norm_backward(const logmel_norm_input& in, const logmel_norm_g
 }  // namespace logmel
 
 int64_t logmel_norm_workspace(const logmel_norm_input& in, int cus) {
-  return logmel::norm_parts(in.rows, cus) * 3 * in.channels * 4;
+  return logmel::norm_parts(in.rows, cus) * 3 * in.channels * 8;
 }
 
 hipError_t logmel_launch_norm(const logmel_norm_input& in, void* y, int64_t y_stride, void* z,

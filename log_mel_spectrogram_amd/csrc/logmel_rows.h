@@ -32,28 +32,42 @@ __device__ __forceinline__ void row_store(T* p, const float (&x)[V]) {
   __builtin_memcpy(p, &r, sizeof(r));
 }
 
-// sigmoid(g) and sigmoid(-g), each to full relative precision: e = e^-|g| is
-// at most 1, so neither is formed as 1 minus the other. A NaN gives two NaN.
-// fp32 rows correct e for the rounding of |g| log2(e) (|g| 2^-24 relative in
-// e, ten ulps at |g| = 10); 2-byte rows, whose own rounding is 2^-11 or 2^-8,
-// do without those four instructions.
+// sigmoid(g + bias) and sigmoid(-(g + bias)), each to full relative precision:
+// with e = e^-(g + bias) they are r = 1 / (1 + e) and e r, and neither is
+// formed as 1 minus the other. The exponent is kept below 2^126 so that e is
+// finite and r is not flushed: from g + bias = -87 on down, r stays at 1e-38.
+// minimum and maximum are those that return a NaN operand, so a NaN gate gives
+// two NaN. Four instructions beside the two transcendentals, which take as
+// long: the recurrence reads 4 bytes per value and is held up by instructions
+// as much as by memory (see the tiles).
+// 2-byte rows take the bias into the exponent's multiply-add (nb = -bias
+// log2(e)): e is off by (|g + bias| + |bias|) 2^-24 relative. fp32 rows add
+// first and correct e for the rounding of the product (|g| 2^-24 in e, ten
+// ulps at |g| = 10).
 template <typename T>
-__device__ __forceinline__ void gate_pair(float g, float& a, float& u) {
-  constexpr float kLog2e = 1.44269504088896340736f;
-  const float x = -__builtin_fabsf(g);
-  const float t = x * kLog2e;
-  float e = __builtin_amdgcn_exp2f(t);
-  if constexpr (sizeof(T) == 4) {
-    constexpr float kLn2 = 0.693147180559945309417f;
-    constexpr float kLog2eRest = (float)(1.44269504088896340735992468 - (double)kLog2e);
-    const float rest = __builtin_fmaf(x, kLog2eRest, __builtin_fmaf(x, kLog2e, -t));
-    // e is 0 from x = -inf on down: rest is NaN at -inf
-    e = e == 0.0f ? e : __builtin_fmaf(e, rest * kLn2, e);
+struct Gate {
+  static constexpr float kLog2e = 1.44269504088896340736f;
+  static __device__ __forceinline__ float bias_of(float bias) {
+    return sizeof(T) == 4 ? bias : -bias * kLog2e;
   }
-  const float r = __builtin_amdgcn_rcpf(1.0f + e);
-  const float s = e * r;
-  a = g >= 0.0f ? r : s;
-  u = g >= 0.0f ? s : r;
-}
+  static __device__ __forceinline__ void pair(float g, float b, float& a, float& u) {
+    float e;
+    if constexpr (sizeof(T) == 4) {
+      constexpr float kLn2 = 0.693147180559945309417f;
+      constexpr float kRest = (float)(1.44269504088896340735992468 - (double)kLog2e);
+      float x = __builtin_elementwise_maximum(g + b, -87.0f);
+      x = __builtin_elementwise_minimum(x, 110.0f);   // e is 0 from 88 on
+      const float t = x * -kLog2e;
+      const float rest = __builtin_fmaf(x, -kRest, __builtin_fmaf(x, -kLog2e, -t));
+      e = __builtin_amdgcn_exp2f(t);
+      e = __builtin_fmaf(e, rest * kLn2, e);
+    } else {
+      e = __builtin_amdgcn_exp2f(
+          __builtin_elementwise_minimum(__builtin_fmaf(g, -kLog2e, b), 125.5f));
+    }
+    a = __builtin_amdgcn_rcpf(1.0f + e);
+    u = e * a;
+  }
+};
 
 }  // namespace logmel

@@ -24,5 +24,5 @@ hipError_t logmel_launch_norm_backward(const logmel_norm_input& in, const logmel
 
 // out[c] = sum over g of part[g * stride + c], c < channels, in a fixed order
 // (logmel_scan.hip).
-hipError_t logmel_launch_part_sum(const float* part, int64_t parts, int64_t stride,
+hipError_t logmel_launch_part_sum(const double* part, int64_t parts, int64_t stride,
                                   int64_t channels, float* out, hipStream_t stream);

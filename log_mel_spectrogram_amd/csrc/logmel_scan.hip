@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "logmel_rows.h"
 #include "logmel_rows_launch.h"
 
@@ -35,7 +37,7 @@ struct ScanGradArgs {
   int64_t dxs;
   T* dg;
   int64_t dgs;
-  float* dbias_part;   // [n_seq][channels]
+  double* dbias_part;   // [work items][channels], or null
   float* dstate;
 };
 
@@ -71,22 +73,34 @@ __global__ void logmel_scan_serial_kernel(ScanArgs<T> p) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       h[v] = p.state ? p.state[j * p.channels + c + v] : 0.0f;
-      b[v] = p.bias ? p.bias[c + v] : 0.0f;
+      b[v] = Gate<T>::bias_of(p.bias ? p.bias[c + v] : 0.0f);
     }
-    for (int64_t t = s; t < e; ++t) {
-      if (p.ck && t % kCk == 0 && t > s) {
+    // rows in batches, a batch read before its first use
+    constexpr int kBatch = 8;
+    for (int64_t t0 = s; t0 < e; t0 += kBatch) {
+      Packed<T, V> x[kBatch], g[kBatch];
 #pragma unroll
-        for (int v = 0; v < V; ++v) p.ck[t / kCk * p.channels + c + v] = h[v];
-      }
-      const auto x = row_load<T, V>(p.x + t * p.xs + c);
-      const auto g = row_load<T, V>(p.g + t * p.gs + c);
+      for (int i = 0; i < kBatch; ++i)
+        if (t0 + i < e) {
+          x[i] = row_load<T, V>(p.x + (t0 + i) * p.xs + c);
+          g[i] = row_load<T, V>(p.g + (t0 + i) * p.gs + c);
+        }
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float a, u;
-        gate_pair<T>((float)g.v[v] + b[v], a, u);
-        h[v] = __builtin_fmaf(a, h[v], u * (float)x.v[v]);
+      for (int i = 0; i < kBatch; ++i) {
+        const int64_t t = t0 + i;
+        if (t >= e) break;
+        if (p.ck && t % kCk == 0 && t > s) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) p.ck[t / kCk * p.channels + c + v] = h[v];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float a, u;
+          Gate<T>::pair((float)g[i].v[v], b[v], a, u);
+          h[v] = __builtin_fmaf(a, h[v], u * (float)x[i].v[v]);
+        }
+        row_store<T, V>(p.h + t * p.hs + c, h);
       }
-      row_store<T, V>(p.h + t * p.hs + c, h);
     }
     if (p.state_out) {
 #pragma unroll
@@ -95,66 +109,836 @@ __global__ void logmel_scan_serial_kernel(ScanArgs<T> p) {
   }
 }
 
-// One wavefront per sequence and 64 channels, a block of kCk rows after the
-// other from the last: the states before each of its rows into LDS, then the
-// rows backwards.
-template <typename T>
-__global__ __launch_bounds__(64) void logmel_scan_backward_serial_kernel(ScanArgs<T> p,
-                                                                         ScanGradArgs<T> q) {
-  __shared__ float prev[kCk][64];
-  const int lane = threadIdx.x;
-  const int64_t slabs = (p.channels + 63) / 64;
-  for (int64_t id = blockIdx.x; id < p.n_seq * slabs; id += gridDim.x) {
-    const int64_t j = id / slabs;
-    const int64_t c = id % slabs * 64 + lane;
-    if (c >= p.channels) continue;
-    int64_t s, e;
-    seq_range(p.off, j, p.rows, s, e);
-    const int64_t at = j * p.channels + c;
-    const float b = p.bias ? p.bias[c] : 0.0f;
-    float carry = q.dstate_out ? q.dstate_out[at] : 0.0f;   // a_{t+1} D_{t+1}
-    float db = 0.0f;
-    for (int64_t k = e > s ? (e - 1) / kCk : -1; k >= 0 && (k + 1) * kCk > s; --k) {
-      const int64_t r0 = k * kCk < s ? s : k * kCk;
-      const int64_t r1 = (k + 1) * kCk < e ? (k + 1) * kCk : e;
-      float h = r0 > s ? p.ck[k * p.channels + c] : (p.state ? p.state[at] : 0.0f);
-      for (int64_t t = r0; t < r1; ++t) {
-        prev[t - r0][lane] = h;
-        float a, u;
-        gate_pair<T>((float)p.g[t * p.gs + c] + b, a, u);
-        h = __builtin_fmaf(a, h, u * (float)p.x[t * p.xs + c]);
-      }
-      for (int64_t t = r1 - 1; t >= r0; --t) {
-        float a, u;
-        gate_pair<T>((float)p.g[t * p.gs + c] + b, a, u);
-        const float d = (float)q.dh[t * q.dhs + c] + carry;
-        const float dg = a * u * (prev[t - r0][lane] - (float)p.x[t * p.xs + c]) * d;
-        q.dx[t * q.dxs + c] = (T)(u * d);
-        q.dg[t * q.dgs + c] = (T)dg;
-        db += dg;
-        carry = a * d;
-      }
+// ---------------------------------------------------------------------------
+// Tiles: a workgroup of 8 wavefronts walks a range of rows, kCk rows at a
+// time, for 64 V channels; wavefront w holds rows 16 w .. 16 w + 15 of a tile,
+// V channels per lane.
+// ---------------------------------------------------------------------------
+
+constexpr int kWaves = 8;
+constexpr int kRun = (int)kCk / kWaves;   // rows per wavefront and tile
+
+// What a run of rows does to the state before it, h -> A h + B, per channel.
+// A < 0 marks a run in which a sequence starts: h -> B, whatever h holds (a
+// product with 0 would let another sequence's NaN through).
+template <int V>
+struct Affine {
+  float a[V], b[V];
+};
+
+constexpr float kCut = -1.0f;
+
+__device__ __forceinline__ float apply(float a, float b, float h) {
+  return a < 0.0f ? b : __builtin_fmaf(a, h, b);
+}
+
+// The sequence a row belongs to: the last j with off[j] <= row, and its rows.
+struct Cursor {
+  int64_t j, s, e;
+};
+
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  return (int64_t)(((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+                   (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
+
+__device__ __forceinline__ void cursor_read(const int64_t* off, int64_t rows, Cursor& k) {
+  int64_t s, e;
+  seq_range(off, k.j, rows, s, e);
+  k.s = uniform64(s);
+  k.e = uniform64(e);
+}
+
+// All 64 lanes look at once; every round leaves at most a 64th of the range.
+__device__ __forceinline__ Cursor cursor_find(const int64_t* off, int64_t n, int64_t rows,
+                                              int64_t row) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int64_t step = (hi - lo + 63) / 64;
+    const int64_t i = lo + lane * step;
+    const int under = __popcll(__ballot(i < hi && off[i] <= row));
+    lo += under ? (under - 1) * step : 0;
+    hi = lo + step < hi ? lo + step : hi;
+  }
+  Cursor k;
+  k.j = uniform64(lo);
+  cursor_read(off, rows, k);
+  return k;
+}
+
+// The rows a work item owns: a whole sequence, or a part of the rows whatever
+// sequences it holds.
+struct Item {
+  int64_t r0, r1;   // r1 <= the end of the last sequence
+  Cursor at;        // the sequence of row r0
+};
+
+// Copies state to state_out for the sequences without rows among the items'
+// share: sequences [64 i, 64 i + 64) for item i, and so on in steps of all.
+template <int V, typename F>
+__device__ __forceinline__ void for_empty(const int64_t* off, int64_t n, int64_t rows,
+                                          int64_t worker, int64_t workers, F&& f) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t j0 = worker * 64; j0 < n; j0 += workers * 64) {
+    bool empty = false;
+    if (j0 + lane < n) {
+      int64_t s, e;
+      seq_range(off, j0 + lane, rows, s, e);
+      empty = s >= e;
     }
-    if (q.dbias_part) q.dbias_part[at] = db;
-    if (q.dstate) q.dstate[at] = carry;
+    for (uint64_t m = __ballot(empty); m; m &= m - 1) f(j0 + (__ffsll((long long)m) - 1));
   }
 }
 
-// 64 channels per workgroup; each of its 4 wavefronts sums every fourth part,
-// and the four sums are added in order.
-__global__ __launch_bounds__(256) void logmel_part_sum_kernel(const float* part, int64_t parts,
-                                                              int64_t stride, int64_t channels,
-                                                              float* out) {
-  __shared__ float sums[4][64];
+template <typename T, int V>
+__device__ __forceinline__ void load_run(Packed<T, V> (&r)[kRun], const T* base, int64_t stride,
+                                         uint32_t c, int64_t w0, int64_t lo, int64_t hi) {
+  const T* p = base + w0 * stride;
+  if (lo <= w0 && w0 + kRun <= hi) {
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) r[i] = row_load<T, V>(p + i * stride + c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      r[i] = Packed<T, V>{};
+      if (w0 + i >= lo && w0 + i < hi) r[i] = row_load<T, V>(p + i * stride + c);
+    }
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void load_floats(float (&r)[V], const float* p, int64_t row,
+                                            int64_t channels, uint32_t c) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) r[v] = p ? p[row * channels + c + v] : 0.0f;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void load_bias(float (&r)[V], const float* bias, int64_t c0,
+                                          uint32_t c) {
+  load_floats<V>(r, bias ? bias + c0 : nullptr, 0, 0, c);
+#pragma unroll
+  for (int v = 0; v < V; ++v) r[v] = Gate<T>::bias_of(r[v]);
+}
+
+template <int V>
+__device__ __forceinline__ void store_floats(float* p, int64_t row, int64_t channels, uint32_t c,
+                                             const float (&r)[V]) {
+#pragma unroll
+  for (int v = 0; v < V; ++v) p[row * channels + c + v] = r[v];
+}
+
+// The workgroup's channels: a uniform first one, and each lane's offset from
+// it. The last lanes of a ragged slab hold the row's last V channels again
+// and write the same values.
+template <int V>
+__device__ __forceinline__ uint32_t lane_offset(int64_t slab, int64_t channels, int64_t& base) {
+  base = slab * 64 * V;
+  if (base + V > channels) base = channels - V;
+  const int64_t most = channels - V - base;
+  const int64_t c = (threadIdx.x & 63) * V;
+  return (uint32_t)(c < most ? c : most);
+}
+
+struct PartArgs {
+  int64_t part_rows;   // a multiple of kCk
+  int64_t parts;
+  float* a;            // [parts][channels]: the part's Affine out of its first or last row
+  float* b;
+  float* state;        // [parts][channels]: the initial state of the sequence that leaves the part
+};
+
+// Rows of part k that belong to a sequence.
+template <typename T>
+__device__ __forceinline__ void part_range(const ScanArgs<T>& p, const PartArgs& q, int64_t k,
+                                           int64_t& r0, int64_t& r1) {
+  const int64_t last = p.off[p.n_seq];
+  const int64_t end = uniform64(last < p.rows ? last : p.rows);
+  r0 = k * q.part_rows;
+  r1 = r0 + q.part_rows < end ? r0 + q.part_rows : end;
+}
+
+// Folds the Affine of `count` runs, the i-th at f(i), onto nothing: the
+// composition of all of them in order.
+template <int V, typename F>
+__device__ __forceinline__ Affine<V> compose(int64_t count, F&& f) {
+  Affine<V> r;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    r.a[v] = 1.0f;
+    r.b[v] = 0.0f;
+  }
+#pragma unroll 4
+  for (int64_t i = 0; i < count; ++i) {
+    const Affine<V> n = f(i);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      r.b[v] = apply(n.a[v], n.b[v], r.b[v]);
+      r.a[v] = n.a[v] < 0.0f ? kCut : n.a[v] * r.a[v];
+    }
+  }
+  return r;
+}
+
+template <int V>
+struct WaveTotals {
+  Affine<V> t[kWaves][64];
+};
+
+// The composition over the workgroup of what each wavefront holds for its
+// share of `count` runs (wavefront w: runs [w per, (w + 1) per)).
+template <int V, typename F>
+__device__ __forceinline__ Affine<V> compose_by_waves(WaveTotals<V>& lds, int64_t count, F&& f) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t per = (count + kWaves - 1) / kWaves;
+  const int64_t i0 = wave * per < count ? wave * per : count;
+  const int64_t i1 = i0 + per < count ? i0 + per : count;
+  lds.t[wave][lane] = compose<V>(i1 - i0, [&](int64_t i) { return f(i0 + i); });
+  __syncthreads();
+  return compose<V>(kWaves, [&](int64_t w) { return lds.t[w][lane]; });
+}
+
+// Before the tiles of parts: what each part does to the state of a sequence
+// that runs on past its end. Only the rows of that sequence count, so a part
+// whose last row ends a sequence has nothing to do.
+template <typename T, int V>
+__global__ __launch_bounds__(512) void logmel_scan_parts_kernel(ScanArgs<T> p, PartArgs q) {
+  __shared__ WaveTotals<V> lds;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
+  const int64_t k = q.parts - 1 - blockIdx.x / slabs;
+  int64_t c0;
+  const uint32_t c = lane_offset<V>(blockIdx.x % slabs, p.channels, c0);
+  int64_t r0, r1;
+  part_range(p, q, k, r0, r1);
+  if (r1 <= r0) return;
+  const Cursor at = cursor_find(p.off, p.n_seq, p.rows, r1 - 1);
+  if (at.e <= r1) return;
+  const bool starts = at.s >= r0;
+  const int64_t lo = starts ? at.s : r0;
+  const int64_t per = ((r1 - lo + kWaves - 1) / kWaves + kRun - 1) / kRun * kRun;
+  const int64_t w0 = lo + wave * per, w1 = w0 + per < r1 ? w0 + per : r1;
+  float bias[V], h0[V];
+  load_bias<T, V>(bias, p.bias, c0, c);
+  if (starts) load_floats<V>(h0, p.state ? p.state + c0 : nullptr, at.j, p.channels, c);
+  float A[V], B[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    A[v] = 1.0f;
+    B[v] = 0.0f;
+    if (starts && wave == 0) B[v] = h0[v];
+  }
+  Packed<T, V> x[kRun], g[kRun];
+  if (w0 < w1) {
+    load_run<T, V>(x, p.x + c0, p.xs, c, w0, w0, w1);
+    load_run<T, V>(g, p.g + c0, p.gs, c, w0, w0, w1);
+  }
+  for (int64_t t = w0; t < w1; t += kRun) {
+    float a[kRun][V], b[kRun][V];
+    const bool whole = t + kRun <= w1;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float u;
+        Gate<T>::pair((float)g[i].v[v], bias[v], a[i][v], u);
+        b[i][v] = u * (float)x[i].v[v];
+      }
+    if (t + kRun < w1) {
+      load_run<T, V>(x, p.x + c0, p.xs, c, t + kRun, w0, w1);
+      load_run<T, V>(g, p.g + c0, p.gs, c, t + kRun, w0, w1);
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      if (!whole && t + i >= w1) break;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        B[v] = __builtin_fmaf(a[i][v], B[v], b[i][v]);
+        A[v] *= a[i][v];
+      }
+    }
+  }
+  Affine<V> mine;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    mine.a[v] = starts && wave == 0 ? kCut : A[v];
+    mine.b[v] = B[v];
+  }
+  lds.t[wave][threadIdx.x & 63] = mine;
+  __syncthreads();
+  if (wave == 0) {
+    const Affine<V> all =
+        compose<V>(kWaves, [&](int64_t w) { return lds.t[w][threadIdx.x & 63]; });
+    store_floats<V>(q.a + c0, k, p.channels, c, all.a);
+    store_floats<V>(q.b + c0, k, p.channels, c, all.b);
+    if (starts) store_floats<V>(q.state + c0, k, p.channels, c, h0);
+  }
+}
+
+// The tiles. kParts: a work item is a part of the rows, entered with the state
+// the parts before it leave (q.a null: there is one part); otherwise it is one
+// sequence. Each tile is read once, ahead of its use: its local recurrence
+// from zero (H) and the product of its gates (P) stay in registers while the
+// wavefronts exchange their runs' Affine through LDS, then h = P carry + H.
+template <typename T, int V, bool kParts, bool kEarly>
+__global__ __launch_bounds__(512, kEarly && V == 2 ? 2 : 4) void logmel_scan_tiles_kernel(ScanArgs<T> p, PartArgs q) {
+  __shared__ WaveTotals<V> lds[2];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
+  const int64_t item = blockIdx.x / slabs;
+  int64_t c0;
+  const uint32_t c = lane_offset<V>(blockIdx.x % slabs, p.channels, c0);
+  const float* state = p.state ? p.state + c0 : nullptr;
+  float bias[V], carry[V];
+  load_bias<T, V>(bias, p.bias, c0, c);
+#pragma unroll
+  for (int v = 0; v < V; ++v) carry[v] = 0.0f;
+  int64_t r0, r1;
+  Cursor at;
+  Cursor out;   // the sequence that runs on past r1, where a part's last one does
+  out.j = -1;
+  if constexpr (kParts) {
+    if (wave == 0 && p.state_out)
+      for_empty<V>(p.off, p.n_seq, p.rows, item, q.parts, [&](int64_t j) {
+        float h[V];
+        load_floats<V>(h, state, j, p.channels, c);
+        store_floats<V>(p.state_out + c0, j, p.channels, c, h);
+      });
+    part_range(p, q, item, r0, r1);
+    if (r1 <= r0) return;
+    at = cursor_find(p.off, p.n_seq, p.rows, r0);
+    if (q.a) {
+      const Cursor end = cursor_find(p.off, p.n_seq, p.rows, r1 - 1);
+      if (end.e > r1) out = end;
+      if (at.s < r0) {
+        const int64_t k0 = at.s / q.part_rows;
+        const Affine<V> in = compose_by_waves<V>(lds[1], item - k0, [&](int64_t i) {
+          Affine<V> n;
+          load_floats<V>(n.a, q.a + c0, k0 + i, p.channels, c);
+          load_floats<V>(n.b, q.b + c0, k0 + i, p.channels, c);
+          return n;
+        });
+#pragma unroll
+        for (int v = 0; v < V; ++v) carry[v] = in.b[v];
+      }
+    }
+  } else {
+    at.j = item;
+    cursor_read(p.off, p.rows, at);
+    r0 = at.s;
+    r1 = at.e;
+    if (r0 >= r1) {
+      if (wave == 0 && p.state_out) {
+        load_floats<V>(carry, state, item, p.channels, c);
+        store_floats<V>(p.state_out + c0, item, p.channels, c, carry);
+      }
+      return;
+    }
+  }
+  int64_t tile = r0 / kCk * kCk;
+  struct Raw {
+    Packed<T, V> x[kRun], g[kRun];
+  };
+  auto load = [&](Raw& raw, int64_t first) {
+    load_run<T, V>(raw.x, p.x + c0, p.xs, c, first + wave * kRun, r0, r1);
+    load_run<T, V>(raw.g, p.g + c0, p.gs, c, first + wave * kRun, r0, r1);
+  };
+  auto one_tile = [&](Raw& raw, Raw& ahead, int buf) {
+    auto& x = raw.x;
+    auto& g = raw.g;
+    const int64_t next = tile + kCk;
+    if (kEarly && next < r1) load(ahead, next);
+    const int64_t w0 = tile + wave * kRun;
+    if (p.ck && wave == 0 && (tile > r0 || (kParts && at.s < r0)))
+      store_floats<V>(p.ck + c0, tile / kCk, p.channels, c, carry);
+    // the wavefront's rows that belong to a sequence here
+    const int64_t lo = w0 < r0 ? r0 : w0, hi = w0 + kRun < r1 ? w0 + kRun : r1;
+    if (kParts && lo < hi && lo >= at.e) at = cursor_find(p.off, p.n_seq, p.rows, lo);
+    const Cursor first = at;
+    const bool plain = w0 > at.s && w0 + kRun < at.e && w0 >= r0 && w0 + kRun <= r1;
+    float P[kRun][V], H[kRun][V];
+    float A[V], B[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      A[v] = 1.0f;
+      B[v] = 0.0f;
+    }
+    auto step = [&](int i, auto may_cut) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float a, u;
+        Gate<T>::pair((float)g[i].v[v], bias[v], a, u);
+        B[v] = __builtin_fmaf(a, B[v], u * (float)x[i].v[v]);
+        A[v] = may_cut && A[v] < 0.0f ? A[v] : A[v] * a;
+        P[i][v] = A[v];
+        H[i][v] = B[v];
+      }
+    };
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) step(i, std::false_type{});
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const int64_t t = w0 + i;
+        if (t >= lo && t < hi) {
+          if (kParts)
+            while (t >= at.e && at.j + 1 < p.n_seq) {
+              ++at.j;
+              cursor_read(p.off, p.rows, at);
+            }
+          if (t == at.s) {
+            float h0[V];
+            if (at.j == out.j)
+              load_floats<V>(h0, q.state + c0, item, p.channels, c);
+            else
+              load_floats<V>(h0, state, at.j, p.channels, c);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              A[v] = kCut;
+              B[v] = h0[v];
+            }
+          }
+          step(i, std::true_type{});
+        }
+      }
+    }
+    Affine<V> mine;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      mine.a[v] = A[v];
+      mine.b[v] = B[v];
+    }
+    lds[buf].t[wave][lane] = mine;
+    if (!kEarly && next < r1) load(raw, next);
+    __syncthreads();
+    float in[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) in[v] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      if (w == wave) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) in[v] = carry[v];
+      }
+      const Affine<V> n = lds[buf].t[w][lane];
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = apply(n.a[v], n.b[v], carry[v]);
+    }
+    T* out_p = p.h + c0 + w0 * p.hs;
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        float h[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(P[i][v], in[v], H[i][v]);
+        row_store<T, V>(out_p + i * p.hs + c, h);
+      }
+    } else {
+      Cursor k = first;
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const int64_t t = w0 + i;
+        if (t >= lo && t < hi) {
+          if (kParts)
+            while (t >= k.e && k.j + 1 < p.n_seq) {
+              ++k.j;
+              cursor_read(p.off, p.rows, k);
+            }
+          float h[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v) h[v] = apply(P[i][v], H[i][v], in[v]);
+          row_store<T, V>(out_p + i * p.hs + c, h);
+          if (t + 1 == k.e && p.state_out)
+            store_floats<V>(p.state_out + c0, k.j, p.channels, c, h);
+        }
+      }
+    }
+    tile = next;
+  };
+  Raw even, odd;
+  load(even, tile);
+  for (;;) {
+    one_tile(even, odd, 0);
+    if (tile >= r1) break;
+    if constexpr (kEarly)
+      one_tile(odd, even, 1);
+    else
+      one_tile(even, even, 1);
+    if (tile >= r1) break;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The gradient. With E_t = a_t D_t, what row t hands to the row before it,
+//   D_t = dh_t + E_{t+1},  E_t = a_t (dh_t + E_{t+1}),
+// an affine recurrence over the rows backwards, which ends at a sequence's
+// last row (E after it is dstate_out). h_{t-1} is formed anew from the
+// checkpoint before the tile, by the same recurrence as in the forward call:
+// reading the rounded h instead would cost as many bytes as reading x does,
+// and lose the digits that h_{t-1} - x cancels.
+// ---------------------------------------------------------------------------
+
+// Before the tiles of parts: what each part does to the E of a sequence that
+// entered the part before its first row.
+template <typename T, int V>
+__global__ __launch_bounds__(512) void logmel_scan_back_parts_kernel(ScanArgs<T> p,
+                                                                     ScanGradArgs<T> d,
+                                                                     PartArgs q) {
+  __shared__ WaveTotals<V> lds;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
+  const int64_t k = blockIdx.x / slabs;
+  int64_t c0;
+  const uint32_t c = lane_offset<V>(blockIdx.x % slabs, p.channels, c0);
+  int64_t r0, r1;
+  part_range(p, q, k, r0, r1);
+  if (r1 <= r0) return;
+  const Cursor at = cursor_find(p.off, p.n_seq, p.rows, r0);
+  if (at.s >= r0) return;
+  const bool ends = at.e <= r1;
+  const int64_t hi = ends ? at.e : r1;
+  const int64_t per = ((hi - r0 + kWaves - 1) / kWaves + kRun - 1) / kRun * kRun;
+  const int64_t w0 = r0 + wave * per, w1 = w0 + per < hi ? w0 + per : hi;
+  const bool last = ends && w0 < hi && w1 == hi;   // the wavefront with the sequence's last row
+  float bias[V];
+  load_bias<T, V>(bias, p.bias, c0, c);
+  Affine<V> mine;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    mine.a[v] = 1.0f;
+    mine.b[v] = 0.0f;
+  }
+  if (last)
+    load_floats<V>(mine.b, d.dstate_out ? d.dstate_out + c0 : nullptr, at.j, p.channels, c);
+  // rows from the wavefront's last run down
+  Packed<T, V> dh[kRun], g[kRun];
+  int64_t t = w0 < w1 ? w0 + (w1 - 1 - w0) / kRun * kRun : w0 - kRun;
+  if (t >= w0) {
+    load_run<T, V>(dh, d.dh + c0, d.dhs, c, t, w0, w1);
+    load_run<T, V>(g, p.g + c0, p.gs, c, t, w0, w1);
+  }
+  for (; t >= w0; t -= kRun) {
+    float a[kRun][V], b[kRun][V];
+    const bool whole = t + kRun <= w1;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float u;
+        Gate<T>::pair((float)g[i].v[v], bias[v], a[i][v], u);
+        b[i][v] = (float)dh[i].v[v];
+      }
+    if (t - kRun >= w0) {
+      load_run<T, V>(dh, d.dh + c0, d.dhs, c, t - kRun, w0, w1);
+      load_run<T, V>(g, p.g + c0, p.gs, c, t - kRun, w0, w1);
+    }
+#pragma unroll
+    for (int i = kRun - 1; i >= 0; --i) {
+      if (whole || t + i < w1) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          mine.b[v] = a[i][v] * (b[i][v] + mine.b[v]);
+          mine.a[v] *= a[i][v];
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) mine.a[v] = last ? kCut : mine.a[v];
+  lds.t[wave][lane] = mine;
+  __syncthreads();
+  if (wave == 0) {
+    const Affine<V> all = compose<V>(kWaves, [&](int64_t w) { return lds.t[kWaves - 1 - w][lane]; });
+    store_floats<V>(q.a + c0, k, p.channels, c, all.a);
+    store_floats<V>(q.b + c0, k, p.channels, c, all.b);
+  }
+}
+
+// The tiles, from a work item's last to its first.
+template <typename T, int V, bool kParts>
+__global__ __launch_bounds__(512, 2) void logmel_scan_back_tiles_kernel(ScanArgs<T> p,
+                                                                        ScanGradArgs<T> d,
+                                                                        PartArgs q) {
+  __shared__ WaveTotals<V> fwd[2], rev[2];
+  __shared__ double sums[kWaves][64][V];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
+  const int64_t item = blockIdx.x / slabs;
+  int64_t c0;
+  const uint32_t c = lane_offset<V>(blockIdx.x % slabs, p.channels, c0);
+  const float* state = p.state ? p.state + c0 : nullptr;
+  const float* dstate_out = d.dstate_out ? d.dstate_out + c0 : nullptr;
+  float* dstate = d.dstate ? d.dstate + c0 : nullptr;
+  float bias[V], carry[V];
+  double db[V];
+  load_bias<T, V>(bias, p.bias, c0, c);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    carry[v] = 0.0f;
+    db[v] = 0.0;
+  }
+  int64_t r0, r1;
+  Cursor at;
+  if constexpr (kParts) {
+    if (wave == 0 && dstate)
+      for_empty<V>(p.off, p.n_seq, p.rows, item, q.parts, [&](int64_t j) {
+        float e[V];
+        load_floats<V>(e, dstate_out, j, p.channels, c);
+        store_floats<V>(dstate, j, p.channels, c, e);
+      });
+    part_range(p, q, item, r0, r1);
+    if (r0 < r1) {
+      at = cursor_find(p.off, p.n_seq, p.rows, r1 - 1);
+      if (q.a && at.e > r1) {
+        const int64_t k1 = (at.e - 1) / q.part_rows;
+        const Affine<V> in = compose_by_waves<V>(fwd[1], k1 - item, [&](int64_t i) {
+          Affine<V> n;
+          load_floats<V>(n.a, q.a + c0, k1 - i, p.channels, c);
+          load_floats<V>(n.b, q.b + c0, k1 - i, p.channels, c);
+          return n;
+        });
+#pragma unroll
+        for (int v = 0; v < V; ++v) carry[v] = in.b[v];
+      }
+    }
+  } else {
+    at.j = item;
+    cursor_read(p.off, p.rows, at);
+    r0 = at.s;
+    r1 = at.e;
+    if (r0 >= r1 && wave == 0 && dstate) {
+      load_floats<V>(carry, dstate_out, item, p.channels, c);
+      store_floats<V>(dstate, item, p.channels, c, carry);
+    }
+  }
+  struct Raw {
+    Packed<T, V> x[kRun], g[kRun], dh[kRun];
+    float ck[V];
+  };
+  auto load = [&](Raw& raw, int64_t first) {
+    const int64_t w0 = first + wave * kRun;
+    load_floats<V>(raw.ck, p.ck + c0, first / kCk, p.channels, c);
+    load_run<T, V>(raw.x, p.x + c0, p.xs, c, w0, r0, r1);
+    load_run<T, V>(raw.g, p.g + c0, p.gs, c, w0, r0, r1);
+    load_run<T, V>(raw.dh, d.dh + c0, d.dhs, c, w0, r0, r1);
+  };
+  int64_t tile = (r1 - 1) / kCk * kCk;
+  auto one_tile = [&](Raw& raw, int buf) {
+    const int64_t w0 = tile + wave * kRun;
+    const int64_t next = tile - kCk;
+    const bool more = next + kCk > r0;
+    const int64_t lo = w0 < r0 ? r0 : w0, hi = w0 + kRun < r1 ? w0 + kRun : r1;
+    if (kParts && lo < hi && (lo < at.s || lo >= at.e))
+      at = cursor_find(p.off, p.n_seq, p.rows, lo);
+    const bool plain = w0 > at.s && w0 + kRun < at.e && w0 >= r0 && w0 + kRun <= r1;
+    float a[kRun][V], u[kRun][V];
+    Affine<V> f, e;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      f.a[v] = e.a[v] = 1.0f;
+      f.b[v] = e.b[v] = 0.0f;
+    }
+    auto onward = [&](Cursor& k, int64_t t) {
+      if (kParts)
+        while (t >= k.e && k.j + 1 < p.n_seq) {
+          ++k.j;
+          cursor_read(p.off, p.rows, k);
+        }
+    };
+    auto backward = [&](Cursor& k, int64_t t) {
+      if (kParts)
+        while (t < k.s && k.j > 0) {
+          --k.j;
+          cursor_read(p.off, p.rows, k);
+        }
+    };
+    Cursor k = at;
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          Gate<T>::pair((float)raw.g[i].v[v], bias[v], a[i][v], u[i][v]);
+          f.b[v] = __builtin_fmaf(a[i][v], f.b[v], u[i][v] * (float)raw.x[i].v[v]);
+          f.a[v] *= a[i][v];
+        }
+      // the product of the gates is the same both ways
+#pragma unroll
+      for (int v = 0; v < V; ++v) e.a[v] = f.a[v];
+#pragma unroll
+      for (int i = kRun - 1; i >= 0; --i)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          e.b[v] = a[i][v] * ((float)raw.dh[i].v[v] + e.b[v]);
+    } else {
+      // rows that are not the item's change nothing: a = 1, u = 0
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const int64_t t = w0 + i;
+        const bool in = t >= lo && t < hi;
+        if (in) {
+          onward(k, t);
+          if (t == k.s) {
+            load_floats<V>(f.b, state, k.j, p.channels, c);
+#pragma unroll
+            for (int v = 0; v < V; ++v) f.a[v] = kCut;
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          Gate<T>::pair((float)raw.g[i].v[v], bias[v], a[i][v], u[i][v]);
+          a[i][v] = in ? a[i][v] : 1.0f;
+          u[i][v] = in ? u[i][v] : 0.0f;
+          f.b[v] = __builtin_fmaf(a[i][v], f.b[v], u[i][v] * (float)raw.x[i].v[v]);
+          f.a[v] = f.a[v] < 0.0f ? f.a[v] : f.a[v] * a[i][v];
+        }
+      }
+#pragma unroll
+      for (int i = kRun - 1; i >= 0; --i) {
+        const int64_t t = w0 + i;
+        if (t >= lo && t < hi) {
+          backward(k, t);
+          if (t + 1 == k.e) {
+            load_floats<V>(e.b, dstate_out, k.j, p.channels, c);
+#pragma unroll
+            for (int v = 0; v < V; ++v) e.a[v] = kCut;
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          e.b[v] = a[i][v] * ((float)raw.dh[i].v[v] + e.b[v]);
+          e.a[v] = e.a[v] < 0.0f ? e.a[v] : e.a[v] * a[i][v];
+        }
+      }
+    }
+    fwd[buf].t[wave][lane] = f;
+    rev[buf].t[wave][lane] = e;
+    __syncthreads();
+    float h[V], E[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      h[v] = raw.ck[v];
+      E[v] = 0.0f;
+    }
+#pragma unroll
+    for (int w = 0; w < kWaves - 1; ++w)
+      if (w < wave) {
+        const Affine<V> n = fwd[buf].t[w][lane];
+#pragma unroll
+        for (int v = 0; v < V; ++v) h[v] = apply(n.a[v], n.b[v], h[v]);
+      }
+#pragma unroll
+    for (int w = kWaves - 1; w >= 0; --w) {
+      if (w == wave) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) E[v] = carry[v];
+      }
+      const Affine<V> n = rev[buf].t[w][lane];
+#pragma unroll
+      for (int v = 0; v < V; ++v) carry[v] = apply(n.a[v], n.b[v], carry[v]);
+    }
+    float prev[kRun][V], part[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) part[v] = 0.0f;
+    T* dx_p = d.dx + c0 + w0 * d.dxs;
+    T* dg_p = d.dg + c0 + w0 * d.dgs;
+    auto forward_row = [&](int i) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float x = (float)raw.x[i].v[v];
+        prev[i][v] = h[v] - x;
+        h[v] = __builtin_fmaf(a[i][v], h[v], u[i][v] * x);
+      }
+    };
+    auto backward_row = [&](int i) {
+      float dx[V], dg[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float D = (float)raw.dh[i].v[v] + E[v];
+        E[v] = a[i][v] * D;
+        dx[v] = u[i][v] * D;
+        dg[v] = prev[i][v] * (u[i][v] * E[v]);
+        part[v] += dg[v];
+      }
+      row_store<T, V>(dx_p + i * d.dxs + c, dx);
+      row_store<T, V>(dg_p + i * d.dgs + c, dg);
+    };
+    if (plain) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) forward_row(i);
+#pragma unroll
+      for (int i = kRun - 1; i >= 0; --i) backward_row(i);
+    } else {
+      k = at;
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const int64_t t = w0 + i;
+        if (t >= lo && t < hi) {
+          onward(k, t);
+          if (t == k.s) load_floats<V>(h, state, k.j, p.channels, c);
+          forward_row(i);
+        }
+      }
+#pragma unroll
+      for (int i = kRun - 1; i >= 0; --i) {
+        const int64_t t = w0 + i;
+        if (t >= lo && t < hi) {
+          backward(k, t);
+          if (t + 1 == k.e) load_floats<V>(E, dstate_out, k.j, p.channels, c);
+          backward_row(i);
+          if (t == k.s && dstate) store_floats<V>(dstate, k.j, p.channels, c, E);
+        }
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) db[v] += (double)part[v];
+    if (more) load(raw, next);
+    tile = next;
+  };
+  if (r0 < r1) {
+    Raw raw;
+    load(raw, tile);
+    for (int buf = 0; tile + kCk > r0; buf ^= 1) one_tile(raw, buf);
+  }
+  if (!d.dbias_part) return;
+#pragma unroll
+  for (int v = 0; v < V; ++v) sums[wave][lane][v] = db[v];
+  __syncthreads();
+  if (wave == 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      double s = 0.0;
+      for (int w = 0; w < kWaves; ++w) s += sums[w][lane][v];
+      d.dbias_part[item * p.channels + c0 + c + v] = s;
+    }
+  }
+}
+
+// Sums over work items: 64 channels per workgroup; each of its 16 wavefronts
+// takes every sixteenth part, and the sixteen sums are added in order.
+__global__ __launch_bounds__(1024) void logmel_part_sum_kernel(const double* part, int64_t parts,
+                                                               int64_t stride, int64_t channels,
+                                                               float* out) {
+  __shared__ double sums[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-  float s = 0.0f;
-  if (c < channels)
-    for (int64_t g = wave; g < parts; g += 4) s += part[g * stride + c];
+  double s = 0.0;
+  if (c < channels) {
+#pragma unroll 8
+    for (int64_t g = wave; g < parts; g += 16) s += part[g * stride + c];
+  }
   sums[wave][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < channels)
-    out[c] = sums[0][lane] + sums[1][lane] + sums[2][lane] + sums[3][lane];
+  if (wave == 0 && c < channels) {
+    double t = sums[0][lane];
+    for (int w = 1; w < 16; ++w) t += sums[w][lane];
+    out[c] = (float)t;
+  }
 }
 
 template <typename T>
@@ -178,57 +962,182 @@ unsigned grid_of(int64_t blocks) {
   return (unsigned)(blocks < 1 ? 1 : blocks > kMost ? kMost : blocks);
 }
 
+int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
+
+// How a call's rows are split over workgroups.
+struct Split {
+  enum How { kSerial, kSequences, kParts } how;
+  int pairs;          // channels per lane
+  int64_t slabs;      // of 64 pairs channels
+  int64_t part_rows, parts;
+};
+
+// Which way is the fastest follows from three figures, in us on this card:
+// the rate of a call that reads and writes each value once (4.6 TB/s over the
+// bytes, 3 per value and byte of its type), the time one workgroup takes for a
+// tile (3, its wavefronts' instructions), and a launch (6). Measured, the way
+// taken first: 512 sequences of 32 rows x 512 bf16 in one lane each 16 us,
+// tiles 22 (of 64 rows 48 and 35, so lanes up to 32 rows); 64 x 2998 x 512
+// bf16 by sequences 128 us, in parts 183; 64 x 2998 x 128 in parts 64 us, by
+// sequences 75; 8 x 2998 x 512 in parts 37, by sequences 61; 16 x 375 x 512
+// fp32 by sequences 20, in parts 25.
+// Two channels per lane halve the memory instructions, with one tile more in
+// flight than fits 128 registers (64 x 2998 x 512 bf16 128 against 140 us,
+// fp32 231 against 250), but need workgroups for most compute units: with 64
+// of them (128 channels) one channel per lane takes 75 us, two 99. In parts,
+// whose first kernel only reads, one channel per lane is the faster (183
+// against 210 us).
+// The gradient reads three values and writes two where the call reads two and
+// writes one, and its first kernel reads two of them as well.
+Split scan_split(const logmel_scan_input& in, int cus, bool backward) {
+  Split s{};
+  const int64_t longest = in.max_frames ? in.max_frames : in.rows;
+  const int64_t rows = in.rows < 1 ? 1 : in.rows;
+  if (longest <= 32 && !backward) {
+    s.how = Split::kSerial;
+    s.pairs = in.channels > 1 ? 2 : 1;
+    return s;
+  }
+  const int64_t pair_slabs = ceil_div(in.channels, 128);
+  s.pairs = in.channels > 1 && in.n_seq >= ceil_div(3 * cus, 4 * pair_slabs) ? 2 : 1;
+  s.slabs = ceil_div(in.channels, 64 * s.pairs);
+  const double size = in.type == LOGMEL_F32 ? 4.0 : 2.0;
+  const double units = backward ? 5.0 : 3.0;
+  const double once = units * size * (double)rows * (double)in.channels / 4.6e6;
+  const double alone = units * (double)ceil_div(longest, kCk);
+  const int64_t part_slabs = ceil_div(in.channels, 64);
+  const int64_t part_rows = ceil_div(ceil_div(rows, kCk), ceil_div(2 * cus, part_slabs)) * kCk;
+  const int64_t parts = ceil_div(rows, part_rows);
+  // the first kernel reads the part of a sequence that runs on past a part
+  const double mean = (double)rows / (double)(in.n_seq < 1 ? 1 : in.n_seq);
+  const double again = mean >= 2.0 * part_rows ? 1.0 : mean / (2.0 * part_rows);
+  const double in_parts = once * (1.0 + again * 2.0 / units) + (parts > 1 ? 6.0 : 0.0);
+  if (in_parts >= (once > alone ? once : alone) && in.n_seq <= (int64_t(1) << 30) / s.slabs) {
+    s.how = Split::kSequences;
+    return s;
+  }
+  s.how = Split::kParts;
+  s.pairs = 1;
+  s.slabs = part_slabs;
+  s.part_rows = part_rows;
+  s.parts = parts;
+  return s;
+}
+
+template <typename T, int V>
+void launch_scan_serial(const ScanArgs<T>& p, hipStream_t stream) {
+  const int64_t lanes = p.n_seq * ceil_div(p.channels, V);
+  logmel_scan_serial_kernel<T, V><<<grid_of(ceil_div(lanes, 256)), 256, 0, stream>>>(p);
+}
+
 template <typename T>
 hipError_t launch_scan(const logmel_scan_input& in, void* h, int64_t h_stride, float* state_out,
-                       float* checkpoints, void*, int, hipStream_t stream) {
+                       float* checkpoints, void* ws, int cus, hipStream_t stream) {
   ScanArgs<T> p = scan_args<T>(in);
   p.h = static_cast<T*>(h);
   p.hs = h_stride;
   p.state_out = state_out;
   p.ck = checkpoints;
-  const int64_t lanes = in.n_seq * ((in.channels + 1) / 2);
-  if (in.channels == 1)
-    logmel_scan_serial_kernel<T, 1><<<grid_of((in.n_seq + 255) / 256), 256, 0, stream>>>(p);
-  else
-    logmel_scan_serial_kernel<T, 2><<<grid_of((lanes + 255) / 256), 256, 0, stream>>>(p);
+  const Split s = scan_split(in, cus, false);
+  PartArgs q{};
+  if (s.how == Split::kSerial) {
+    if (s.pairs == 2)
+      launch_scan_serial<T, 2>(p, stream);
+    else
+      launch_scan_serial<T, 1>(p, stream);
+  } else if (s.how == Split::kSequences) {
+    const unsigned grid = (unsigned)(in.n_seq * s.slabs);
+    if (s.pairs == 2)
+      logmel_scan_tiles_kernel<T, 2, false, true><<<grid, 512, 0, stream>>>(p, q);
+    else
+      logmel_scan_tiles_kernel<T, 1, false, false><<<grid, 512, 0, stream>>>(p, q);
+  } else {
+    const unsigned grid = (unsigned)(s.parts * s.slabs);
+    q.part_rows = s.part_rows;
+    q.parts = s.parts;
+    if (s.parts > 1) {
+      q.a = static_cast<float*>(ws);
+      q.b = q.a + s.parts * in.channels;
+      q.state = q.b + s.parts * in.channels;
+      logmel_scan_parts_kernel<T, 1><<<grid, 512, 0, stream>>>(p, q);
+    }
+    logmel_scan_tiles_kernel<T, 1, true, false><<<grid, 512, 0, stream>>>(p, q);
+  }
   return hipGetLastError();
+}
+
+// Where a gradient's workspace holds what, in bytes from its start: the sums
+// of dgate (doubles, first), then the parts' Affine.
+struct BackSpace {
+  int64_t items, sums, affine, bytes;
+};
+
+BackSpace back_space(const logmel_scan_input& in, const Split& s) {
+  BackSpace b;
+  b.items = s.how == Split::kParts ? s.parts : in.n_seq;
+  b.sums = in.d_bias ? b.items * in.channels * 8 : 0;
+  b.affine = s.how == Split::kParts && s.parts > 1 ? 2 * s.parts * in.channels * 4 : 0;
+  b.bytes = b.sums + b.affine;
+  return b;
 }
 
 template <typename T>
 hipError_t launch_scan_backward(const logmel_scan_input& in, const float* checkpoints,
-                                const logmel_scan_grad& grad, void* ws, int,
+                                const logmel_scan_grad& grad, void* ws, int cus,
                                 hipStream_t stream) {
   ScanArgs<T> p = scan_args<T>(in);
   p.ck = const_cast<float*>(checkpoints);
-  ScanGradArgs<T> q{};
-  q.dh = static_cast<const T*>(grad.d_dh);
-  q.dhs = grad.dh_stride;
-  q.dstate_out = grad.d_dstate_out;
-  q.dx = static_cast<T*>(grad.d_dx);
-  q.dxs = grad.dx_stride;
-  q.dg = static_cast<T*>(grad.d_dgate);
-  q.dgs = grad.dgate_stride;
-  q.dbias_part = grad.d_dbias ? static_cast<float*>(ws) : nullptr;
-  q.dstate = grad.d_dstate;
-  logmel_scan_backward_serial_kernel<T>
-      <<<grid_of(in.n_seq * ((in.channels + 63) / 64)), 64, 0, stream>>>(p, q);
+  const Split s = scan_split(in, cus, true);
+  const BackSpace b = back_space(in, s);
+  if (in.n_seq == 0)   // no offsets to read; the sum over no rows
+    return logmel_launch_part_sum(nullptr, 0, 0, in.channels, grad.d_dbias, stream);
+  ScanGradArgs<T> d{};
+  d.dh = static_cast<const T*>(grad.d_dh);
+  d.dhs = grad.dh_stride;
+  d.dstate_out = grad.d_dstate_out;
+  d.dx = static_cast<T*>(grad.d_dx);
+  d.dxs = grad.dx_stride;
+  d.dg = static_cast<T*>(grad.d_dgate);
+  d.dgs = grad.dgate_stride;
+  d.dbias_part = grad.d_dbias ? static_cast<double*>(ws) : nullptr;
+  d.dstate = grad.d_dstate;
+  PartArgs q{};
+  if (s.how == Split::kSequences) {
+    const unsigned grid = (unsigned)(in.n_seq * s.slabs);
+    if (s.pairs == 2)
+      logmel_scan_back_tiles_kernel<T, 2, false><<<grid, 512, 0, stream>>>(p, d, q);
+    else
+      logmel_scan_back_tiles_kernel<T, 1, false><<<grid, 512, 0, stream>>>(p, d, q);
+  } else {
+    const unsigned grid = (unsigned)(s.parts * s.slabs);
+    q.part_rows = s.part_rows;
+    q.parts = s.parts;
+    if (s.parts > 1) {
+      q.a = reinterpret_cast<float*>(static_cast<char*>(ws) + b.sums);
+      q.b = q.a + s.parts * in.channels;
+      logmel_scan_back_parts_kernel<T, 1><<<grid, 512, 0, stream>>>(p, d, q);
+    }
+    logmel_scan_back_tiles_kernel<T, 1, true><<<grid, 512, 0, stream>>>(p, d, q);
+  }
   if (grad.d_dbias)
-    return logmel_launch_part_sum(q.dbias_part, in.n_seq, in.channels, in.channels, grad.d_dbias,
+    return logmel_launch_part_sum(d.dbias_part, b.items, in.channels, in.channels, grad.d_dbias,
                                   stream);
   return hipGetLastError();
 }
 
 }  // namespace logmel
 
-hipError_t logmel_launch_part_sum(const float* part, int64_t parts, int64_t stride,
+hipError_t logmel_launch_part_sum(const double* part, int64_t parts, int64_t stride,
                                   int64_t channels, float* out, hipStream_t stream) {
-  logmel::logmel_part_sum_kernel<<<(unsigned)((channels + 63) / 64), 256, 0, stream>>>(
+  logmel::logmel_part_sum_kernel<<<(unsigned)((channels + 63) / 64), 1024, 0, stream>>>(
       part, parts, stride, channels, out);
   return hipGetLastError();
 }
 
-int64_t logmel_scan_workspace(const logmel_scan_input& in, int backward, int) {
-  return backward ? in.n_seq * in.channels * 4 : 0;
+int64_t logmel_scan_workspace(const logmel_scan_input& in, int backward, int cus) {
+  const logmel::Split s = logmel::scan_split(in, cus, backward);
+  if (backward) return logmel::back_space(in, s).bytes;
+  return s.how == logmel::Split::kParts && s.parts > 1 ? 3 * s.parts * in.channels * 4 : 0;
 }
 
 hipError_t logmel_launch_scan(const logmel_scan_input& in, void* h, int64_t h_stride,

@@ -48,6 +48,8 @@ def scan(x, g, off, bias=None, state=None, dh=None, dstate_out=None, dtype="floa
     gb = g.astype(np.float64) + (0.0 if bias is None else bias.astype(np.float64))
     a, u = sigmoid(gb), sigmoid(-gb)
     k = 6.0 + 2.0 * np.abs(gb) + 4.0
+    if bias is not None:
+        k = k + 2.0 * np.abs(bias.astype(np.float64))
     h0 = np.zeros((n, c)) if state is None else state.astype(np.float64)
     h = np.full((rows, c), np.nan)
     prev, prev_err, prev_abs = h.copy(), h.copy(), h.copy()
