@@ -1,8 +1,17 @@
 // The block norm and its gradient (gfx950):
 //   t = h / rms(h) * w_post * silu(gate), y = res + scale * t,
 //   z = y / rms(y) * w_pre.
+//
+// A row is held by kLanes lanes, 16 bytes of it per lane and vector, kVecs
+// vectors per lane, from its one read to its writes; the sums over it are
+// formed in registers (and across wavefronts, where a row takes more than
+// one, through LDS). The grid is resident and walks the rows, so a lane reads
+// its channels' parameters once, and the next rows' values are on their way
+// while a row is worked.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "logmel_rows.h"
 #include "logmel_rows_launch.h"
@@ -11,7 +20,8 @@ namespace logmel {
 
 template <typename T>
 struct NormArgs {
-  int64_t rows, channels;
+  int64_t rows;
+  int channels;
   const T* res;
   int64_t ress;
   const T* h;
@@ -22,6 +32,14 @@ struct NormArgs {
   const float* scale;
   const float* w_pre;
   float eps;
+};
+
+template <typename T>
+struct NormOut {
+  T* y;
+  int64_t ys;
+  T* z;
+  int64_t zs;
 };
 
 template <typename T>
@@ -36,136 +54,421 @@ struct NormGradArgs {
   int64_t dhs;
   T* dgate;
   int64_t dgates;
-  double* part;   // [workgroups][3][channels]: dw_post, dscale, dw_pre
+  float* part;   // [workgroups][2][channels]: sums of G n act and of dz y / rms(y); or null
 };
 
-// Sum over the workgroup's 4 wavefronts, in every lane.
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float sums[4];
+// What stands between res and y.
+enum Parts { kNone, kNorm, kGated };
+
+template <int kPattern>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                           0, __builtin_bit_cast(int, v), kPattern, 0xf, 0xf, true));
+}
+
+// Sum over 16, 32 or 64 lanes, in every one of them: neighbours, pairs, then
+// the mirrored half rows and rows of 16, which hold one value each by then;
+// rows and halves of the wavefront by the lane swaps.
+template <int kLanes>
+__device__ __forceinline__ float lane_sum(float v) {
+  v = dpp_add<0xB1>(v);    // quad_perm 1 0 3 2
+  v = dpp_add<0x4E>(v);    // quad_perm 2 3 0 1
+  v = dpp_add<0x141>(v);   // row_half_mirror
+  v = dpp_add<0x140>(v);   // row_mirror
+  if constexpr (kLanes >= 32) {
+    const unsigned b = __builtin_bit_cast(unsigned, v);
+    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+    v = __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
+  }
+  if constexpr (kLanes >= 64) {
+    const unsigned c = __builtin_bit_cast(unsigned, v);
+    const auto s = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+    v = __builtin_bit_cast(float, (unsigned)s[0]) + __builtin_bit_cast(float, (unsigned)s[1]);
+  }
+  return v;
+}
+
+// Wavefronts per SIMD that the kernels leave room for. The gradient of a gated
+// 2-byte row holds eight values of five operands per lane; where a wavefront
+// takes several rows, whose addresses are then per lane too, that is more than
+// the 128 registers of four (96 us for 191,872 x 128 bf16 with three, 112 with
+// values spilled).
+constexpr int front_waves(int lanes) { return lanes > 256 ? 4 : 5; }
+constexpr int back_waves(bool narrow_gated) { return narrow_gated ? 3 : 4; }
+
+template <int kLanes>
+constexpr int kThreads = kLanes > 256 ? kLanes : 256;
+
+// Sums over a row's lanes, up to two at once. Rows of several wavefronts meet
+// in LDS: one barrier per sum, on two slots in turn (a slot is written again
+// only after the barrier of the other, which comes after its last read).
+template <int kLanes>
+struct RowSum {
+  static constexpr bool kShared = kLanes > 64;
+  static constexpr int kWaves = kThreads<kLanes> / 64;
+  float (*slots)[2][kWaves];
+  int turn = 0;
+
+  __device__ void operator()(float& a, float& b, bool two) {
+    a = lane_sum<kLanes>(a);
+    if (two) b = lane_sum<kLanes>(b);
+    if constexpr (kShared) {
+      const int wave = threadIdx.x >> 6;
+      constexpr int kPer = kLanes / 64;
+      const int w0 = wave / kPer * kPer;
+      if ((threadIdx.x & 63) == 0) {
+        slots[turn][0][wave] = a;
+        if (two) slots[turn][1][wave] = b;
+      }
+      __syncthreads();
+      a = b = 0.0f;
 #pragma unroll
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) sums[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return (sums[0] + sums[1]) + (sums[2] + sums[3]);
-}
-
-// The factors of channel c of row r; r1 = 1 / rms(h).
-template <typename T>
-struct Cell {
-  float h, n, act, slope, s, t, y;
-  __device__ Cell(const NormArgs<T>& p, int64_t r, int64_t c, float r1) {
-    y = (float)p.res[r * p.ress + c];
-    if (!p.h) return;
-    h = (float)p.h[r * p.hs + c];
-    n = h * r1 * (p.w_post ? p.w_post[c] : 1.0f);
-    act = 1.0f;
-    if (p.o) {
-      const float o = (float)p.o[r * p.os + c];
-      float a, u;
-      Gate<T>::pair(o, 0.0f, a, u);
-      act = o * a;
-      slope = a * __builtin_fmaf(o, u, 1.0f);
+      for (int i = 0; i < kPer; ++i) {
+        a += slots[turn][0][w0 + i];
+        if (two) b += slots[turn][1][w0 + i];
+      }
+      turn ^= 1;
     }
-    s = p.scale ? p.scale[c] : 1.0f;
-    t = n * act;
-    y = __builtin_fmaf(s, t, y);
+  }
+  __device__ void operator()(float& a) {
+    float b = 0.0f;
+    (*this)(a, b, false);
   }
 };
 
-// One workgroup per row, a pass over the row for each sum it needs.
-template <typename T>
-__global__ __launch_bounds__(256) void logmel_norm_simple_kernel(NormArgs<T> p, T* y, int64_t ys,
-                                                                 T* z, int64_t zs) {
-  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-    float r1 = 0.0f;
-    if (p.h) {
-      float s = 0.0f;
-      for (int64_t c = threadIdx.x; c < p.channels; c += 256) {
-        const float h = (float)p.h[r * p.hs + c];
-        s = __builtin_fmaf(h, h, s);
+// The channels a lane holds: vector j is c[j] .. c[j] + V - 1. The last vector
+// of a width that V does not divide is shifted back to end with the row, so
+// that it is read and written whole: its first values are another lane's too,
+// who writes the same, and only the sums leave them out. Lanes past the row's
+// end hold nothing. (Rows narrower than V go value by value.)
+template <int kLanes, int kVecs, int V>
+struct Channels {
+  int C;
+  int c[kVecs], skip[kVecs];
+  bool on[kVecs];
+
+  __device__ explicit Channels(int channels) : C(channels) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      const int first = (j * kLanes + (int)(threadIdx.x & (kLanes - 1))) * V;
+      on[j] = first < C;
+      c[j] = first + V <= C || C < V ? first : C - V;
+      skip[j] = first - c[j];
+    }
+  }
+  // Whether value i of vector j counts in this lane's sums.
+  __device__ __forceinline__ bool counts(int j, int i) const {
+    return on[j] && i >= skip[j] && c[j] + i < C;
+  }
+};
+
+// A lane's vectors of one row operand, 0 where it holds nothing.
+template <typename T, int kLanes, int kVecs>
+struct RowPiece {
+  static constexpr int V = 16 / sizeof(T);
+  using Ch = Channels<kLanes, kVecs, V>;
+  Packed<T, V> v[kVecs];
+
+  __device__ __forceinline__ void load(const T* row, const Ch& k, bool on) {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) {
+      v[j] = Packed<T, V>{};
+      if (on && k.on[j]) {
+        if (k.C >= V) {
+          v[j] = row_load<T, V>(row + k.c[j]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (i < k.C) v[j].v[i] = row[i];
+        }
       }
-      r1 = 1.0f / __builtin_sqrtf(block_sum(s) / (float)p.channels + p.eps);
     }
-    float s = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.channels; c += 256) {
-      const Cell<T> k(p, r, c, r1);
-      s = __builtin_fmaf(k.y, k.y, s);
-      if (y) y[r * ys + c] = (T)k.y;
+  }
+
+  __device__ __forceinline__ float at(int j, int i) const { return (float)v[j].v[i]; }
+
+  // Keeps the values packed up to here: what is unpacked after this point is
+  // unpacked anew (an instruction per value) instead of being held in twice
+  // the registers since its last use.
+  __device__ __forceinline__ void repack() {
+    if constexpr (sizeof(T) == 2) {
+      struct Words {
+        uint32_t w[4];
+      };
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j) {
+        Words x = __builtin_bit_cast(Words, v[j]);
+        asm("" : "+v"(x.w[0]), "+v"(x.w[1]), "+v"(x.w[2]), "+v"(x.w[3]));
+        v[j] = __builtin_bit_cast(Packed<T, V>, x);
+      }
     }
-    if (!z) continue;
-    const float r2 = 1.0f / __builtin_sqrtf(block_sum(s) / (float)p.channels + p.eps);
-    for (int64_t c = threadIdx.x; c < p.channels; c += 256)
-      z[r * zs + c] = (T)(Cell<T>(p, r, c, r1).y * r2 * (p.w_pre ? p.w_pre[c] : 1.0f));
+  }
+};
+
+template <typename T, int kLanes, int kVecs, int V>
+__device__ __forceinline__ void piece_store(T* row, const Channels<kLanes, kVecs, V>& k,
+                                            const float (&x)[kVecs][V]) {
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    if (!k.on[j]) continue;
+    if (k.C >= V) {
+      row_store<T, V>(row + k.c[j], x[j]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < k.C) row[i] = (T)x[j][i];
+    }
   }
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void logmel_norm_backward_simple_kernel(NormArgs<T> p,
-                                                                          NormGradArgs<T> q) {
-  double* part = q.part + (int64_t)blockIdx.x * 3 * p.channels;
-  for (int64_t c = threadIdx.x; c < p.channels; c += 256)
-    part[c] = part[p.channels + c] = part[2 * p.channels + c] = 0.0;
+// A lane's channels of a parameter, 1 where it is absent.
+template <int kLanes, int kVecs, int V>
+__device__ __forceinline__ void load_params(float (&r)[kVecs][V], const float* p,
+                                            const Channels<kLanes, kVecs, V>& k) {
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      r[j][i] = p && k.on[j] && k.c[j] + i < k.C ? p[k.c[j] + i] : 1.0f;
+}
+
+// w_post scale, the two factors of t that do not depend on the row.
+template <typename T, int kLanes, int kVecs, int V>
+__device__ __forceinline__ void load_block_params(float (&r)[kVecs][V], const NormArgs<T>& p,
+                                                  const Channels<kLanes, kVecs, V>& k) {
+  float s[kVecs][V];
+  load_params(r, p.w_post, k);
+  load_params(s, p.scale, k);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) r[j][i] *= s[j][i];
+}
+
+// The workgroup's row of this lane, 0 on; one for the whole wavefront, and so
+// in a scalar register, where a row takes a wavefront or more.
+template <int kLanes>
+__device__ __forceinline__ int group_of() {
+  const int g = threadIdx.x / kLanes;
+  return kLanes >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
+}
+
+template <typename T, int kParts, int kLanes, int kVecs>
+__global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_norm_kernel(NormArgs<T> p,
+                                                                         NormOut<T> out) {
+  using P = RowPiece<T, kLanes, kVecs>;
+  constexpr int V = P::V;
+  constexpr int kRows = kThreads<kLanes> / kLanes;
+  __shared__ float slots[2][2][kThreads<kLanes> / 64];
+  RowSum<kLanes> sum{slots};
+  const typename P::Ch k(p.channels);
   const float inv = 1.0f / (float)p.channels;
-  for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-    float r1 = 0.0f;
-    if (p.h) {
-      float s = 0.0f;
-      for (int64_t c = threadIdx.x; c < p.channels; c += 256) {
-        const float h = (float)p.h[r * p.hs + c];
-        s = __builtin_fmaf(h, h, s);
+  float w1[kVecs][V], w2[kVecs][V];
+  if constexpr (kParts != kNone) load_block_params(w1, p, k);
+  load_params(w2, p.w_pre, k);
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t r = (int64_t)blockIdx.x * kRows + group_of<kLanes>();
+  P res, h, o;
+  auto load = [&](int64_t row) {
+    const bool on = row < p.rows;
+    res.load(p.res + row * p.ress, k, on);
+    if constexpr (kParts != kNone) h.load(p.h + row * p.hs, k, on);
+    if constexpr (kParts == kGated) o.load(p.o + row * p.os, k, on);
+  };
+  load(r);
+  // the workgroup's rows together: barriers are met by all of it
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.rows; first += step, r += step) {
+    float y[kVecs][V], t[kVecs][V];
+    float s1 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        y[j][i] = res.at(j, i);
+        if constexpr (kParts != kNone) {
+          const float x = h.at(j, i);
+          s1 = k.counts(j, i) ? __builtin_fmaf(x, x, s1) : s1;
+          t[j][i] = x * w1[j][i];
+        }
+        if constexpr (kParts == kGated) {
+          float a, u;
+          Gate<T>::pair(o.at(j, i), 0.0f, a, u);
+          t[j][i] *= o.at(j, i) * a;
+        }
       }
-      r1 = 1.0f / __builtin_sqrtf(block_sum(s) * inv + p.eps);
+    if (first + step < p.rows) load(r + step);
+    if constexpr (kParts != kNone) {
+      sum(s1);
+      const float r1 = 1.0f / __builtin_sqrtf(__builtin_fmaf(s1, inv, p.eps));
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[j][i] = __builtin_fmaf(t[j][i], r1, y[j][i]);
+      if (out.y && r < p.rows) piece_store(out.y + r * out.ys, k, y);
     }
-    float r2 = 0.0f, m2 = 0.0f;
-    auto weighted = [&](int64_t c) {
-      return q.dz ? (float)q.dz[r * q.dzs + c] * (p.w_pre ? p.w_pre[c] : 1.0f) : 0.0f;
-    };
-    if (q.dz) {
-      float s = 0.0f, m = 0.0f;
-      for (int64_t c = threadIdx.x; c < p.channels; c += 256) {
-        const float y = Cell<T>(p, r, c, r1).y;
-        s = __builtin_fmaf(y, y, s);
-        m = __builtin_fmaf(weighted(c), y, m);
-      }
-      r2 = 1.0f / __builtin_sqrtf(block_sum(s) * inv + p.eps);
-      m2 = block_sum(m) * inv;
-    }
-    auto total = [&](int64_t c, float y) {
-      float d = q.dy ? (float)q.dy[r * q.dys + c] : 0.0f;
-      if (q.dz) d += r2 * (weighted(c) - y * (r2 * r2 * m2));
-      return d;
-    };
-    float m = 0.0f;
-    for (int64_t c = threadIdx.x; c < p.channels; c += 256) {
-      const Cell<T> k(p, r, c, r1);
-      const float d = total(c, k.y);
-      if (p.h)
-        m = __builtin_fmaf(d * k.s * k.act * (p.w_post ? p.w_post[c] : 1.0f), k.h, m);
-    }
-    const float m1 = p.h ? block_sum(m) * inv : 0.0f;
-    for (int64_t c = threadIdx.x; c < p.channels; c += 256) {
-      const Cell<T> k(p, r, c, r1);
-      const float d = total(c, k.y);
-      q.dres[r * q.dress + c] = (T)d;
-      if (p.h) {
-        const float ds = d * k.s;
-        const float qa = ds * k.act;
-        if (p.o) q.dgate[r * q.dgates + c] = (T)(ds * k.n * k.slope);
-        const float w = qa * (p.w_post ? p.w_post[c] : 1.0f);
-        q.dh[r * q.dhs + c] = (T)(r1 * (w - k.h * (r1 * r1 * m1)));
-        part[c] += qa * k.h * r1;
-        part[p.channels + c] += d * k.t;
-      }
-      if (q.dz) part[2 * p.channels + c] += (float)q.dz[r * q.dzs + c] * k.y * r2;
+    if (out.z) {
+      float s2 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          s2 = k.counts(j, i) ? __builtin_fmaf(y[j][i], y[j][i], s2) : s2;
+      sum(s2);
+      const float r2 = 1.0f / __builtin_sqrtf(__builtin_fmaf(s2, inv, p.eps));
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[j][i] *= r2 * w2[j][i];
+      if (r < p.rows) piece_store(out.z + r * out.zs, k, y);
     }
   }
+}
+
+// The gradient. Per row, with n = h / rms(h), w = w_post scale, q = dz w_pre
+// and G = dy + r2 (q - y r2^2 mean(q y)):
+//   dres = G;  e = G act w;  dh = r1 (e - h r1^2 mean(e h));
+//   dgate = G n w slope;  dw_post = scale sum(G n act), dscale = w_post of the
+//   same sum;  dw_pre = sum(dz y r2).
+// Three sums over the row one after the other. The two sums over the lane's
+// rows stay in its registers to the end, then the workgroup's rows are added
+// in LDS and each workgroup writes one part. Eight values per lane keep all of
+// it within 128 registers, so that 16 wavefronts a compute unit have their
+// rows in flight.
+template <typename T, int kParts, int kLanes, int kVecs>
+__global__ __launch_bounds__(kThreads<kLanes>,
+                             back_waves(kParts == kGated && sizeof(T) == 2 &&
+                                        kLanes < 64)) void logmel_norm_backward_kernel(NormArgs<T> p,
+                                                                                       NormGradArgs<T> q) {
+  using P = RowPiece<T, kLanes, kVecs>;
+  constexpr int V = P::V;
+  constexpr int kRows = kThreads<kLanes> / kLanes;
+  __shared__ float slots[2][2][kThreads<kLanes> / 64];
+  RowSum<kLanes> sum{slots};
+  const typename P::Ch k(p.channels);
+  const float inv = 1.0f / (float)p.channels;
+  float w1[kVecs][V], w2[kVecs][V];
+  float a1[kVecs][V], a2[kVecs][V];
+  if constexpr (kParts != kNone) load_block_params(w1, p, k);
+  load_params(w2, p.w_pre, k);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) a1[j][i] = a2[j][i] = 0.0f;
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t r = (int64_t)blockIdx.x * kRows + group_of<kLanes>();
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.rows; first += step, r += step) {
+    P res, h, o, dy, dz;
+    const bool on = r < p.rows;
+    if constexpr (kParts != kNone) h.load(p.h + r * p.hs, k, on);
+    res.load(p.res + r * p.ress, k, on);
+    if constexpr (kParts == kGated) o.load(p.o + r * p.os, k, on);
+    dz.load(q.dz + r * q.dzs, k, on && q.dz);
+    dy.load(q.dy + r * q.dys, k, on && q.dy);
+    float r1 = 0.0f;
+    float y[kVecs][V], sig[kVecs][V];   // sig: sigmoid(gate)
+    if constexpr (kParts != kNone) {
+      float s1 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          s1 = k.counts(j, i) ? __builtin_fmaf(h.at(j, i), h.at(j, i), s1) : s1;
+      sum(s1);
+      r1 = 1.0f / __builtin_sqrtf(__builtin_fmaf(s1, inv, p.eps));
+      h.repack();
+    }
+    // silu(gate), formed again wherever it is needed
+    auto act = [&](int j, int i) { return kParts == kGated ? o.at(j, i) * sig[j][i] : 1.0f; };
+    float s2 = 0.0f, m2 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        y[j][i] = res.at(j, i);
+        if constexpr (kParts != kNone) {
+          float u;
+          if constexpr (kParts == kGated) Gate<T>::pair(o.at(j, i), 0.0f, sig[j][i], u);
+          y[j][i] = __builtin_fmaf(h.at(j, i) * r1, w1[j][i] * act(j, i), y[j][i]);
+        }
+        const float yc = k.counts(j, i) ? y[j][i] : 0.0f;
+        s2 = __builtin_fmaf(yc, y[j][i], s2);
+        m2 = __builtin_fmaf(dz.at(j, i) * w2[j][i], yc, m2);
+      }
+    float r2 = 0.0f, k2 = 0.0f;
+    if (q.dz) {
+      sum(s2, m2, true);
+      r2 = 1.0f / __builtin_sqrtf(__builtin_fmaf(s2, inv, p.eps));
+      k2 = r2 * r2 * (m2 * inv);
+      dz.repack();
+    }
+    h.repack();
+    o.repack();
+    float m1 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float z = dz.at(j, i);
+        a2[j][i] = __builtin_fmaf(z * r2, y[j][i], a2[j][i]);
+        // y holds G from here on
+        y[j][i] = __builtin_fmaf(r2, __builtin_fmaf(-k2, y[j][i], z * w2[j][i]), dy.at(j, i));
+        if constexpr (kParts != kNone)
+          m1 = k.counts(j, i)
+                   ? __builtin_fmaf(y[j][i] * (w1[j][i] * act(j, i)), h.at(j, i), m1)
+                   : m1;
+      }
+    if (on) piece_store(q.dres + r * q.dress, k, y);
+    if constexpr (kParts != kNone) {
+      sum(m1);
+      h.repack();
+      o.repack();
+      const float k1 = r1 * r1 * (m1 * inv);
+#pragma unroll
+      for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float x = h.at(j, i);
+          const float n = x * r1;
+          const float silu = act(j, i);
+          a1[j][i] = __builtin_fmaf(y[j][i] * silu, n, a1[j][i]);
+          const float gw = y[j][i] * w1[j][i];
+          if constexpr (kParts == kGated) {
+            const float s = sig[j][i];   // the slope of silu: s (1 + gate (1 - s))
+            sig[j][i] = gw * n * (s * __builtin_fmaf(o.at(j, i), 1.0f - s, 1.0f));
+          }
+          y[j][i] = r1 * __builtin_fmaf(-k1, x, gw * silu);
+        }
+      if (on) {
+        piece_store(q.dh + r * q.dhs, k, y);
+        if constexpr (kParts == kGated)
+          piece_store(q.dgate + r * q.dgates, k, sig);
+      }
+    }
+  }
+  if (!q.part) return;
+  __shared__ float rows[kRows][kLanes * V * kVecs];
+  auto write = [&](float (&a)[kVecs][V], int which) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (k.counts(j, i)) rows[group_of<kLanes>()][k.c[j] + i] = a[j][i];
+    __syncthreads();
+    for (int c = threadIdx.x; c < k.C; c += kThreads<kLanes>) {
+      float s = 0.0f;
+      for (int g = 0; g < kRows; ++g) s += rows[g][c];
+      q.part[((int64_t)blockIdx.x * 2 + which) * k.C + c] = s;
+    }
+  };
+  if constexpr (kParts != kNone) write(a1, 0);
+  write(a2, 1);
 }
 
 template <typename T>
 NormArgs<T> norm_args(const logmel_norm_input& in) {
   return {in.rows,
-          in.channels,
+          (int)in.channels,
           static_cast<const T*>(in.d_res),
           in.res_stride,
           static_cast<const T*>(in.d_h),
@@ -178,67 +481,114 @@ NormArgs<T> norm_args(const logmel_norm_input& in) {
           in.eps};
 }
 
-int64_t norm_parts(int64_t rows, int cus) { return rows < 4 * cus ? rows : 4 * cus; }
+// The lanes a row takes: the fewest, in powers of two from 16, that hold it
+// with one vector each (8192 fp32 channels: 1024 lanes with two).
+struct NormShape {
+  int lanes, vecs;
+};
 
-template <typename T>
-hipError_t launch_norm(const logmel_norm_input& in, void* y, int64_t ys, void* z, int64_t zs,
-                       hipStream_t stream) {
-  const unsigned grid = (unsigned)(in.rows < (1 << 20) ? in.rows : 1 << 20);
-  logmel_norm_simple_kernel<T><<<grid, 256, 0, stream>>>(norm_args<T>(in), static_cast<T*>(y), ys,
-                                                         static_cast<T*>(z), zs);
-  return hipGetLastError();
+NormShape norm_shape(const logmel_norm_input& in) {
+  const int v = in.type == LOGMEL_F32 ? 4 : 8;
+  const int64_t vecs = (in.channels + v - 1) / v;
+  NormShape s{16, 1};
+  while (s.lanes < vecs && s.lanes < 1024) s.lanes *= 2;
+  if (s.lanes < vecs) s.vecs = 2;
+  return s;
 }
 
-template <typename T>
-hipError_t launch_norm_backward(const logmel_norm_input& in, const logmel_norm_grad& g, void* ws,
-                                int cus, hipStream_t stream) {
-  NormGradArgs<T> q{static_cast<const T*>(g.d_dy),
-                    g.dy_stride,
-                    static_cast<const T*>(g.d_dz),
-                    g.dz_stride,
-                    static_cast<T*>(g.d_dres),
-                    g.dres_stride,
-                    static_cast<T*>(g.d_dh),
-                    g.dh_stride,
-                    static_cast<T*>(g.d_dgate),
-                    g.dgate_stride,
-                    static_cast<double*>(ws)};
-  const int64_t parts = norm_parts(in.rows, cus);
-  if (parts)
-    logmel_norm_backward_simple_kernel<T>
-        <<<(unsigned)parts, 256, 0, stream>>>(norm_args<T>(in), q);
-  float* outs[3] = {g.d_dw_post, g.d_dscale, g.d_dw_pre};
-  for (int i = 0; i < 3; ++i)
-    if (outs[i]) {
-      const hipError_t e = logmel_launch_part_sum(q.part + i * in.channels, parts,
-                                                  3 * in.channels, in.channels, outs[i], stream);
-      if (e != hipSuccess) return e;
+// Workgroups: as many as are resident at once (the kernels' bounds on their
+// registers), or one pass over the rows. Fewer leave rows waiting for memory,
+// more a last round of workgroups that runs alone: 64 x 2998 x 512 bf16 with 3,
+// 4, 5, 6 and 8 wavefronts per SIMD 243, 201, 191, 195 and 234 us.
+int64_t norm_grid(const logmel_norm_input& in, int cus, bool backward) {
+  const int lanes = norm_shape(in).lanes;
+  const int threads = lanes > 256 ? lanes : 256;
+  const bool narrow = in.d_gate && in.type != LOGMEL_F32 && lanes < 64;
+  const int waves = backward ? back_waves(narrow) : front_waves(lanes);
+  const int64_t all = (in.rows + threads / lanes - 1) / (threads / lanes);
+  const int64_t most = (int64_t)cus * waves * 256 / threads;
+  return all < most ? all : most;
+}
+
+// f(type, parts, lanes, vecs) as compile-time constants.
+template <typename F>
+void norm_dispatch(const logmel_norm_input& in, F&& f) {
+  const NormShape s = norm_shape(in);
+  auto shape = [&](auto zero, auto parts) {
+    using std::integral_constant;
+    integral_constant<int, 1> one;
+    if constexpr (sizeof(zero) == 4)
+      if (s.vecs == 2)
+        return f(zero, parts, integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+    switch (s.lanes) {
+      case 16: return f(zero, parts, integral_constant<int, 16>{}, one);
+      case 32: return f(zero, parts, integral_constant<int, 32>{}, one);
+      case 64: return f(zero, parts, integral_constant<int, 64>{}, one);
+      case 128: return f(zero, parts, integral_constant<int, 128>{}, one);
+      case 256: return f(zero, parts, integral_constant<int, 256>{}, one);
+      case 512: return f(zero, parts, integral_constant<int, 512>{}, one);
+      default: return f(zero, parts, integral_constant<int, 1024>{}, one);
     }
-  return hipGetLastError();
+  };
+  auto parts = [&](auto zero) {
+    if (!in.d_h) return shape(zero, std::integral_constant<int, kNone>{});
+    if (!in.d_gate) return shape(zero, std::integral_constant<int, kNorm>{});
+    return shape(zero, std::integral_constant<int, kGated>{});
+  };
+  if (in.type == LOGMEL_F32)
+    parts(0.0f);
+  else if (in.type == LOGMEL_F16)
+    parts((f16_t)0.0f);
+  else
+    parts((bf16_t)0.0f);
 }
+
 
 }  // namespace logmel
 
 int64_t logmel_norm_workspace(const logmel_norm_input& in, int cus) {
-  return logmel::norm_parts(in.rows, cus) * 3 * in.channels * 8;
+  return logmel::norm_grid(in, cus, true) * 2 * in.channels * 4;
 }
 
 hipError_t logmel_launch_norm(const logmel_norm_input& in, void* y, int64_t y_stride, void* z,
-                              int64_t z_stride, int, hipStream_t stream) {
-  auto go = [&](auto zero) {
-    return logmel::launch_norm<decltype(zero)>(in, y, y_stride, z, z_stride, stream);
-  };
-  if (in.type == LOGMEL_F32) return go(0.0f);
-  if (in.type == LOGMEL_F16) return go((logmel::f16_t)0.0f);
-  return go((logmel::bf16_t)0.0f);
+                              int64_t z_stride, int cus, hipStream_t stream) {
+  using namespace logmel;
+  norm_dispatch(in, [&](auto zero, auto parts, auto lanes, auto vecs) {
+    using T = decltype(zero);
+    const NormOut<T> out{static_cast<T*>(y), y_stride, static_cast<T*>(z), z_stride};
+    logmel_norm_kernel<T, parts.value, lanes.value, vecs.value>
+        <<<(unsigned)norm_grid(in, cus, false), kThreads<lanes.value>, 0, stream>>>(
+            norm_args<T>(in), out);
+  });
+  return hipGetLastError();
 }
 
-hipError_t logmel_launch_norm_backward(const logmel_norm_input& in, const logmel_norm_grad& grad,
+hipError_t logmel_launch_norm_backward(const logmel_norm_input& in, const logmel_norm_grad& g,
                                        void* ws, int cus, hipStream_t stream) {
-  auto go = [&](auto zero) {
-    return logmel::launch_norm_backward<decltype(zero)>(in, grad, ws, cus, stream);
-  };
-  if (in.type == LOGMEL_F32) return go(0.0f);
-  if (in.type == LOGMEL_F16) return go((logmel::f16_t)0.0f);
-  return go((logmel::bf16_t)0.0f);
+  using namespace logmel;
+  const int64_t grid = norm_grid(in, cus, true);
+  const PartSums sums[3] = {{g.d_dw_post, 0, in.d_scale},
+                            {g.d_dscale, 0, in.d_w_post},
+                            {g.d_dw_pre, 1, nullptr}};
+  const bool params = g.d_dw_post || g.d_dscale || g.d_dw_pre;
+  float* part = params ? static_cast<float*>(ws) : nullptr;
+  if (grid)
+    norm_dispatch(in, [&](auto zero, auto parts, auto lanes, auto vecs) {
+      using T = decltype(zero);
+      const NormGradArgs<T> q{static_cast<const T*>(g.d_dy),
+                              g.dy_stride,
+                              static_cast<const T*>(g.d_dz),
+                              g.dz_stride,
+                              static_cast<T*>(g.d_dres),
+                              g.dres_stride,
+                              static_cast<T*>(g.d_dh),
+                              g.dh_stride,
+                              static_cast<T*>(g.d_dgate),
+                              g.dgate_stride,
+                              part};
+      logmel_norm_backward_kernel<T, parts.value, lanes.value, vecs.value>
+          <<<(unsigned)grid, kThreads<lanes.value>, 0, stream>>>(norm_args<T>(in), q);
+    });
+  if (params) return logmel_launch_part_sums(part, grid, 2, in.channels, sums, stream);
+  return hipGetLastError();
 }

@@ -22,7 +22,15 @@ hipError_t logmel_launch_norm(const logmel_norm_input& in, void* y, int64_t y_st
 hipError_t logmel_launch_norm_backward(const logmel_norm_input& in, const logmel_norm_grad& grad,
                                        void* ws, int cus, hipStream_t stream);
 
-// out[c] = sum over g of part[g * stride + c], c < channels, in a fixed order
-// (logmel_scan.hip).
-hipError_t logmel_launch_part_sum(const double* part, int64_t parts, int64_t stride,
-                                  int64_t channels, float* out, hipStream_t stream);
+// One sum of a launch: out[c] = factor[c] times the sum over g of
+// part[g][which][c], part being [parts][sums][channels]; factor null: 1, out
+// null: left out.
+struct PartSums {
+  float* out;
+  int which;
+  const float* factor;
+};
+
+// Three of them, each in a fixed order and in fp64 (logmel_scan.hip).
+hipError_t logmel_launch_part_sums(const float* part, int64_t parts, int sums, int64_t channels,
+                                   const PartSums out[3], hipStream_t stream);

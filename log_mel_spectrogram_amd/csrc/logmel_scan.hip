@@ -920,25 +920,41 @@ __global__ __launch_bounds__(512, 2) void logmel_scan_back_tiles_kernel(ScanArgs
 }
 
 // Sums over work items: 64 channels per workgroup; each of its 16 wavefronts
-// takes every sixteenth part, and the sixteen sums are added in order.
-__global__ __launch_bounds__(1024) void logmel_part_sum_kernel(const double* part, int64_t parts,
+// takes every sixteenth part, and the sixteen sums are added in order. Up to
+// three sums in one launch, one per blockIdx.y.
+struct SumOut {
+  PartSums s[3];
+};
+
+template <typename T>
+__global__ __launch_bounds__(1024) void logmel_part_sum_kernel(const T* part, int64_t parts,
                                                                int64_t stride, int64_t channels,
-                                                               float* out) {
+                                                               SumOut o) {
   __shared__ double sums[16][64];
+  const PartSums k = o.s[blockIdx.y];
+  if (!k.out) return;
+  part += k.which * channels;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t c = (int64_t)blockIdx.x * 64 + lane;
   double s = 0.0;
   if (c < channels) {
 #pragma unroll 8
-    for (int64_t g = wave; g < parts; g += 16) s += part[g * stride + c];
+    for (int64_t g = wave; g < parts; g += 16) s += (double)part[g * stride + c];
   }
   sums[wave][lane] = s;
   __syncthreads();
   if (wave == 0 && c < channels) {
     double t = sums[0][lane];
     for (int w = 1; w < 16; ++w) t += sums[w][lane];
-    out[c] = (float)t;
+    k.out[c] = (float)(k.factor ? t * (double)k.factor[c] : t);
   }
+}
+
+hipError_t launch_part_sum(const double* part, int64_t parts, int64_t channels, float* out,
+                           hipStream_t stream) {
+  logmel_part_sum_kernel<<<(unsigned)((channels + 63) / 64), 1024, 0, stream>>>(
+      part, parts, channels, channels, SumOut{{{out, 0, nullptr}}});
+  return hipGetLastError();
 }
 
 template <typename T>
@@ -1090,7 +1106,7 @@ hipError_t launch_scan_backward(const logmel_scan_input& in, const float* checkp
   const Split s = scan_split(in, cus, true);
   const BackSpace b = back_space(in, s);
   if (in.n_seq == 0)   // no offsets to read; the sum over no rows
-    return logmel_launch_part_sum(nullptr, 0, 0, in.channels, grad.d_dbias, stream);
+    return launch_part_sum(nullptr, 0, in.channels, grad.d_dbias, stream);
   ScanGradArgs<T> d{};
   d.dh = static_cast<const T*>(grad.d_dh);
   d.dhs = grad.dh_stride;
@@ -1120,17 +1136,16 @@ hipError_t launch_scan_backward(const logmel_scan_input& in, const float* checkp
     logmel_scan_back_tiles_kernel<T, 1, true><<<grid, 512, 0, stream>>>(p, d, q);
   }
   if (grad.d_dbias)
-    return logmel_launch_part_sum(d.dbias_part, b.items, in.channels, in.channels, grad.d_dbias,
-                                  stream);
+    return launch_part_sum(d.dbias_part, b.items, in.channels, grad.d_dbias, stream);
   return hipGetLastError();
 }
 
 }  // namespace logmel
 
-hipError_t logmel_launch_part_sum(const double* part, int64_t parts, int64_t stride,
-                                  int64_t channels, float* out, hipStream_t stream) {
-  logmel::logmel_part_sum_kernel<<<(unsigned)((channels + 63) / 64), 1024, 0, stream>>>(
-      part, parts, stride, channels, out);
+hipError_t logmel_launch_part_sums(const float* part, int64_t parts, int sums, int64_t channels,
+                                   const PartSums out[3], hipStream_t stream) {
+  logmel::logmel_part_sum_kernel<<<dim3((unsigned)((channels + 63) / 64), 3), 1024, 0, stream>>>(
+      part, parts, sums * channels, channels, logmel::SumOut{{out[0], out[1], out[2]}});
   return hipGetLastError();
 }
 
