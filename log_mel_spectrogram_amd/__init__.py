@@ -694,21 +694,25 @@ def _rows(t, what, like, plan):
         return None, 0
     if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a torch tensor on a ROCm device")
-    if t.device.index != plan.device:
+    if t is not like:
+        if t.dtype != like.dtype:
+            raise TypeError(f"{what} must be {like.dtype}, got {t.dtype}")
+        if t.shape != like.shape:
+            raise ValueError(f"{what} must be [rows, channels] = {list(like.shape)}, "
+                             f"got {list(t.shape)}")
+    if t.get_device() != plan.device:
         raise ValueError(f"{what} must be on the plan's device {plan.device}, got {t.device}")
-    if t.dtype != like.dtype:
-        raise TypeError(f"{what} must be {like.dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape != like.shape:
-        raise ValueError(f"{what} must be [rows, channels] = {list(like.shape)}, "
-                         f"got {list(t.shape)}")
+    strides = t.stride()
+    if len(strides) != 2:
+        raise ValueError(f"{what} must be [rows, channels], got {list(t.shape)}")
+    stride, inner = strides
     rows, channels = t.shape
-    if channels > 1 and t.stride(1) != 1:
+    if inner != 1 and channels > 1:
         raise ValueError(f"{what} must have contiguous rows")
-    stride = t.stride(0)
-    if rows <= 1:
-        stride = max(stride, channels)
     if stride < channels:
-        raise ValueError(f"{what} must not repeat or overlap rows")
+        if rows > 1:
+            raise ValueError(f"{what} must not repeat or overlap rows")
+        stride = channels
     # an empty operand has no address; any aligned one stands for it
     return (t.data_ptr() or 16), stride
 
@@ -720,15 +724,23 @@ def _params(t, what, shape, plan):
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{what} must be a torch tensor on a ROCm device")
-    if t.device.index != plan.device:
+    if t.get_device() != plan.device:
         raise ValueError(f"{what} must be on the plan's device {plan.device}, got {t.device}")
     if t.dtype != torch.float32:
         raise TypeError(f"{what} must be torch.float32, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr() or None
+
+
+def _raw_stream(stream, plan):
+    """The HIP stream of a call on the plan's device (None: torch's current
+    one, asked for without making a stream object)."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(plan.device)
 
 
 def _empty(shape, dtype, device, stream):
@@ -757,12 +769,16 @@ def _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames):
     px, sx = _rows(x, "x", x, plan)
     pg, sg = _rows(gate, "gate", x, plan)
     rows, channels = x.shape
-    n_seq = int(seq_offsets.numel()) - 1
-    if seq_offsets.dim() != 1 or n_seq < 0:
-        raise ValueError("seq_offsets must have n_seq + 1 entries")
-    if seq_offsets.device != x.device:
-        raise ValueError("seq_offsets must be on the device of x")
-    po = _dev_ptr(seq_offsets, torch.int64, "seq_offsets").value
+    if not isinstance(seq_offsets, torch.Tensor) or not seq_offsets.is_cuda:
+        raise TypeError("seq_offsets must be a torch tensor on a ROCm device")
+    if seq_offsets.dtype != torch.int64:
+        raise TypeError(f"seq_offsets must be torch.int64, got {seq_offsets.dtype}")
+    n_seq = seq_offsets.numel() - 1
+    if seq_offsets.dim() != 1 or n_seq < 0 or not seq_offsets.is_contiguous():
+        raise ValueError("seq_offsets must be contiguous with n_seq + 1 entries")
+    if seq_offsets.get_device() != plan.device:
+        raise ValueError(f"seq_offsets must be on the plan's device {plan.device}")
+    po = seq_offsets.data_ptr()
     return logmel_scan_input(ty, rows, channels, n_seq, po, int(max_frames), px, sx, pg, sg,
                              _params(bias, "bias", (channels,), plan),
                              _params(state, "state", (n_seq, channels), plan))
@@ -797,7 +813,7 @@ def logmel_gated_scan(plan: Plan, x, gate, seq_offsets, bias=None, state=None, o
     need = _gated_scan_workspace(plan.handle, inp, 0)
     ws, pws = _workspace(need, x.device, stream, "logmel_gated_scan")
     _check(_gated_scan(plan.handle, inp, po, so, pso, pck, pws, need,
-                       _stream_handle(stream, x.device)), "logmel_gated_scan")
+                       _raw_stream(stream, plan)), "logmel_gated_scan")
     return out
 
 
@@ -826,7 +842,7 @@ def logmel_gated_scan_backward(plan: Plan, dh, x, gate, seq_offsets, checkpoints
     need = _gated_scan_workspace(plan.handle, inp, 1)
     ws, pws = _workspace(need, x.device, stream, "logmel_gated_scan_backward")
     _check(_gated_scan_backward(plan.handle, inp, pck, grad, pws, need,
-                                _stream_handle(stream, x.device)), "logmel_gated_scan_backward")
+                                _raw_stream(stream, plan)), "logmel_gated_scan_backward")
     return dx, dgate, dbias, dstate
 
 
@@ -859,7 +875,7 @@ def logmel_block_norm(plan: Plan, res, h=None, gate=None, w_post=None, scale=Non
         z = _empty(res.shape, res.dtype, res.device, stream)
     py, sy = _rows(y, "y", res, plan)
     pz, sz = _rows(z, "z", res, plan)
-    _check(_block_norm(plan.handle, inp, py, sy, pz, sz, _stream_handle(stream, res.device)),
+    _check(_block_norm(plan.handle, inp, py, sy, pz, sz, _raw_stream(stream, plan)),
            "logmel_block_norm")
     return y, z
 
@@ -893,6 +909,6 @@ def logmel_block_norm_backward(plan: Plan, res, h=None, gate=None, w_post=None, 
     need = _block_norm_workspace(plan.handle, inp)
     ws, pws = _workspace(need, res.device, stream, "logmel_block_norm_backward")
     _check(_block_norm_backward(plan.handle, inp, grad, pws, need,
-                                _stream_handle(stream, res.device)),
+                                _raw_stream(stream, plan)),
            "logmel_block_norm_backward")
     return out

@@ -666,7 +666,7 @@ def test_binding_refuses(env):
         lm.logmel_gated_scan(plan, x, x.half(), off)
     with pytest.raises(TypeError):
         lm.logmel_gated_scan(plan, x, x, off.int())
-    with pytest.raises(ValueError):
+    with pytest.raises(TypeError):
         lm.logmel_gated_scan(plan, x, x, off.cpu())
     with pytest.raises(ValueError):
         lm.logmel_gated_scan(plan, x, x, off, state=torch.zeros((2, 8), device=dev))

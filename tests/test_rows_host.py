@@ -170,7 +170,8 @@ def test_scan_backward_refuses(lm):
                 dgate_stride=8)
 
     def call(ck=0x500000, ws=0x400000, wsb=1 << 30, **kw):
-        return lm._gated_scan_backward(FAKE, _scan_in(lm), ck,
+        # with a bias there are its gradient's sums to hold, so workspace is needed
+        return lm._gated_scan_backward(FAKE, _scan_in(lm, d_bias=0x700000), ck,
                                        lm.logmel_scan_grad(**{**fine, **kw}), ws, wsb, None)
 
     assert call(ck=None) == bad
