@@ -187,20 +187,10 @@ struct RowPiece {
 
   __device__ __forceinline__ float at(int j, int i) const { return (float)v[j].v[i]; }
 
-  // Keeps the values packed up to here: what is unpacked after this point is
-  // unpacked anew (an instruction per value) instead of being held in twice
-  // the registers since its last use.
-  __device__ __forceinline__ void repack() {
+  __device__ __forceinline__ void unpack_anew() {
     if constexpr (sizeof(T) == 2) {
-      struct Words {
-        uint32_t w[4];
-      };
 #pragma unroll
-      for (int j = 0; j < kVecs; ++j) {
-        Words x = __builtin_bit_cast(Words, v[j]);
-        asm("" : "+v"(x.w[0]), "+v"(x.w[1]), "+v"(x.w[2]), "+v"(x.w[3]));
-        v[j] = __builtin_bit_cast(Packed<T, V>, x);
-      }
+      for (int j = 0; j < kVecs; ++j) repack(v[j]);
     }
   }
 };
@@ -375,7 +365,7 @@ __global__ __launch_bounds__(kThreads<kLanes>,
           s1 = k.counts(j, i) ? __builtin_fmaf(h.at(j, i), h.at(j, i), s1) : s1;
       sum(s1);
       r1 = 1.0f / __builtin_sqrtf(__builtin_fmaf(s1, inv, p.eps));
-      h.repack();
+      h.unpack_anew();
     }
     // silu(gate), formed again wherever it is needed
     auto act = [&](int j, int i) { return kParts == kGated ? o.at(j, i) * sig[j][i] : 1.0f; };
@@ -399,10 +389,10 @@ __global__ __launch_bounds__(kThreads<kLanes>,
       sum(s2, m2, true);
       r2 = 1.0f / __builtin_sqrtf(__builtin_fmaf(s2, inv, p.eps));
       k2 = r2 * r2 * (m2 * inv);
-      dz.repack();
+      dz.unpack_anew();
     }
-    h.repack();
-    o.repack();
+    h.unpack_anew();
+    o.unpack_anew();
     float m1 = 0.0f;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
@@ -420,8 +410,8 @@ __global__ __launch_bounds__(kThreads<kLanes>,
     if (on) piece_store(q.dres + r * q.dress, k, y);
     if constexpr (kParts != kNone) {
       sum(m1);
-      h.repack();
-      o.repack();
+      h.unpack_anew();
+      o.unpack_anew();
       const float k1 = r1 * r1 * (m1 * inv);
 #pragma unroll
       for (int j = 0; j < kVecs; ++j)

@@ -24,6 +24,27 @@ __device__ __forceinline__ Packed<T, V> row_load(const T* p) {
   return r;
 }
 
+// The same values to a reader, to the compiler new ones: what is unpacked from
+// them afterwards is unpacked anew (an instruction per 2-byte value) instead
+// of being held as floats, in up to twice the registers, since its last use.
+template <typename T, int V>
+__device__ __forceinline__ void repack(Packed<T, V>& p) {
+  if constexpr (sizeof(p) % 4 == 0) {
+    struct Words {
+      uint32_t w[sizeof(p) / 4];
+    };
+    Words x = __builtin_bit_cast(Words, p);
+#pragma unroll
+    for (size_t i = 0; i < sizeof(p) / 4; ++i) asm("" : "+v"(x.w[i]));
+    p = __builtin_bit_cast(Packed<T, V>, x);
+  } else {
+    static_assert(sizeof(p) == 2);
+    uint16_t x = __builtin_bit_cast(uint16_t, p);
+    asm("" : "+v"(x));
+    p = __builtin_bit_cast(Packed<T, V>, x);
+  }
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void row_store(T* p, const float (&x)[V]) {
   Packed<T, V> r;

@@ -191,18 +191,31 @@ __device__ __forceinline__ void for_empty(const int64_t* off, int64_t n, int64_t
   }
 }
 
+// The offset of the next row, as a new value to the compiler.
+__device__ __forceinline__ int64_t next_row(int64_t at, int64_t stride) {
+  at += stride;
+  asm("" : "+s"(at));
+  return at;
+}
+
 template <typename T, int V>
 __device__ __forceinline__ void load_run(Packed<T, V> (&r)[kRun], const T* base, int64_t stride,
                                          uint32_t c, int64_t w0, int64_t lo, int64_t hi) {
-  const T* p = base + w0 * stride;
+  // a running scalar offset: 16 multiples of the stride kept over the tiles
+  // would not fit the scalar registers
+  int64_t at = w0 * stride;
   if (lo <= w0 && w0 + kRun <= hi) {
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) r[i] = row_load<T, V>(p + i * stride + c);
+    for (int i = 0; i < kRun; ++i) {
+      r[i] = row_load<T, V>(base + at + c);
+      at = next_row(at, stride);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
       r[i] = Packed<T, V>{};
-      if (w0 + i >= lo && w0 + i < hi) r[i] = row_load<T, V>(p + i * stride + c);
+      if (w0 + i >= lo && w0 + i < hi) r[i] = row_load<T, V>(base + at + c);
+      at = next_row(at, stride);
     }
   }
 }
@@ -239,6 +252,18 @@ __device__ __forceinline__ uint32_t lane_offset(int64_t slab, int64_t channels, 
   const int64_t most = channels - V - base;
   const int64_t c = (threadIdx.x & 63) * V;
   return (uint32_t)(c < most ? c : most);
+}
+
+// A workgroup's item and slab. Workgroups go to the 8 dies in turn, so the
+// slabs of one item are 8 apart: the ends of unaligned row pieces, which two
+// slabs share, meet in one die's L2.
+struct Place {
+  int64_t item, slab;
+};
+
+__device__ __forceinline__ Place place_of(int64_t slabs) {
+  const int64_t b = blockIdx.x;
+  return {b / (8 * slabs) * 8 + b % 8, b / 8 % slabs};
 }
 
 struct PartArgs {
@@ -307,9 +332,11 @@ __global__ __launch_bounds__(512) void logmel_scan_parts_kernel(ScanArgs<T> p, P
   __shared__ WaveTotals<V> lds;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
-  const int64_t k = q.parts - 1 - blockIdx.x / slabs;
+  const Place at_grid = place_of(slabs);
+  const int64_t k = q.parts - 1 - at_grid.item;
+  if (k < 0) return;
   int64_t c0;
-  const uint32_t c = lane_offset<V>(blockIdx.x % slabs, p.channels, c0);
+  const uint32_t c = lane_offset<V>(at_grid.slab, p.channels, c0);
   int64_t r0, r1;
   part_range(p, q, k, r0, r1);
   if (r1 <= r0) return;
@@ -387,9 +414,11 @@ __global__ __launch_bounds__(512, kEarly && V == 2 ? 2 : 4) void logmel_scan_til
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
-  const int64_t item = blockIdx.x / slabs;
+  const Place at_grid = place_of(slabs);
+  const int64_t item = at_grid.item;
+  if (item >= (kParts ? q.parts : p.n_seq)) return;
   int64_t c0;
-  const uint32_t c = lane_offset<V>(blockIdx.x % slabs, p.channels, c0);
+  const uint32_t c = lane_offset<V>(at_grid.slab, p.channels, c0);
   const float* state = p.state ? p.state + c0 : nullptr;
   float bias[V], carry[V];
   load_bias<T, V>(bias, p.bias, c0, c);
@@ -527,14 +556,16 @@ __global__ __launch_bounds__(512, kEarly && V == 2 ? 2 : 4) void logmel_scan_til
 #pragma unroll
       for (int v = 0; v < V; ++v) carry[v] = apply(n.a[v], n.b[v], carry[v]);
     }
-    T* out_p = p.h + c0 + w0 * p.hs;
+    T* const out_h = p.h + c0;
+    int64_t out_at = w0 * p.hs;
     if (plain) {
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
         float h[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(P[i][v], in[v], H[i][v]);
-        row_store<T, V>(out_p + i * p.hs + c, h);
+        row_store<T, V>(out_h + out_at + c, h);
+        out_at = next_row(out_at, p.hs);
       }
     } else {
       Cursor k = first;
@@ -550,7 +581,7 @@ __global__ __launch_bounds__(512, kEarly && V == 2 ? 2 : 4) void logmel_scan_til
           float h[V];
 #pragma unroll
           for (int v = 0; v < V; ++v) h[v] = apply(P[i][v], H[i][v], in[v]);
-          row_store<T, V>(out_p + i * p.hs + c, h);
+          row_store<T, V>(out_h + t * p.hs + c, h);
           if (t + 1 == k.e && p.state_out)
             store_floats<V>(p.state_out + c0, k.j, p.channels, c, h);
         }
@@ -591,9 +622,11 @@ __global__ __launch_bounds__(512) void logmel_scan_back_parts_kernel(ScanArgs<T>
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
-  const int64_t k = blockIdx.x / slabs;
+  const Place at_grid = place_of(slabs);
+  const int64_t k = at_grid.item;
+  if (k >= q.parts) return;
   int64_t c0;
-  const uint32_t c = lane_offset<V>(blockIdx.x % slabs, p.channels, c0);
+  const uint32_t c = lane_offset<V>(at_grid.slab, p.channels, c0);
   int64_t r0, r1;
   part_range(p, q, k, r0, r1);
   if (r1 <= r0) return;
@@ -668,9 +701,11 @@ __global__ __launch_bounds__(512, 2) void logmel_scan_back_tiles_kernel(ScanArgs
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
-  const int64_t item = blockIdx.x / slabs;
+  const Place at_grid = place_of(slabs);
+  const int64_t item = at_grid.item;
+  if (item >= (kParts ? q.parts : p.n_seq)) return;
   int64_t c0;
-  const uint32_t c = lane_offset<V>(blockIdx.x % slabs, p.channels, c0);
+  const uint32_t c = lane_offset<V>(at_grid.slab, p.channels, c0);
   const float* state = p.state ? p.state + c0 : nullptr;
   const float* dstate_out = d.dstate_out ? d.dstate_out + c0 : nullptr;
   float* dstate = d.dstate ? d.dstate + c0 : nullptr;
@@ -819,6 +854,13 @@ __global__ __launch_bounds__(512, 2) void logmel_scan_back_tiles_kernel(ScanArgs
     fwd[buf].t[wave][lane] = f;
     rev[buf].t[wave][lane] = e;
     __syncthreads();
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        repack(raw.x[i]);
+        repack(raw.dh[i]);
+      }
+    }
     float h[V], E[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -845,8 +887,7 @@ __global__ __launch_bounds__(512, 2) void logmel_scan_back_tiles_kernel(ScanArgs
     float prev[kRun][V], part[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) part[v] = 0.0f;
-    T* dx_p = d.dx + c0 + w0 * d.dxs;
-    T* dg_p = d.dg + c0 + w0 * d.dgs;
+    int64_t dx_at = (w0 + kRun - 1) * d.dxs, dg_at = (w0 + kRun - 1) * d.dgs;
     auto forward_row = [&](int i) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -865,14 +906,21 @@ __global__ __launch_bounds__(512, 2) void logmel_scan_back_tiles_kernel(ScanArgs
         dg[v] = prev[i][v] * (u[i][v] * E[v]);
         part[v] += dg[v];
       }
-      row_store<T, V>(dx_p + i * d.dxs + c, dx);
-      row_store<T, V>(dg_p + i * d.dgs + c, dg);
+      row_store<T, V>(d.dx + c0 + dx_at + c, dx);
+      row_store<T, V>(d.dg + c0 + dg_at + c, dg);
+    };
+    auto row_up = [&] {
+      dx_at = next_row(dx_at, -d.dxs);
+      dg_at = next_row(dg_at, -d.dgs);
     };
     if (plain) {
 #pragma unroll
       for (int i = 0; i < kRun; ++i) forward_row(i);
 #pragma unroll
-      for (int i = kRun - 1; i >= 0; --i) backward_row(i);
+      for (int i = kRun - 1; i >= 0; --i) {
+        backward_row(i);
+        row_up();
+      }
     } else {
       k = at;
 #pragma unroll
@@ -893,6 +941,7 @@ __global__ __launch_bounds__(512, 2) void logmel_scan_back_tiles_kernel(ScanArgs
           backward_row(i);
           if (t == k.s && dstate) store_floats<V>(dstate, k.j, p.channels, c, E);
         }
+        row_up();
       }
     }
 #pragma unroll
@@ -980,6 +1029,10 @@ unsigned grid_of(int64_t blocks) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
 
+unsigned grid_for(int64_t items, int64_t slabs) {
+  return (unsigned)(ceil_div(items, 8) * 8 * slabs);
+}
+
 // How a call's rows are split over workgroups.
 struct Split {
   enum How { kSerial, kSequences, kParts } how;
@@ -1004,7 +1057,11 @@ struct Split {
 // whose first kernel only reads, one channel per lane is the faster (183
 // against 210 us).
 // The gradient reads three values and writes two where the call reads two and
-// writes one, and its first kernel reads two of them as well.
+// writes one, and its first kernel reads two of them as well. Its tiles hold
+// twice the registers, one workgroup a compute unit, so it has as many parts
+// as compute units, two channels per lane: 64 x 2998 x 128 bf16 89 us against
+// 108 with one channel per lane and twice the parts, 6 x 9000 x 1024 fp16 182
+// against 223.
 Split scan_split(const logmel_scan_input& in, int cus, bool backward) {
   Split s{};
   const int64_t longest = in.max_frames ? in.max_frames : in.rows;
@@ -1021,8 +1078,10 @@ Split scan_split(const logmel_scan_input& in, int cus, bool backward) {
   const double units = backward ? 5.0 : 3.0;
   const double once = units * size * (double)rows * (double)in.channels / 4.6e6;
   const double alone = units * (double)ceil_div(longest, kCk);
-  const int64_t part_slabs = ceil_div(in.channels, 64);
-  const int64_t part_rows = ceil_div(ceil_div(rows, kCk), ceil_div(2 * cus, part_slabs)) * kCk;
+  const int part_pairs = backward && in.channels > 1 ? 2 : 1;
+  const int64_t part_slabs = ceil_div(in.channels, 64 * part_pairs);
+  const int64_t want = ceil_div((backward ? 1 : 2) * cus, part_slabs);
+  const int64_t part_rows = ceil_div(ceil_div(rows, kCk), want) * kCk;
   const int64_t parts = ceil_div(rows, part_rows);
   // the first kernel reads the part of a sequence that runs on past a part
   const double mean = (double)rows / (double)(in.n_seq < 1 ? 1 : in.n_seq);
@@ -1033,7 +1092,7 @@ Split scan_split(const logmel_scan_input& in, int cus, bool backward) {
     return s;
   }
   s.how = Split::kParts;
-  s.pairs = 1;
+  s.pairs = part_pairs;
   s.slabs = part_slabs;
   s.part_rows = part_rows;
   s.parts = parts;
@@ -1062,13 +1121,13 @@ hipError_t launch_scan(const logmel_scan_input& in, void* h, int64_t h_stride, f
     else
       launch_scan_serial<T, 1>(p, stream);
   } else if (s.how == Split::kSequences) {
-    const unsigned grid = (unsigned)(in.n_seq * s.slabs);
+    const unsigned grid = grid_for(in.n_seq, s.slabs);
     if (s.pairs == 2)
       logmel_scan_tiles_kernel<T, 2, false, true><<<grid, 512, 0, stream>>>(p, q);
     else
       logmel_scan_tiles_kernel<T, 1, false, false><<<grid, 512, 0, stream>>>(p, q);
   } else {
-    const unsigned grid = (unsigned)(s.parts * s.slabs);
+    const unsigned grid = grid_for(s.parts, s.slabs);
     q.part_rows = s.part_rows;
     q.parts = s.parts;
     if (s.parts > 1) {
@@ -1119,21 +1178,27 @@ hipError_t launch_scan_backward(const logmel_scan_input& in, const float* checkp
   d.dstate = grad.d_dstate;
   PartArgs q{};
   if (s.how == Split::kSequences) {
-    const unsigned grid = (unsigned)(in.n_seq * s.slabs);
+    const unsigned grid = grid_for(in.n_seq, s.slabs);
     if (s.pairs == 2)
       logmel_scan_back_tiles_kernel<T, 2, false><<<grid, 512, 0, stream>>>(p, d, q);
     else
       logmel_scan_back_tiles_kernel<T, 1, false><<<grid, 512, 0, stream>>>(p, d, q);
   } else {
-    const unsigned grid = (unsigned)(s.parts * s.slabs);
+    const unsigned grid = grid_for(s.parts, s.slabs);
     q.part_rows = s.part_rows;
     q.parts = s.parts;
     if (s.parts > 1) {
       q.a = reinterpret_cast<float*>(static_cast<char*>(ws) + b.sums);
       q.b = q.a + s.parts * in.channels;
-      logmel_scan_back_parts_kernel<T, 1><<<grid, 512, 0, stream>>>(p, d, q);
+      if (s.pairs == 2)
+        logmel_scan_back_parts_kernel<T, 2><<<grid, 512, 0, stream>>>(p, d, q);
+      else
+        logmel_scan_back_parts_kernel<T, 1><<<grid, 512, 0, stream>>>(p, d, q);
     }
-    logmel_scan_back_tiles_kernel<T, 1, true><<<grid, 512, 0, stream>>>(p, d, q);
+    if (s.pairs == 2)
+      logmel_scan_back_tiles_kernel<T, 2, true><<<grid, 512, 0, stream>>>(p, d, q);
+    else
+      logmel_scan_back_tiles_kernel<T, 1, true><<<grid, 512, 0, stream>>>(p, d, q);
   }
   if (grad.d_dbias)
     return launch_part_sum(d.dbias_part, b.items, in.channels, grad.d_dbias, stream);
