@@ -968,9 +968,9 @@ __global__ __launch_bounds__(512, 2) void logmel_scan_back_tiles_kernel(ScanArgs
   }
 }
 
-// Sums over work items: 64 channels per workgroup; each of its 16 wavefronts
-// takes every sixteenth part, and the sixteen sums are added in order. Up to
-// three sums in one launch, one per blockIdx.y.
+// Sums over work items: 32 channels per workgroup, 32 lanes a channel, each
+// taking every 32nd part; the 32 sums are added in order. Up to three sums in
+// one launch, one per blockIdx.y.
 struct SumOut {
   PartSums s[3];
 };
@@ -979,29 +979,29 @@ template <typename T>
 __global__ __launch_bounds__(1024) void logmel_part_sum_kernel(const T* part, int64_t parts,
                                                                int64_t stride, int64_t channels,
                                                                SumOut o) {
-  __shared__ double sums[16][64];
+  __shared__ double sums[32][33];
   const PartSums k = o.s[blockIdx.y];
   if (!k.out) return;
   part += k.which * channels;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   double s = 0.0;
   if (c < channels) {
 #pragma unroll 8
-    for (int64_t g = wave; g < parts; g += 16) s += (double)part[g * stride + c];
+    for (int64_t g = row; g < parts; g += 32) s += (double)part[g * stride + c];
   }
-  sums[wave][lane] = s;
+  sums[row][lane] = s;
   __syncthreads();
-  if (wave == 0 && c < channels) {
+  if (row == 0 && c < channels) {
     double t = sums[0][lane];
-    for (int w = 1; w < 16; ++w) t += sums[w][lane];
+    for (int w = 1; w < 32; ++w) t += sums[w][lane];
     k.out[c] = (float)(k.factor ? t * (double)k.factor[c] : t);
   }
 }
 
 hipError_t launch_part_sum(const double* part, int64_t parts, int64_t channels, float* out,
                            hipStream_t stream) {
-  logmel_part_sum_kernel<<<(unsigned)((channels + 63) / 64), 1024, 0, stream>>>(
+  logmel_part_sum_kernel<<<(unsigned)((channels + 31) / 32), 1024, 0, stream>>>(
       part, parts, channels, channels, SumOut{{{out, 0, nullptr}}});
   return hipGetLastError();
 }
@@ -1209,7 +1209,7 @@ hipError_t launch_scan_backward(const logmel_scan_input& in, const float* checkp
 
 hipError_t logmel_launch_part_sums(const float* part, int64_t parts, int sums, int64_t channels,
                                    const PartSums out[3], hipStream_t stream) {
-  logmel::logmel_part_sum_kernel<<<dim3((unsigned)((channels + 63) / 64), 3), 1024, 0, stream>>>(
+  logmel::logmel_part_sum_kernel<<<dim3((unsigned)((channels + 31) / 32), 3), 1024, 0, stream>>>(
       part, parts, sums * channels, channels, logmel::SumOut{{out[0], out[1], out[2]}});
   return hipGetLastError();
 }
