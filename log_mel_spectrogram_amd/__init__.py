@@ -263,9 +263,15 @@ def logmel_plan_destroy(plan: Plan):
 
 # ----------------------------------------------------------- device glue
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev_ptr(t, dtype, what):
@@ -687,21 +693,29 @@ def _row_type(dtype):
     return t
 
 
+def _on_device(t, what, plan):
+    """The device a tensor argument is on must be the plan's."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{what} must be a torch tensor on a ROCm device")
+    if t.get_device() != plan.device:
+        raise ValueError(f"{what} must be on the plan's device {plan.device}, got {t.device}")
+
+
 def _rows(t, what, like, plan):
     """(address, row stride) of a row operand [rows, channels] like ``like``;
     (None, 0) for None."""
     if t is None:
         return None, 0
-    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
-        raise TypeError(f"{what} must be a torch tensor on a ROCm device")
+    # on the accepted path a single question; what is wrong is told apart after
+    if type(t) is not type(like) or t.get_device() != plan.device:
+        _on_device(t, what, plan)
     if t is not like:
         if t.dtype != like.dtype:
             raise TypeError(f"{what} must be {like.dtype}, got {t.dtype}")
         if t.shape != like.shape:
             raise ValueError(f"{what} must be [rows, channels] = {list(like.shape)}, "
                              f"got {list(t.shape)}")
-    if t.get_device() != plan.device:
-        raise ValueError(f"{what} must be on the plan's device {plan.device}, got {t.device}")
     strides = t.stride()
     if len(strides) != 2:
         raise ValueError(f"{what} must be [rows, channels], got {list(t.shape)}")
@@ -722,10 +736,8 @@ def _params(t, what, shape, plan):
     if t is None:
         return None
     torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{what} must be a torch tensor on a ROCm device")
-    if t.get_device() != plan.device:
-        raise ValueError(f"{what} must be on the plan's device {plan.device}, got {t.device}")
+    if type(t) is not torch.Tensor or t.get_device() != plan.device:
+        _on_device(t, what, plan)
     if t.dtype != torch.float32:
         raise TypeError(f"{what} must be torch.float32, got {t.dtype}")
     if t.shape != shape:
@@ -765,19 +777,18 @@ def _workspace(need, device, stream, what):
 
 def _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames):
     torch = _torch()
+    _on_device(x, "x", plan)
     ty = _row_type(x.dtype)
     px, sx = _rows(x, "x", x, plan)
     pg, sg = _rows(gate, "gate", x, plan)
     rows, channels = x.shape
-    if not isinstance(seq_offsets, torch.Tensor) or not seq_offsets.is_cuda:
-        raise TypeError("seq_offsets must be a torch tensor on a ROCm device")
+    if type(seq_offsets) is not torch.Tensor or seq_offsets.get_device() != plan.device:
+        _on_device(seq_offsets, "seq_offsets", plan)
     if seq_offsets.dtype != torch.int64:
         raise TypeError(f"seq_offsets must be torch.int64, got {seq_offsets.dtype}")
     n_seq = seq_offsets.numel() - 1
     if seq_offsets.dim() != 1 or n_seq < 0 or not seq_offsets.is_contiguous():
         raise ValueError("seq_offsets must be contiguous with n_seq + 1 entries")
-    if seq_offsets.get_device() != plan.device:
-        raise ValueError(f"seq_offsets must be on the plan's device {plan.device}")
     po = seq_offsets.data_ptr()
     return logmel_scan_input(ty, rows, channels, n_seq, po, int(max_frames), px, sx, pg, sg,
                              _params(bias, "bias", (channels,), plan),
@@ -847,6 +858,7 @@ def logmel_gated_scan_backward(plan: Plan, dh, x, gate, seq_offsets, checkpoints
 
 
 def _norm_input(plan, res, h, gate, w_post, scale, w_pre, eps):
+    _on_device(res, "res", plan)
     ty = _row_type(res.dtype)
     pr, sr = _rows(res, "res", res, plan)
     rows, channels = res.shape
