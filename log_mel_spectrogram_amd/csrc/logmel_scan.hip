@@ -41,15 +41,6 @@ struct ScanGradArgs {
   float* dstate;
 };
 
-// A lane's first channel: V channels per lane, the last lane of an odd width
-// shifted back so that its pair stays inside the row (both lanes then hold
-// that channel and write the same value).
-template <int V>
-__device__ __forceinline__ int64_t lane_channel(int64_t lane, int64_t channels) {
-  const int64_t c = lane * V;
-  return c + V > channels ? channels - V : c;
-}
-
 __device__ __forceinline__ void seq_range(const int64_t* off, int64_t j, int64_t rows, int64_t& s,
                                           int64_t& e) {
   s = off[j];
@@ -58,15 +49,17 @@ __device__ __forceinline__ void seq_range(const int64_t* off, int64_t j, int64_t
   e = e > rows ? rows : e;
 }
 
-// One lane per sequence and channel group, row after row.
+// One lane per sequence and V channels (V divides the width: no channel has
+// two lanes, of which one could write a state in place that the other has yet
+// to read), row after row.
 template <typename T, int V>
 __global__ void logmel_scan_serial_kernel(ScanArgs<T> p) {
-  const int64_t groups = (p.channels + V - 1) / V;
+  const int64_t groups = p.channels / V;
   const int64_t total = p.n_seq * groups;
   for (int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; id < total;
        id += (int64_t)gridDim.x * blockDim.x) {
     const int64_t j = id / groups;
-    const int64_t c = lane_channel<V>(id % groups, p.channels);
+    const int64_t c = id % groups * V;
     int64_t s, e;
     seq_range(p.off, j, p.rows, s, e);
     float h[V], b[V];
@@ -167,15 +160,8 @@ __device__ __forceinline__ Cursor cursor_find(const int64_t* off, int64_t n, int
   return k;
 }
 
-// The rows a work item owns: a whole sequence, or a part of the rows whatever
-// sequences it holds.
-struct Item {
-  int64_t r0, r1;   // r1 <= the end of the last sequence
-  Cursor at;        // the sequence of row r0
-};
-
-// Copies state to state_out for the sequences without rows among the items'
-// share: sequences [64 i, 64 i + 64) for item i, and so on in steps of all.
+// f(j) for the sequences without rows among a worker's share: sequences
+// [64 i, 64 i + 64) for worker i, and so on in steps of all workers.
 template <int V, typename F>
 __device__ __forceinline__ void for_empty(const int64_t* off, int64_t n, int64_t rows,
                                           int64_t worker, int64_t workers, F&& f) {
@@ -244,7 +230,8 @@ __device__ __forceinline__ void store_floats(float* p, int64_t row, int64_t chan
 
 // The workgroup's channels: a uniform first one, and each lane's offset from
 // it. The last lanes of a ragged slab hold the row's last V channels again
-// and write the same values.
+// and write the same values; with two channels per lane and one channel over
+// the slabs, the last slab holds one of the slab before as well.
 template <int V>
 __device__ __forceinline__ uint32_t lane_offset(int64_t slab, int64_t channels, int64_t& base) {
   base = slab * 64 * V;
@@ -333,6 +320,8 @@ __global__ __launch_bounds__(512) void logmel_scan_parts_kernel(ScanArgs<T> p, P
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
   const Place at_grid = place_of(slabs);
+  // from the last part down: the tiles start with the first, whose rows are
+  // then the latest read
   const int64_t k = q.parts - 1 - at_grid.item;
   if (k < 0) return;
   int64_t c0;
@@ -409,7 +398,8 @@ __global__ __launch_bounds__(512) void logmel_scan_parts_kernel(ScanArgs<T> p, P
 // from zero (H) and the product of its gates (P) stay in registers while the
 // wavefronts exchange their runs' Affine through LDS, then h = P carry + H.
 template <typename T, int V, bool kParts, bool kEarly>
-__global__ __launch_bounds__(512, kEarly && V == 2 ? 2 : 4) void logmel_scan_tiles_kernel(ScanArgs<T> p, PartArgs q) {
+__global__ __launch_bounds__(512, kEarly ? 2 : 4) void logmel_scan_tiles_kernel(
+    ScanArgs<T> p, PartArgs q) {
   __shared__ WaveTotals<V> lds[2];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1068,11 +1058,14 @@ Split scan_split(const logmel_scan_input& in, int cus, bool backward) {
   const int64_t rows = in.rows < 1 ? 1 : in.rows;
   if (longest <= 32 && !backward) {
     s.how = Split::kSerial;
-    s.pairs = in.channels > 1 ? 2 : 1;
+    s.pairs = in.channels % 2 ? 1 : 2;
     return s;
   }
   const int64_t pair_slabs = ceil_div(in.channels, 128);
-  s.pairs = in.channels > 1 && in.n_seq >= ceil_div(3 * cus, 4 * pair_slabs) ? 2 : 1;
+  // one channel over the slabs would be held by two workgroups, of which one
+  // could write the state in place that the other has yet to read
+  const bool shared = in.channels % 128 == 1 && !backward;
+  s.pairs = in.channels > 1 && !shared && in.n_seq >= ceil_div(3 * cus, 4 * pair_slabs) ? 2 : 1;
   s.slabs = ceil_div(in.channels, 64 * s.pairs);
   const double size = in.type == LOGMEL_F32 ? 4.0 : 2.0;
   const double units = backward ? 5.0 : 3.0;
@@ -1101,7 +1094,7 @@ Split scan_split(const logmel_scan_input& in, int cus, bool backward) {
 
 template <typename T, int V>
 void launch_scan_serial(const ScanArgs<T>& p, hipStream_t stream) {
-  const int64_t lanes = p.n_seq * ceil_div(p.channels, V);
+  const int64_t lanes = p.n_seq * (p.channels / V);
   logmel_scan_serial_kernel<T, V><<<grid_of(ceil_div(lanes, 256)), 256, 0, stream>>>(p);
 }
 

@@ -260,6 +260,29 @@ def test_scan_state_in_place_over_many_parts(env):
         assert torch.equal(h, again)
 
 
+@pytest.mark.parametrize("channels", [3, 65, 129, 257])
+def test_scan_state_in_place_odd_widths(env, channels):
+    """In place at widths where the last lanes, or the last workgroup, could
+    share a channel with others: one row to a few per sequence, and sequences
+    long enough for a workgroup each."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    for n, rows in ((700, 1), (333, 9), (200, 200)):
+        say(f"in place, {n} sequences of {rows} x {channels}")
+        off = torch.arange(n + 1, device=dev) * rows
+        gen = torch.Generator(device=dev).manual_seed(channels)
+        x, g = (torch.randn((n * rows, channels), generator=gen, device=dev).half()
+                for _ in range(2))
+        state = torch.randn((n, channels), generator=gen, device=dev)
+        apart = torch.empty_like(state)
+        h = lm.logmel_gated_scan(plan, x, g, off, state=state, state_out=apart, max_frames=rows)
+        for _ in range(3):
+            kept = state.clone()
+            h2 = lm.logmel_gated_scan(plan, x, g, off, state=kept, state_out=kept,
+                                      max_frames=rows)
+            assert torch.equal(h, h2) and torch.equal(apart, kept)
+
+
 def test_scan_gradient_repeats_bit_for_bit(env):
     lm, plan, torch = env
     dev = torch.device("cuda", 0)
