@@ -470,8 +470,9 @@ int logmel_gated_scan_backward(const logmel_plan* plan, const logmel_scan_input*
  * d_h NULL: y = res (the norm before a first block, as of log-mel rows).
  * d_gate NULL: no silu factor. d_w_post, d_scale, d_w_pre NULL: 1. gate,
  * w_post and scale without h are INVALID_ARGUMENT. channels 1..8192
- * (UNSUPPORTED beyond); eps a finite number >= 0 (a row of zeros with eps 0
- * gives NaN). */
+ * (UNSUPPORTED beyond); eps a finite number >= 0. Squares are fp32: a row whose
+ * mean square plus eps is 0 or below the smallest normal number gives NaN or
+ * infinities, one whose squares overflow a norm of 0. */
 #define LOGMEL_NORM_MAX_CHANNELS 8192
 typedef struct logmel_norm_input {
   int32_t type;

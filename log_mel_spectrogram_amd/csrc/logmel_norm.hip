@@ -57,6 +57,15 @@ struct NormGradArgs {
   float* part;   // [workgroups][2][channels]: sums of G n act and of dz y / rms(y); or null
 };
 
+// 1 / sqrt(m): the hardware's estimate (one ulp) and one Newton step, a third
+// of the instructions of a square root and a division, which two or three
+// times a row are as many as four of its values take. Infinity gives 0.
+__device__ __forceinline__ float inv_root(float m) {
+  const float r = __builtin_amdgcn_rsqf(m);
+  const float e = __builtin_fmaf(-m * r, r, 1.0f);
+  return m < __builtin_inff() ? __builtin_fmaf(0.5f * r, e, r) : r;
+}
+
 // What stands between res and y.
 enum Parts { kNone, kNorm, kGated };
 
@@ -289,7 +298,7 @@ __global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_
     if (first + step < p.rows) load(r + step);
     if constexpr (kParts != kNone) {
       sum(s1);
-      const float r1 = 1.0f / __builtin_sqrtf(__builtin_fmaf(s1, inv, p.eps));
+      const float r1 = inv_root(__builtin_fmaf(s1, inv, p.eps));
 #pragma unroll
       for (int j = 0; j < kVecs; ++j)
 #pragma unroll
@@ -304,7 +313,7 @@ __global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_
         for (int i = 0; i < V; ++i)
           s2 = k.counts(j, i) ? __builtin_fmaf(y[j][i], y[j][i], s2) : s2;
       sum(s2);
-      const float r2 = 1.0f / __builtin_sqrtf(__builtin_fmaf(s2, inv, p.eps));
+      const float r2 = inv_root(__builtin_fmaf(s2, inv, p.eps));
 #pragma unroll
       for (int j = 0; j < kVecs; ++j)
 #pragma unroll
@@ -364,7 +373,7 @@ __global__ __launch_bounds__(kThreads<kLanes>,
         for (int i = 0; i < V; ++i)
           s1 = k.counts(j, i) ? __builtin_fmaf(h.at(j, i), h.at(j, i), s1) : s1;
       sum(s1);
-      r1 = 1.0f / __builtin_sqrtf(__builtin_fmaf(s1, inv, p.eps));
+      r1 = inv_root(__builtin_fmaf(s1, inv, p.eps));
       h.unpack_anew();
     }
     // silu(gate), formed again wherever it is needed
@@ -387,7 +396,7 @@ __global__ __launch_bounds__(kThreads<kLanes>,
     float r2 = 0.0f, k2 = 0.0f;
     if (q.dz) {
       sum(s2, m2, true);
-      r2 = 1.0f / __builtin_sqrtf(__builtin_fmaf(s2, inv, p.eps));
+      r2 = inv_root(__builtin_fmaf(s2, inv, p.eps));
       k2 = r2 * r2 * (m2 * inv);
       dz.unpack_anew();
     }
