@@ -225,10 +225,20 @@ template <int kLanes, int kVecs, int V>
 __device__ __forceinline__ void load_params(float (&r)[kVecs][V], const float* p,
                                             const Channels<kLanes, kVecs, V>& k) {
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j)
+  for (int j = 0; j < kVecs; ++j) {
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      r[j][i] = p && k.on[j] && k.c[j] + i < k.C ? p[k.c[j] + i] : 1.0f;
+    for (int i = 0; i < V; ++i) r[j][i] = 1.0f;
+    if (!p || !k.on[j]) continue;
+    if (k.C >= V) {
+      const auto v = row_load<float, V>(p + k.c[j]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) r[j][i] = v.v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i < k.C) r[j][i] = p[i];
+    }
+  }
 }
 
 // w_post scale, the two factors of t that do not depend on the row.
@@ -262,9 +272,6 @@ __global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_
   RowSum<kLanes> sum{slots};
   const typename P::Ch k(p.channels);
   const float inv = 1.0f / (float)p.channels;
-  float w1[kVecs][V], w2[kVecs][V];
-  if constexpr (kParts != kNone) load_block_params(w1, p, k);
-  load_params(w2, p.w_pre, k);
   const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t r = (int64_t)blockIdx.x * kRows + group_of<kLanes>();
   P res, h, o;
@@ -274,7 +281,10 @@ __global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_
     if constexpr (kParts != kNone) h.load(p.h + row * p.hs, k, on);
     if constexpr (kParts == kGated) o.load(p.o + row * p.os, k, on);
   };
-  load(r);
+  load(r);   // on its way before the parameters are waited for
+  float w1[kVecs][V], w2[kVecs][V];
+  if constexpr (kParts != kNone) load_block_params(w1, p, k);
+  load_params(w2, p.w_pre, k);
   // the workgroup's rows together: barriers are met by all of it
   for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.rows; first += step, r += step) {
     float y[kVecs][V], t[kVecs][V];
@@ -347,14 +357,14 @@ __global__ __launch_bounds__(kThreads<kLanes>,
   const float inv = 1.0f / (float)p.channels;
   float w1[kVecs][V], w2[kVecs][V];
   float a1[kVecs][V], a2[kVecs][V];
-  if constexpr (kParts != kNone) load_block_params(w1, p, k);
-  load_params(w2, p.w_pre, k);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) a1[j][i] = a2[j][i] = 0.0f;
   const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t r = (int64_t)blockIdx.x * kRows + group_of<kLanes>();
+  if constexpr (kParts != kNone) load_block_params(w1, p, k);
+  load_params(w2, p.w_pre, k);
   for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.rows; first += step, r += step) {
     P res, h, o, dy, dz;
     const bool on = r < p.rows;
