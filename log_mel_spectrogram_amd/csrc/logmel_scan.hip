@@ -3,6 +3,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
 #include <type_traits>
 
 #include "logmel_rows.h"
@@ -53,7 +54,7 @@ __device__ __forceinline__ void seq_range(const int64_t* off, int64_t j, int64_t
 // two lanes, of which one could write a state in place that the other has yet
 // to read), row after row.
 template <typename T, int V>
-__global__ void logmel_scan_serial_kernel(ScanArgs<T> p) {
+__global__ void logmel_scan_lanes_kernel(ScanArgs<T> p) {
   const int64_t groups = p.channels / V;
   const int64_t total = p.n_seq * groups;
   for (int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; id < total;
@@ -68,16 +69,29 @@ __global__ void logmel_scan_serial_kernel(ScanArgs<T> p) {
       h[v] = p.state ? p.state[j * p.channels + c + v] : 0.0f;
       b[v] = Gate<T>::bias_of(p.bias ? p.bias[c + v] : 0.0f);
     }
-    // rows in batches, a batch read before its first use
+    // rows in batches, the next one on its way while one is worked
     constexpr int kBatch = 8;
-    for (int64_t t0 = s; t0 < e; t0 += kBatch) {
-      Packed<T, V> x[kBatch], g[kBatch];
+    Packed<T, V> x[kBatch], g[kBatch];
+    auto load = [&](int64_t t0) {
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
         if (t0 + i < e) {
           x[i] = row_load<T, V>(p.x + (t0 + i) * p.xs + c);
           g[i] = row_load<T, V>(p.g + (t0 + i) * p.gs + c);
         }
+    };
+    load(s);
+    for (int64_t t0 = s; t0 < e; t0 += kBatch) {
+      float a[kBatch][V], ux[kBatch][V];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float u;
+          Gate<T>::pair((float)g[i].v[v], b[v], a[i][v], u);
+          ux[i][v] = u * (float)x[i].v[v];
+        }
+      load(t0 + kBatch);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int64_t t = t0 + i;
@@ -87,11 +101,7 @@ __global__ void logmel_scan_serial_kernel(ScanArgs<T> p) {
           for (int v = 0; v < V; ++v) p.ck[t / kCk * p.channels + c + v] = h[v];
         }
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float a, u;
-          Gate<T>::pair((float)g[i].v[v], b[v], a, u);
-          h[v] = __builtin_fmaf(a, h[v], u * (float)x[i].v[v]);
-        }
+        for (int v = 0; v < V; ++v) h[v] = __builtin_fmaf(a[i][v], h[v], ux[i][v]);
         row_store<T, V>(p.h + t * p.hs + c, h);
       }
     }
@@ -241,19 +251,22 @@ __device__ __forceinline__ uint32_t lane_offset(int64_t slab, int64_t channels, 
   return (uint32_t)(c < most ? c : most);
 }
 
-// A workgroup's item and slab. Workgroups go to the 8 dies in turn, so the
-// slabs of one item are 8 apart: the ends of unaligned row pieces, which two
-// slabs share, meet in one die's L2.
+// A workgroup's item and slab. Workgroups go to the 8 dies in turn; by_die,
+// the slabs of one item are 8 apart, so that the ends of unaligned row pieces,
+// which two slabs share, meet in one die's L2 (24 x 2917 x 257 fp16 55 us, 70
+// with the slabs side by side).
 struct Place {
   int64_t item, slab;
 };
 
-__device__ __forceinline__ Place place_of(int64_t slabs) {
+__device__ __forceinline__ Place place_of(int64_t slabs, bool by_die) {
   const int64_t b = blockIdx.x;
-  return {b / (8 * slabs) * 8 + b % 8, b / 8 % slabs};
+  if (by_die) return {b / (8 * slabs) * 8 + b % 8, b / 8 % slabs};
+  return {b / slabs, b % slabs};
 }
 
 struct PartArgs {
+  bool by_die;
   int64_t part_rows;   // a multiple of kCk
   int64_t parts;
   float* a;            // [parts][channels]: the part's Affine out of its first or last row
@@ -319,7 +332,7 @@ __global__ __launch_bounds__(512) void logmel_scan_parts_kernel(ScanArgs<T> p, P
   __shared__ WaveTotals<V> lds;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
-  const Place at_grid = place_of(slabs);
+  const Place at_grid = place_of(slabs, q.by_die);
   // from the last part down: the tiles start with the first, whose rows are
   // then the latest read
   const int64_t k = q.parts - 1 - at_grid.item;
@@ -404,7 +417,7 @@ __global__ __launch_bounds__(512, kEarly ? 2 : 4) void logmel_scan_tiles_kernel(
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
-  const Place at_grid = place_of(slabs);
+  const Place at_grid = place_of(slabs, q.by_die);
   const int64_t item = at_grid.item;
   if (item >= (kParts ? q.parts : p.n_seq)) return;
   int64_t c0;
@@ -612,7 +625,7 @@ __global__ __launch_bounds__(512) void logmel_scan_back_parts_kernel(ScanArgs<T>
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
-  const Place at_grid = place_of(slabs);
+  const Place at_grid = place_of(slabs, q.by_die);
   const int64_t k = at_grid.item;
   if (k >= q.parts) return;
   int64_t c0;
@@ -691,7 +704,7 @@ __global__ __launch_bounds__(512, 2) void logmel_scan_back_tiles_kernel(ScanArgs
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t slabs = (p.channels + 64 * V - 1) / (64 * V);
-  const Place at_grid = place_of(slabs);
+  const Place at_grid = place_of(slabs, q.by_die);
   const int64_t item = at_grid.item;
   if (item >= (kParts ? q.parts : p.n_seq)) return;
   int64_t c0;
@@ -1019,83 +1032,120 @@ unsigned grid_of(int64_t blocks) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
 
+// Whether a die each for 8 items in turn leaves none of them much behind.
+bool by_die(int64_t items) { return ceil_div(items, 8) * 8 <= items + items / 8; }
+
 unsigned grid_for(int64_t items, int64_t slabs) {
-  return (unsigned)(ceil_div(items, 8) * 8 * slabs);
+  return (unsigned)((by_die(items) ? ceil_div(items, 8) * 8 : items) * slabs);
 }
 
 // How a call's rows are split over workgroups.
 struct Split {
-  enum How { kSerial, kSequences, kParts } how;
+  enum How { kLanes, kSequences, kParts } how;
   int pairs;          // channels per lane
   int64_t slabs;      // of 64 pairs channels
   int64_t part_rows, parts;
 };
 
-// Which way is the fastest follows from three figures, in us on this card:
-// the rate of a call that reads and writes each value once (4.6 TB/s over the
-// bytes, 3 per value and byte of its type), the time one workgroup takes for a
-// tile (3, its wavefronts' instructions), and a launch (6). Measured, the way
-// taken first: 512 sequences of 32 rows x 512 bf16 in one lane each 16 us,
-// tiles 22 (of 64 rows 48 and 35, so lanes up to 32 rows); 64 x 2998 x 512
-// bf16 by sequences 128 us, in parts 183; 64 x 2998 x 128 in parts 64 us, by
-// sequences 75; 8 x 2998 x 512 in parts 37, by sequences 61; 16 x 375 x 512
-// fp32 by sequences 20, in parts 25.
-// Two channels per lane halve the memory instructions, with one tile more in
-// flight than fits 128 registers (64 x 2998 x 512 bf16 128 against 140 us,
-// fp32 231 against 250), but need workgroups for most compute units: with 64
-// of them (128 channels) one channel per lane takes 75 us, two 99. In parts,
-// whose first kernel only reads, one channel per lane is the faster (183
-// against 210 us).
-// The gradient reads three values and writes two where the call reads two and
-// writes one, and its first kernel reads two of them as well. Its tiles hold
-// twice the registers, one workgroup a compute unit, so it has as many parts
-// as compute units, two channels per lane: 64 x 2998 x 128 bf16 89 us against
-// 108 with one channel per lane and twice the parts, 6 x 9000 x 1024 fp16 182
-// against 223.
+// Which way is the fastest follows from the sizes and a few times measured on
+// this card, in us:
+//  - once: each value read or written once, 4.6 TB/s over the bytes (3 values
+//    of the type per row and channel, 5 in the gradient);
+//  - a row of a lane that walks a sequence alone: 0.2 (2-byte rows), 0.35;
+//  - a tile: 3 for a workgroup on an idle card, whose longest sequence sets
+//    the least time of a split by sequences (6 in the gradient); 5 where the
+//    compute units are full, with one workgroup of two channels per lane or
+//    two of one channel per lane each (8 and 6 in the gradient, one workgroup
+//    a compute unit in either). A sequence of L rows touches
+//    (L + 127) / 128 tiles on average;
+//  - in parts, the first kernel reads two values per row and channel again of
+//    each sequence that runs on past its part, and costs a launch, 6; a tile
+//    with a sequence's end in it takes up to 1.4 times as long, and the lanes
+//    past a width's end cost what the others do.
+// Measured, the way taken first: 512 sequences of 128 rows x 512 bf16 one lane
+// each 44, by sequences 59, in parts 75; 64 of them by sequences 10, one lane
+// each 27; 64 x 2998 x 512 by sequences 126, in parts 183; 64 x 2998 x 128 in
+// parts 60, by sequences 67; 8 x 2998 x 512 in parts 32, by sequences 61.
+// Gradient: 64 x 2998 x 512 by sequences 228, in parts 258; 2000 x 100 x 100
+// fp32 in parts 130, by sequences 215; 64 x 2998 x 128 in parts 90, by
+// sequences 149.
+// Two channels per lane halve the memory instructions (64 x 2998 x 512 bf16
+// 126 against 140 with one, fp32 231 against 250), but need workgroups for
+// most compute units (64 x 2998 x 128: 99 against 75) and most of their lanes.
+// In parts, whose first kernel only reads, one channel per lane is the faster
+// (64 x 2998 x 512 183 against 210); in the gradient's, whose tiles hold twice
+// the registers, two and as many parts as compute units (64 x 2998 x 128 bf16
+// 89 against 108 with one and twice the parts, 6 x 9000 x 1024 fp16 182 against
+// 223).
 Split scan_split(const logmel_scan_input& in, int cus, bool backward) {
   Split s{};
   const int64_t longest = in.max_frames ? in.max_frames : in.rows;
   const int64_t rows = in.rows < 1 ? 1 : in.rows;
-  if (longest <= 32 && !backward) {
-    s.how = Split::kSerial;
-    s.pairs = in.channels % 2 ? 1 : 2;
-    return s;
-  }
-  const int64_t pair_slabs = ceil_div(in.channels, 128);
-  // one channel over the slabs would be held by two workgroups, of which one
-  // could write the state in place that the other has yet to read
-  const bool shared = in.channels % 128 == 1 && !backward;
-  s.pairs = in.channels > 1 && !shared && in.n_seq >= ceil_div(3 * cus, 4 * pair_slabs) ? 2 : 1;
-  s.slabs = ceil_div(in.channels, 64 * s.pairs);
-  const double size = in.type == LOGMEL_F32 ? 4.0 : 2.0;
+  const double mean = (double)rows / (double)(in.n_seq < 1 ? 1 : in.n_seq);
   const double units = backward ? 5.0 : 3.0;
+  const double size = in.type == LOGMEL_F32 ? 4.0 : 2.0;
   const double once = units * size * (double)rows * (double)in.channels / 4.6e6;
-  const double alone = units * (double)ceil_div(longest, kCk);
+
+  // by sequences
+  const int64_t pair_slabs = ceil_div(in.channels, 128);
+  const int64_t over = in.channels % 128;
+  // the gradient may share a channel over the slabs between two workgroups;
+  // in a call, one could write the state in place that the other has yet to
+  // read
+  const bool pairs = in.channels > 1 && (over == 0 || over > 64 || (backward && pair_slabs > 2)) &&
+                     in.n_seq >= ceil_div(3 * cus, 4 * pair_slabs);
+  const int64_t slabs = ceil_div(in.channels, pairs ? 128 : 64);
+  const bool too_many = in.n_seq > (int64_t(1) << 30) / slabs;   // workgroups
+  const int64_t groups = too_many ? 0 : in.n_seq * slabs;
+  const int64_t slots = !backward && !pairs ? 2 * cus : cus;
+  const double tile = backward ? (pairs ? 8.0 : 6.0) : !pairs && groups <= cus ? 3.0 : 5.0;
+  const double full = (double)ceil_div(groups, slots) * (mean + 127.0) / 128.0 * tile;
+  const double alone = (backward ? 6.0 : 3.0) * (double)ceil_div(longest, kCk);
+  double by_sequences = once > alone ? once : alone;
+  if (full > by_sequences) by_sequences = full;
+  if (too_many) by_sequences = HUGE_VAL;
+
+  // in parts
   const int part_pairs = backward && in.channels > 1 ? 2 : 1;
   const int64_t part_slabs = ceil_div(in.channels, 64 * part_pairs);
-  const int64_t want = ceil_div((backward ? 1 : 2) * cus, part_slabs);
+  // as many as the compute units hold, of every die
+  int64_t want = (backward ? 1 : 2) * cus / part_slabs;
+  want = want >= 8 ? want / 8 * 8 : want < 1 ? 1 : want;
   const int64_t part_rows = ceil_div(ceil_div(rows, kCk), want) * kCk;
   const int64_t parts = ceil_div(rows, part_rows);
-  // the first kernel reads the part of a sequence that runs on past a part
-  const double mean = (double)rows / (double)(in.n_seq < 1 ? 1 : in.n_seq);
   const double again = mean >= 2.0 * part_rows ? 1.0 : mean / (2.0 * part_rows);
-  const double in_parts = once * (1.0 + again * 2.0 / units) + (parts > 1 ? 6.0 : 0.0);
-  if (in_parts >= (once > alone ? once : alone) && in.n_seq <= (int64_t(1) << 30) / s.slabs) {
+  const double lanes = (double)(part_slabs * 64 * part_pairs) / (double)in.channels;
+  double in_parts = once * lanes * (1.0 + again * 2.0 / units) *
+                    (1.0 + 0.4 * (mean > 128.0 ? 128.0 / mean : 1.0));
+  const double walk = (backward ? 6.0 : 3.0) * (double)(part_rows / kCk);
+  if (walk > in_parts) in_parts = walk;
+  if (parts > 1) in_parts += 6.0;
+
+  // one lane each
+  const double rowwise = (size == 4.0 ? 0.35 : 0.2) * (double)longest;
+  const double in_lanes = rowwise > once ? rowwise : once;
+
+  if (!backward && in_lanes <= by_sequences && in_lanes <= in_parts) {
+    s.how = Split::kLanes;
+    s.pairs = in.channels % 2 ? 1 : 2;
+  } else if (by_sequences <= in_parts) {
     s.how = Split::kSequences;
-    return s;
+    s.pairs = pairs ? 2 : 1;
+    s.slabs = slabs;
+  } else {
+    s.how = Split::kParts;
+    s.pairs = part_pairs;
+    s.slabs = part_slabs;
+    s.part_rows = part_rows;
+    s.parts = parts;
   }
-  s.how = Split::kParts;
-  s.pairs = part_pairs;
-  s.slabs = part_slabs;
-  s.part_rows = part_rows;
-  s.parts = parts;
   return s;
 }
 
 template <typename T, int V>
-void launch_scan_serial(const ScanArgs<T>& p, hipStream_t stream) {
+void launch_scan_lanes(const ScanArgs<T>& p, hipStream_t stream) {
   const int64_t lanes = p.n_seq * (p.channels / V);
-  logmel_scan_serial_kernel<T, V><<<grid_of(ceil_div(lanes, 256)), 256, 0, stream>>>(p);
+  logmel_scan_lanes_kernel<T, V><<<grid_of(ceil_div(lanes, 256)), 256, 0, stream>>>(p);
 }
 
 template <typename T>
@@ -1108,19 +1158,21 @@ hipError_t launch_scan(const logmel_scan_input& in, void* h, int64_t h_stride, f
   p.ck = checkpoints;
   const Split s = scan_split(in, cus, false);
   PartArgs q{};
-  if (s.how == Split::kSerial) {
+  if (s.how == Split::kLanes) {
     if (s.pairs == 2)
-      launch_scan_serial<T, 2>(p, stream);
+      launch_scan_lanes<T, 2>(p, stream);
     else
-      launch_scan_serial<T, 1>(p, stream);
+      launch_scan_lanes<T, 1>(p, stream);
   } else if (s.how == Split::kSequences) {
     const unsigned grid = grid_for(in.n_seq, s.slabs);
+    q.by_die = by_die(in.n_seq);
     if (s.pairs == 2)
       logmel_scan_tiles_kernel<T, 2, false, true><<<grid, 512, 0, stream>>>(p, q);
     else
       logmel_scan_tiles_kernel<T, 1, false, false><<<grid, 512, 0, stream>>>(p, q);
   } else {
     const unsigned grid = grid_for(s.parts, s.slabs);
+    q.by_die = by_die(s.parts);
     q.part_rows = s.part_rows;
     q.parts = s.parts;
     if (s.parts > 1) {
@@ -1172,12 +1224,14 @@ hipError_t launch_scan_backward(const logmel_scan_input& in, const float* checkp
   PartArgs q{};
   if (s.how == Split::kSequences) {
     const unsigned grid = grid_for(in.n_seq, s.slabs);
+    q.by_die = by_die(in.n_seq);
     if (s.pairs == 2)
       logmel_scan_back_tiles_kernel<T, 2, false><<<grid, 512, 0, stream>>>(p, d, q);
     else
       logmel_scan_back_tiles_kernel<T, 1, false><<<grid, 512, 0, stream>>>(p, d, q);
   } else {
     const unsigned grid = grid_for(s.parts, s.slabs);
+    q.by_die = by_die(s.parts);
     q.part_rows = s.part_rows;
     q.parts = s.parts;
     if (s.parts > 1) {
