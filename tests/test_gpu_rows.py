@@ -705,3 +705,41 @@ def test_binding_refuses(env):
         lm.logmel_block_norm_backward(plan, x)
     with pytest.raises(TypeError):
         lm.logmel_block_norm(plan, x, w_pre=torch.ones(8, device=dev).half())
+
+
+def test_rows_past_2_31(env):
+    """More than 2^31 rows of one channel: states by the closed form of a
+    constant gate (a = 1/2, x = 1: h_t = 1 - 2^-(t+1) from a sequence's first
+    row), gradients by that of a constant dh, and the norm of one channel."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    first = 2 ** 31 + 77
+    rows = first + 1001
+    say(f"{rows} rows x 1")
+    off = torch.tensor([0, first, rows], device=dev)
+    x = torch.ones((rows, 1), dtype=torch.float16, device=dev)
+    g = torch.zeros((rows, 1), dtype=torch.float16, device=dev)
+    ck = torch.empty((lm.logmel_gated_scan_checkpoint_rows(rows), 1), device=dev)
+    so = torch.empty((2, 1), device=dev)
+    h = lm.logmel_gated_scan(plan, x, g, off, state_out=so, checkpoints=ck)
+    # exact: every h is a multiple of 2^-11 or rounds to 1
+    t = torch.arange(40, device=dev).double()
+    want = (1.0 - 0.5 ** (t + 1)).half().unsqueeze(1)
+    for start in (0, first):
+        assert torch.equal(h[start:start + 40], want)
+    assert (h[40:first] == 1.0).all() and (h[first + 40:] == 1.0).all()
+    assert torch.equal(so, torch.ones_like(so))
+    say("gradient")
+    dx, dg, _, _ = lm.logmel_gated_scan_backward(plan, x, x, g, off, ck)
+    # D_t = 2 - 2^-(last - t): dx = D / 2; dg = (h_{t-1} - 1) D / 4
+    for start, end in ((0, first), (first, rows)):
+        assert torch.equal(dx[end - 40:end].flip(0), want)
+        assert (dx[start:end - 40] == 1.0).all()
+        head = (-(0.5 ** t) * 2.0 / 4.0).half().unsqueeze(1)
+        assert torch.allclose(dg[start:start + 20], head[:20], rtol=2.0 ** -10, atol=0.0)
+    del dx, dg, ck
+    say("norm")
+    _, z = lm.logmel_block_norm(plan, x, eps=0.0)
+    assert (z == 1.0).all()
+    del h, z, x, g
+    torch.cuda.empty_cache()
