@@ -445,8 +445,9 @@ int logmel_gated_scan(const logmel_plan* plan, const logmel_scan_input* in, void
  *     rows,  dstate = a_0 D_0 (of an empty sequence: its row of dstate_out).
  *   d_checkpoints  what the forward call wrote; the states between are
  *                  formed anew from x and gate
- *   d_dx, d_dgate  row outputs; d_dbias [channels] and d_dstate
- *                  [n_seq][channels] may be NULL. */
+ *   d_dx, d_dgate  row outputs
+ *   d_dbias        [channels], or NULL; NULL where d_bias is
+ *   d_dstate       [n_seq][channels], or NULL */
 typedef struct logmel_scan_grad {
   const void* d_dh;
   int64_t dh_stride;

@@ -208,6 +208,8 @@ int logmel_gated_scan_backward(const logmel_plan* plan, const logmel_scan_input*
   if (o.status()) return o.status();
   const int64_t need = logmel_scan_workspace(*in, 1, cus_of(plan));
   if (!d_checkpoints && in->rows && in->n_seq) return LOGMEL_ERR_INVALID_ARGUMENT;
+  // the sums of a bias that is not there have no place in the workspace
+  if (grad->d_dbias && !in->d_bias) return LOGMEL_ERR_INVALID_ARGUMENT;
   o.floats(d_checkpoints, checkpoint_rows(in->rows), false);
   o.row(grad->d_dh, grad->dh_stride, false, in->n_seq > 0);
   o.floats(grad->d_dstate_out, in->n_seq, false);

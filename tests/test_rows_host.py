@@ -182,6 +182,11 @@ def test_scan_backward_refuses(lm):
     assert call(wsb=4) == bad
     assert call(ws=0x400004) == bad
     assert call(ws=0x310000) == bad     # workspace in dx
+    # the gradient of a bias that is not there
+    grad = lm.logmel_scan_grad(**fine, d_dbias=0x710000)
+    for n_seq in (0, 2):
+        assert lm._gated_scan_backward(FAKE, _scan_in(lm, n_seq=n_seq), 0x500000, grad, 0x400000,
+                                       1 << 30, None) == bad
 
 
 def _norm_in(lm, **kw):
