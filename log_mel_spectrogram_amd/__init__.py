@@ -905,12 +905,14 @@ def logmel_block_norm_backward(plan: Plan, res, h=None, gate=None, w_post=None, 
             return t
         return _empty(res.shape, res.dtype, res.device, stream)
 
-    def param(of):
-        return None if of is None else _empty(of.shape, of.dtype, res.device, stream)
-
-    out = dict(dres=rows(dres, res), dh=rows(dh, h), dgate=rows(dgate, gate),
-               dw_post=param(w_post), dscale=param(scale),
-               dw_pre=None if dz is None else param(w_pre))
+    # the parameters' gradients are rows of one tensor
+    wanted = [k for k, of in (("dw_post", w_post), ("dscale", scale),
+                              ("dw_pre", None if dz is None else w_pre)) if of is not None]
+    params = dict.fromkeys(("dw_post", "dscale", "dw_pre"))
+    if wanted:
+        flat = _empty((len(wanted), inp.channels), _torch().float32, res.device, stream)
+        params.update(zip(wanted, flat.unbind(0)))
+    out = dict(dres=rows(dres, res), dh=rows(dh, h), dgate=rows(dgate, gate), **params)
     ptrs = []
     for t, what in ((dy, "dy"), (dz, "dz"), (out["dres"], "dres"), (out["dh"], "dh"),
                     (out["dgate"], "dgate")):

@@ -50,6 +50,7 @@ struct ScanGradArgs {
   T* dg;
   int64_t dgs;
   double* dbias_part;   // [work items][channels], or null
+  float* dbias;         // where there is one work item, its sums themselves; or null
   float* dstate;
 };
 
@@ -984,7 +985,7 @@ __global__ __launch_bounds__(512, 2) void logmel_scan_back_tiles_kernel(ScanArgs
     load(raw, tile);
     for (int buf = 0; tile + kCk > r0; buf ^= 1) one_tile(raw, buf);
   }
-  if (!d.dbias_part) return;
+  if (!d.dbias_part && !d.dbias) return;
 #pragma unroll
   for (int v = 0; v < V; ++v) sums[wave][lane][v] = db[v];
   __syncthreads();
@@ -993,7 +994,10 @@ __global__ __launch_bounds__(512, 2) void logmel_scan_back_tiles_kernel(ScanArgs
     for (int v = 0; v < V; ++v) {
       double s = 0.0;
       for (int w = 0; w < kWaves; ++w) s += sums[w][lane][v];
-      d.dbias_part[item * p.channels + c0 + c + v] = s;
+      if (d.dbias)
+        d.dbias[c0 + c + v] = (float)s;
+      else
+        d.dbias_part[item * p.channels + c0 + c + v] = s;
     }
   }
 }
@@ -1222,7 +1226,7 @@ struct BackSpace {
 BackSpace back_space(const logmel_scan_input& in, const Split& s) {
   BackSpace b;
   b.items = s.how == Split::kParts ? s.parts : in.n_seq;
-  b.sums = in.d_bias ? b.items * in.channels * 8 : 0;
+  b.sums = in.d_bias && b.items > 1 ? b.items * in.channels * 8 : 0;
   b.affine = s.how == Split::kParts && s.parts > 1 ? 2 * s.parts * in.channels * 4 : 0;
   b.bytes = b.sums + b.affine;
   return b;
@@ -1246,7 +1250,10 @@ hipError_t launch_scan_backward(const logmel_scan_input& in, const float* checkp
   d.dxs = grad.dx_stride;
   d.dg = static_cast<T*>(grad.d_dgate);
   d.dgs = grad.dgate_stride;
-  d.dbias_part = grad.d_dbias ? static_cast<double*>(ws) : nullptr;
+  if (b.items == 1)
+    d.dbias = grad.d_dbias;
+  else if (grad.d_dbias)
+    d.dbias_part = static_cast<double*>(ws);
   d.dstate = grad.d_dstate;
   PartArgs q{};
   if (s.how == Split::kSequences) {
@@ -1274,7 +1281,7 @@ hipError_t launch_scan_backward(const logmel_scan_input& in, const float* checkp
     else
       logmel_scan_back_tiles_kernel<T, 1, true><<<grid, 512, 0, stream>>>(p, d, q);
   }
-  if (grad.d_dbias)
+  if (d.dbias_part)
     return launch_part_sum(d.dbias_part, b.items, in.channels, grad.d_dbias, stream);
   return hipGetLastError();
 }

@@ -166,12 +166,14 @@ def test_scan_refuses_overlap(lm):
 
 def test_scan_backward_refuses(lm):
     bad = lm.LOGMEL_ERR_INVALID_ARGUMENT
-    fine = dict(d_dh=0x300000, dh_stride=8, d_dx=0x310000, dx_stride=8, d_dgate=0x320000,
+    fine = dict(d_dh=0x300000, dh_stride=8, d_dx=0x340000, dx_stride=8, d_dgate=0x380000,
                 dgate_stride=8)
 
-    def call(ck=0x500000, ws=0x400000, wsb=1 << 30, **kw):
-        # with a bias there are its gradient's sums to hold, so workspace is needed
-        return lm._gated_scan_backward(FAKE, _scan_in(lm, d_bias=0x700000), ck,
+    def call(ck=0x500000, ws=0x800000, wsb=1 << 30, **kw):
+        # rows enough for several work items, whose sums of a bias's gradient
+        # (and of the parts they are) need workspace
+        inp = _scan_in(lm, rows=5000, d_bias=0x700000, d_x=0x1000000, d_gate=0x1100000)
+        return lm._gated_scan_backward(FAKE, inp, ck,
                                        lm.logmel_scan_grad(**{**fine, **kw}), ws, wsb, None)
 
     assert call(ck=None) == bad
@@ -180,8 +182,8 @@ def test_scan_backward_refuses(lm):
     assert call(dx_stride=7) == bad
     assert call(ws=None) == bad
     assert call(wsb=4) == bad
-    assert call(ws=0x400004) == bad
-    assert call(ws=0x310000) == bad     # workspace in dx
+    assert call(ws=0x800004) == bad
+    assert call(ws=0x340000) == bad     # workspace in dx
     # the gradient of a bias that is not there
     grad = lm.logmel_scan_grad(**fine, d_dbias=0x710000)
     for n_seq in (0, 2):
