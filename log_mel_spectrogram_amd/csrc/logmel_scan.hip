@@ -66,8 +66,10 @@ __device__ __forceinline__ void seq_range(const int64_t* off, int64_t j, int64_t
 // two lanes, of which one could write a state in place that the other has yet
 // to read), row after row. With 131,072 lanes or more bound by memory (4000
 // sequences of 50 rows x 512 bf16: 123 us, 5.0 TB/s; 512 of 128 rows 44 us, 4.6
-// TB/s), below by the latency of a batch of rows; the push of 512 x 8 rows
-// takes 7 us on the device.
+// TB/s, of fp32 82 us, 4.9 TB/s), below by the latency of a batch of rows; the
+// push of 512 x 8 rows takes 7 us on the device. 2-byte rows take two channels
+// per lane (2000 x 100 x 128 bf16 35 us, one channel 39); fp32 rows one, as two
+// with a batch in flight spill (65 against 106 us).
 template <typename T, int V>
 __global__ void logmel_scan_lanes_kernel(ScanArgs<T> p) {
   const int64_t groups = p.channels / V;
@@ -1082,7 +1084,7 @@ struct Split {
 // this card, in us:
 //  - once: each value read or written once, 4.6 TB/s over the bytes (3 values
 //    of the type per row and channel, 5 in the gradient);
-//  - a row of a lane that walks a sequence alone: 0.2 (2-byte rows), 0.35;
+//  - a row of a lane that walks a sequence alone: 0.2;
 //  - a tile: 3 for a workgroup on an idle card, whose longest sequence sets
 //    the least time of a split by sequences (6 in the gradient); 5 where the
 //    compute units are full, with one workgroup of two channels per lane or
@@ -1153,12 +1155,12 @@ Split scan_split(const logmel_scan_input& in, int cus, bool backward) {
   if (parts > 1) in_parts += 6.0;
 
   // one lane each
-  const double rowwise = (size == 4.0 ? 0.35 : 0.2) * (double)longest;
+  const double rowwise = 0.2 * (double)longest;
   const double in_lanes = rowwise > once ? rowwise : once;
 
   if (!backward && in_lanes <= by_sequences && in_lanes <= in_parts) {
     s.how = Split::kLanes;
-    s.pairs = in.channels % 2 ? 1 : 2;
+    s.pairs = in.channels % 2 || size == 4.0 ? 1 : 2;
   } else if (by_sequences <= in_parts) {
     s.how = Split::kSequences;
     s.pairs = pairs ? 2 : 1;
@@ -1190,10 +1192,14 @@ hipError_t launch_scan(const logmel_scan_input& in, void* h, int64_t h_stride, f
   const Split s = scan_split(in, cus, false);
   PartArgs q{};
   if (s.how == Split::kLanes) {
-    if (s.pairs == 2)
-      launch_scan_lanes<T, 2>(p, stream);
-    else
+    if constexpr (sizeof(T) == 2) {
+      if (s.pairs == 2)
+        launch_scan_lanes<T, 2>(p, stream);
+      else
+        launch_scan_lanes<T, 1>(p, stream);
+    } else {
       launch_scan_lanes<T, 1>(p, stream);
+    }
   } else if (s.how == Split::kSequences) {
     const unsigned grid = grid_for(in.n_seq, s.slabs);
     q.by_die = by_die(in.n_seq);
