@@ -1088,13 +1088,13 @@ struct Split {
 //  - a tile: 3 for a workgroup on an idle card, whose longest sequence sets
 //    the least time of a split by sequences (6 in the gradient); 5 where the
 //    compute units are full, with one workgroup of two channels per lane or
-//    two of one channel per lane each (8 and 6 in the gradient, one workgroup
-//    a compute unit in either). A sequence of L rows touches
-//    (L + 127) / 128 tiles on average;
+//    two of one channel per lane each (7 to 8.5 and 6 in the gradient, one
+//    workgroup a compute unit in either), and 3 (4) to start. A sequence of L
+//    rows touches (L + 127) / 128 tiles on average;
 //  - in parts, the first kernel reads two values per row and channel again of
-//    each sequence that runs on past its part, and costs a launch, 6; a tile
-//    with a sequence's end in it takes up to 1.4 times as long, and the lanes
-//    past a width's end cost what the others do.
+//    each sequence that runs on past its part, and costs a launch, 8; a tile
+//    with a sequence's end in it takes up to 1.4 times as long, and for 2-byte
+//    rows the lanes past a width's end cost what the others do.
 // Measured, the way taken first: 512 sequences of 128 rows x 512 bf16 one lane
 // each 44, by sequences 59, in parts 75; 64 of them by sequences 10, one lane
 // each 27; 64 x 2998 x 512 by sequences 126, in parts 183; 64 x 2998 x 128 in
@@ -1131,8 +1131,10 @@ Split scan_split(const logmel_scan_input& in, int cus, bool backward) {
   const bool too_many = in.n_seq > (int64_t(1) << 30) / slabs;   // workgroups
   const int64_t groups = too_many ? 0 : in.n_seq * slabs;
   const int64_t slots = !backward && !pairs ? 2 * cus : cus;
-  const double tile = backward ? (pairs ? 8.0 : 6.0) : !pairs && groups <= cus ? 3.0 : 5.0;
-  const double full = (double)ceil_div(groups, slots) * (mean + 127.0) / 128.0 * tile;
+  const double tile = backward ? (!pairs ? 6.0 : groups <= cus ? 7.0 : 8.5)
+                               : !pairs && groups <= cus ? 3.0 : 5.0;
+  const double start = backward ? 4.0 : 3.0;
+  const double full = (double)ceil_div(groups, slots) * ((mean + 127.0) / 128.0 * tile + start);
   const double alone = (backward ? 6.0 : 3.0) * (double)ceil_div(longest, kCk);
   double by_sequences = once > alone ? once : alone;
   if (full > by_sequences) by_sequences = full;
@@ -1147,12 +1149,13 @@ Split scan_split(const logmel_scan_input& in, int cus, bool backward) {
   const int64_t part_rows = ceil_div(ceil_div(rows, kCk), want) * kCk;
   const int64_t parts = ceil_div(rows, part_rows);
   const double again = mean >= 2.0 * part_rows ? 1.0 : mean / (2.0 * part_rows);
-  const double lanes = (double)(part_slabs * 64 * part_pairs) / (double)in.channels;
+  const double lanes =
+      size == 2.0 ? (double)(part_slabs * 64 * part_pairs) / (double)in.channels : 1.0;
   double in_parts = once * lanes * (1.0 + again * 2.0 / units) *
                     (1.0 + 0.4 * (mean > 128.0 ? 128.0 / mean : 1.0));
   const double walk = (backward ? 6.0 : 3.0) * (double)(part_rows / kCk);
   if (walk > in_parts) in_parts = walk;
-  if (parts > 1) in_parts += 6.0;
+  if (parts > 1) in_parts += 8.0;
 
   // one lane each
   const double rowwise = 0.2 * (double)longest;
