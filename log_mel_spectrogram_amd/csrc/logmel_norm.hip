@@ -349,7 +349,7 @@ __global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_
 // it within 128 registers, so that 16 wavefronts a compute unit have their
 // rows in flight. 64 x 2998 x 512 bf16: 303 us (5.2 TB/s, traffic 1.00 x); with
 // 40 values spilled to memory it took 896. 2998 x 4096 fp32 83 us. fp32 rows of
-// more than 4096 channels hold 8 values a lane in 1024 lanes and spill 33 (4.0
+// more than 4096 channels hold 8 values a lane in 1024 lanes and spill 35 (4.0
 // TB/s).
 template <typename T, int kParts, int kLanes, int kVecs>
 __global__ __launch_bounds__(kThreads<kLanes>,
@@ -391,7 +391,9 @@ __global__ __launch_bounds__(kThreads<kLanes>,
         for (int i = 0; i < V; ++i)
           s1 = k.counts(j, i) ? __builtin_fmaf(h.at(j, i), h.at(j, i), s1) : s1;
       sum(s1);
-      r1 = inv_root(__builtin_fmaf(s1, inv, p.eps));
+      // without a row 0, which leaves the sums over rows as they are: the
+      // root of a mean square and eps of 0 would not
+      r1 = on ? inv_root(__builtin_fmaf(s1, inv, p.eps)) : 0.0f;
       h.unpack_anew();
     }
     // silu(gate), formed again wherever it is needed
@@ -414,7 +416,7 @@ __global__ __launch_bounds__(kThreads<kLanes>,
     float r2 = 0.0f, k2 = 0.0f;
     if (q.dz) {
       sum(s2, m2, true);
-      r2 = inv_root(__builtin_fmaf(s2, inv, p.eps));
+      r2 = on ? inv_root(__builtin_fmaf(s2, inv, p.eps)) : 0.0f;
       k2 = r2 * r2 * (m2 * inv);
       dz.unpack_anew();
     }

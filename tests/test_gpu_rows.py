@@ -433,6 +433,16 @@ def test_norm_extremes(env):
             assert torch.isfinite(y3[:, 1::4]).all() and torch.isfinite(y3[:, 2::4]).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_norm_without_eps(env, dtype):
+    """eps 0, and rows that leave the last workgroup partly empty: the lanes
+    without a row add nothing to the parameters' sums."""
+    for channels in (64, 200, 700):
+        for rows in (1, 5, 33):
+            say(f"norm without eps {dtype} {rows} x {channels}")
+            norm_case(env, dtype, rows, channels, "dense", eps=0.0, seed=rows)
+
+
 def test_norm_gradient_repeats_bit_for_bit(env):
     lm, plan, torch = env
     dev = torch.device("cuda", 0)
