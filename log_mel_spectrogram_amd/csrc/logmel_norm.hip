@@ -304,11 +304,7 @@ __global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_
           s1 = k.counts(j, i) ? __builtin_fmaf(x, x, s1) : s1;
           t[j][i] = x * w1[j][i];
         }
-        if constexpr (kParts == kGated) {
-          float a, u;
-          Gate<T>::pair(o.at(j, i), 0.0f, a, u);
-          t[j][i] *= o.at(j, i) * a;
-        }
+        if constexpr (kParts == kGated) t[j][i] *= o.at(j, i) * Gate<T>::sigmoid(o.at(j, i));
       }
     if (first + step < p.rows) load(r + step);
     if constexpr (kParts != kNone) {
@@ -405,8 +401,7 @@ __global__ __launch_bounds__(kThreads<kLanes>,
       for (int i = 0; i < V; ++i) {
         y[j][i] = res.at(j, i);
         if constexpr (kParts != kNone) {
-          float u;
-          if constexpr (kParts == kGated) Gate<T>::pair(o.at(j, i), 0.0f, sig[j][i], u);
+          if constexpr (kParts == kGated) sig[j][i] = Gate<T>::sigmoid(o.at(j, i));
           y[j][i] = __builtin_fmaf(h.at(j, i) * r1, w1[j][i] * act(j, i), y[j][i]);
         }
         const float yc = k.counts(j, i) ? y[j][i] : 0.0f;

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace logmel {
 
 using bf16_t = __bf16;
@@ -56,7 +58,10 @@ __device__ __forceinline__ void row_store(T* p, const float (&x)[V]) {
 // sigmoid(g + bias) and sigmoid(-(g + bias)), each to full relative precision:
 // with e = e^-(g + bias) they are r = 1 / (1 + e) and e r, and neither is
 // formed as 1 minus the other. The exponent is kept below 2^126 so that e is
-// finite and r is not flushed: from g + bias = -87 on down, r stays at 1e-38.
+// finite and r is not flushed: from g + bias = -87 on down, r would stay at
+// 1e-38, which of a state near the type's largest value leaves ones, so there a
+// is 0 (fp16 states are too small for that to matter, and do without the two
+// instructions: 1 % of a bf16 call's time).
 // minimum and maximum are those that return a NaN operand, so a NaN gate gives
 // two NaN. Four instructions beside the two transcendentals, which take as
 // long: the recurrence reads 4 bytes per value and is held up by instructions
@@ -68,6 +73,7 @@ __device__ __forceinline__ void row_store(T* p, const float (&x)[V]) {
 template <typename T>
 struct Gate {
   static constexpr float kLog2e = 1.44269504088896340736f;
+  static constexpr float kClosed = 5e37f;   // the largest e there is is 6.0e37
   static __device__ __forceinline__ float bias_of(float bias) {
     return sizeof(T) == 4 ? bias : -bias * kLog2e;
   }
@@ -88,6 +94,16 @@ struct Gate {
     }
     a = __builtin_amdgcn_rcpf(1.0f + e);
     u = e * a;
+    if constexpr (!std::is_same_v<T, f16_t>) a = e > kClosed ? 0.0f : a;
+  }
+  // a alone, of a gate without a bias: nothing needs e finite for 2-byte rows.
+  static __device__ __forceinline__ float sigmoid(float g) {
+    float a, u;
+    if constexpr (sizeof(T) == 4)
+      pair(g, 0.0f, a, u);
+    else
+      a = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -kLog2e));
+    return a;
   }
 };
 

@@ -209,6 +209,33 @@ def test_scan_gate_extremes(env):
         assert not torch.isfinite(h2[15, 7])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [8, 300, 4000])
+def test_scan_closes_behind_the_largest_values(env, dtype, rows):
+    """A row near the type's largest and lowest values, taken whole, and a gate
+    at the lowest value behind it: nothing of the large state is left."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say(f"scan closes {dtype} {rows} rows")
+    dt = getattr(torch, dtype)
+    top = float(torch.finfo(dt).max)
+    rng = np.random.default_rng(rows)
+    x = torch.from_numpy(rng.normal(size=(rows, 64))).to(dt).to(dev)
+    g = torch.from_numpy(rng.normal(size=(rows, 64))).to(dt).to(dev)
+    first = rows // 2   # of the rows from the closing one on
+    x[first - 1, 0::2], x[first - 1, 1::2] = top / 4, -top / 4
+    g[first - 1 : first + 1] = -top
+    state_out = torch.empty((1, 64), device=dev)
+    off_d = torch.tensor([0, rows], device=dev)
+    h = lm.logmel_gated_scan(plan, x, g, off_d, state_out=state_out)
+    assert torch.isfinite(h[first - 1]).all() and (h[first - 1].abs() > top / 5).all()
+    # from there on it is the recurrence of a sequence that starts there
+    val, tol = rows_ref.scan(host(x)[first:], np.maximum(host(g)[first:], -60.0),
+                             np.array([0, rows - first]), dtype=dtype)
+    check(h[first:], val["h"], tol["h"] + 1e-20, "h")
+    check(state_out, val["state_out"], tol["state_out"] + 1e-20, "state_out")
+
+
 def test_scan_pushes_carry_the_state(env):
     """Streams fed a few rows at a time with the state updated in place give
     the rows of the whole sequences (streams that get nothing included)."""
@@ -441,6 +468,31 @@ def test_norm_without_eps(env, dtype):
         for rows in (1, 5, 33):
             say(f"norm without eps {dtype} {rows} x {channels}")
             norm_case(env, dtype, rows, channels, "dense", eps=0.0, seed=rows)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_norm_gates_far_out(env, dtype):
+    """A gate at the type's lowest value, or far below 0, closes its channel:
+    y is res there and the gradients of h and of the gate are 0; the others
+    come out as without it. silu is below 1e-36 from -100 on down."""
+    lm, plan, torch = env
+    say(f"norm gates far out {dtype}")
+    mk = Rows(torch, dtype, 40, 96, "dense", 4)
+    res, h, gate, dy = mk.normal(), mk.normal(), mk.normal(2.0), mk.normal()
+    low = float(torch.finfo(gate.dtype).min)
+    gate[:, 3::4], gate[:, 1::4] = low, -100.0 if dtype != "float32" else -1e30
+    gate[7] = low
+    y, _ = lm.logmel_block_norm(plan, res, h=h, gate=gate)
+    got = lm.logmel_block_norm_backward(plan, res, h=h, gate=gate, dy=dy)
+    mid = host(gate).astype(np.float64)
+    val, tol = rows_ref.norm(host(res), h=host(h), gate=np.maximum(mid, -100.0), dy=host(dy),
+                             grad=True, dtype=dtype)
+    for k, t in dict(y=y, **got).items():
+        if t is not None:
+            check(t, val[k], tol[k], k)
+    for cols in (slice(3, None, 4), slice(1, None, 4)):
+        assert torch.equal(y[:, cols], res[:, cols])
+        assert np.abs(host(got["dgate"])[:, cols]).max() < 1e-30
 
 
 def test_norm_gradient_repeats_bit_for_bit(env):
