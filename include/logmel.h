@@ -393,10 +393,11 @@ int logmel_resample(const logmel_resampler* r, const void* d_samples, int sample
  * h_{-1} the sequence's row of d_state (zero if d_state is NULL).
  * Products are plain IEEE: a NaN or infinity in x or gate stays in its
  * sequence and channel, from its row on. */
+#define LOGMEL_SCAN_MAX_CHANNELS (1 << 26)
 typedef struct logmel_scan_input {
   int32_t type;
   int64_t rows;                 /* rows of the row operands */
-  int64_t channels;             /* >= 1 */
+  int64_t channels;             /* 1..LOGMEL_SCAN_MAX_CHANNELS (INPUT_TOO_LONG beyond) */
   int64_t n_seq;                /* sequence i is rows [d_seq_offsets[i], d_seq_offsets[i+1]) */
   const int64_t* d_seq_offsets; /* int64[n_seq + 1], non-decreasing, the first 0, the last at most
                                    rows; rows from the last on belong to no sequence: they are not

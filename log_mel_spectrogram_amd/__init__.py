@@ -38,6 +38,7 @@ LOGMEL_I16 = 1
 LOGMEL_F16 = 2
 LOGMEL_BF16 = 3       # rows of the row operators only
 SCAN_CHECKPOINT = 128   # LOGMEL_SCAN_CHECKPOINT
+SCAN_MAX_CHANNELS = 1 << 26   # LOGMEL_SCAN_MAX_CHANNELS
 NORM_MAX_CHANNELS = 8192   # LOGMEL_NORM_MAX_CHANNELS
 N_FFT = 400
 HOP = 160

@@ -107,7 +107,8 @@ Operands scan_operands(const logmel_scan_input& in) {
   if (in.n_seq < 0 || in.max_frames < 0 || (!in.d_seq_offsets && in.n_seq) ||
       (uintptr_t)in.d_seq_offsets % 8)
     o.fault(LOGMEL_ERR_INVALID_ARGUMENT);
-  if (in.n_seq > INT64_MAX / 16) o.fault(LOGMEL_ERR_INPUT_TOO_LONG);
+  if (in.n_seq > INT64_MAX / 16 || in.channels > LOGMEL_SCAN_MAX_CHANNELS)
+    o.fault(LOGMEL_ERR_INPUT_TOO_LONG);
   o.row(in.d_x, in.x_stride, false, in.n_seq > 0);
   o.row(in.d_gate, in.gate_stride, false, in.n_seq > 0);
   if (!o.status()) o.bytes(in.d_seq_offsets, (in.n_seq + 1) * 8, false);

@@ -1128,7 +1128,9 @@ Split scan_split(const logmel_scan_input& in, int cus, bool backward) {
   const bool pairs = in.channels > 1 && (over == 0 || over > 64 || (backward && pair_slabs > 2)) &&
                      in.n_seq >= ceil_div(3 * cus, 4 * pair_slabs);
   const int64_t slabs = ceil_div(in.channels, pairs ? 128 : 64);
-  const bool too_many = in.n_seq > (int64_t(1) << 30) / slabs;   // workgroups
+  // a launch takes less than 2^32 threads: 2^23 workgroups, of which by_die
+  // may add an eighth
+  const bool too_many = in.n_seq > (int64_t(1) << 22) / slabs;
   const int64_t groups = too_many ? 0 : in.n_seq * slabs;
   const int64_t slots = !backward && !pairs ? 2 * cus : cus;
   const double tile = backward ? (!pairs ? 6.0 : groups <= cus ? 7.0 : 8.5)

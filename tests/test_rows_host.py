@@ -132,6 +132,27 @@ def test_scan_refuses_types_and_lengths(lm):
         lm.LOGMEL_ERR_INPUT_TOO_LONG
 
 
+def test_scan_splits_within_a_launch(lm):
+    """Ever more sequences of 1000 rows of two channels: one workgroup each
+    holds up to 2^22 of them (2^32 threads are too many for a launch), more
+    are worked in parts, whose sums of a bias's gradient take less room."""
+    for log2, most in ((20, None), (22, None), (23, 1 << 20), (24, 1 << 20)):
+        n = 1 << log2
+        inp = _scan_in(lm, type=lm.LOGMEL_F16, rows=1000 * n, channels=2, n_seq=n, x_stride=2,
+                       gate_stride=2, max_frames=1000, d_bias=0x800000,
+                       d_x=0x100000000000, d_gate=0x200000000000)
+        need = lm._gated_scan_workspace(FAKE, inp, 1)
+        assert need == 16 * n if most is None else 0 < need < most
+    wide = lm.SCAN_MAX_CHANNELS
+    inp = _scan_in(lm, rows=1, channels=wide, x_stride=wide, gate_stride=wide,
+                   d_x=0x100000000000, d_gate=0x200000000000)
+    assert lm._gated_scan_workspace(FAKE, inp, 1) >= 0
+    inp = _scan_in(lm, rows=1, channels=wide + 1, x_stride=wide + 1, gate_stride=wide + 1,
+                   d_x=0x100000000000, d_gate=0x200000000000)
+    assert _scan(lm, inp) == lm.LOGMEL_ERR_INPUT_TOO_LONG
+    assert lm._gated_scan_workspace(FAKE, inp, 1) == -1
+
+
 def test_scan_refuses_bad_outputs(lm):
     bad = lm.LOGMEL_ERR_INVALID_ARGUMENT
     assert _scan(lm, _scan_in(lm), h=None) == bad
