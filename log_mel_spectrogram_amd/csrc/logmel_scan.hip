@@ -434,7 +434,7 @@ __global__ __launch_bounds__(512) void logmel_scan_parts_kernel(ScanArgs<T> p, P
 // wavefronts exchange their runs' Affine through LDS, then h = P carry + H.
 // One barrier a tile, on two buffers in turn; the next tile's loads pass it in
 // flight. 16 rows a wavefront: 64 registers of P and H for two channels. By
-// sequences 64 x 2998 x 512 bf16 takes 124 us (4.75 TB/s; traffic 1.00 x the
+// sequences 64 x 2998 x 512 bf16 takes 125 us (4.7 TB/s; traffic 1.00 x the
 // bytes), fp32 231 us (5.1 TB/s); in parts 521,998 x 128 fp32 140 us after the
 // 120 of the parts' maps.
 template <typename T, int V, bool kParts, bool kEarly>
@@ -639,7 +639,7 @@ __global__ __launch_bounds__(512, kEarly ? 2 : 4) void logmel_scan_tiles_kernel(
 // last row (E after it is dstate_out). h_{t-1} is formed anew from the
 // checkpoint before the tile, by the same recurrence as in the forward call:
 // reading the rounded h instead would cost as many bytes as reading x does,
-// and lose the digits that h_{t-1} - x cancels. 64 x 2998 x 512 bf16: 216 us on
+// and lose the digits that h_{t-1} - x cancels. 64 x 2998 x 512 bf16: 220 us on
 // the device (4.5 TB/s; traffic 1.00 x), fp32 383 us (5.1 TB/s): two
 // wavefronts per SIMD, whose instructions take half of that time for 2-byte
 // rows. Loading a tile ahead as well does not fit the registers (358 us).
