@@ -163,6 +163,31 @@ def test_scan_wide_and_split(env, seqs):
               seed=11)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_scan_very_wide_rows(env, dtype):
+    say(f"scan {dtype} 70,001 channels")
+    scan_case(env, dtype, 70001, [3, 0, 2], "odd", True, True, behind=1, seed=13)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_scan_tens_of_thousands_of_sequences(env, dtype):
+    lens = np.random.default_rng(14).integers(0, 4, size=30000).tolist()
+    for max_frames in (0, 3):
+        say(f"scan {dtype} 30,000 sequences max_frames {max_frames}")
+        scan_case(env, dtype, 3, lens, "dense", True, True, behind=1, max_frames=max_frames,
+                  seed=15)
+
+
+@pytest.mark.parametrize("max_frames", [1, 200, 1 << 40])
+def test_scan_wrong_hint_changes_no_result(env, max_frames):
+    """max_frames below and far above the longest sequence: another split, the
+    same recurrence."""
+    say(f"scan max_frames {max_frames}")
+    for n in (1, 40):
+        scan_case(env, "float16", 130, [700, 3, 0, 129] * n, "slice", True, True,
+                  max_frames=max_frames, seed=16)
+
+
 def test_scan_long_sequence_many_parts(env):
     say("scan 60000 rows x 4")
     scan_case(env, "float32", 4, [60000, 17], "dense", True, True, seed=12, gate_scale=1.0)
