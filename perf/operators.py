@@ -298,7 +298,7 @@ def _plain_scan(st):
     if case["train"]:
         prev = torch.roll(h, 1, 0)
         prev[first] = h0[seq]
-        d = st["dh"].to(torch.float32, copy=True)   # changed below, not the caller's
+        d = st["dh"].float()
         if st["dstate_out"] is not None:
             d[last] = d[last] + st["dstate_out"][seq]
         back = torch.roll(a, -1, 0)
