@@ -5,8 +5,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <type_traits>
-
 namespace logmel {
 
 using bf16_t = __bf16;
@@ -58,14 +56,14 @@ __device__ __forceinline__ void row_store(T* p, const float (&x)[V]) {
 // sigmoid(g + bias) and sigmoid(-(g + bias)), each to full relative precision:
 // with e = e^-(g + bias) they are r = 1 / (1 + e) and e r, and neither is
 // formed as 1 minus the other. The exponent is kept below 2^126 so that e is
-// finite and r is not flushed: from g + bias = -87 on down, r would stay at
-// 1e-38, which of a state near the type's largest value leaves ones, so there a
-// is 0 (fp16 states are too small for that to matter, and do without the two
-// instructions: 1 % of a bf16 call's time).
+// finite and r is not flushed: from g + bias = -87 on down r would stay at
+// 1e-38, which of a state near fp32's largest value leaves ones, so there a is
+// 0, in 2-byte rows too: their states are fp32, and the caller's (two
+// instructions: 1 to 2 % of a 2-byte call's time).
 // minimum and maximum are those that return a NaN operand, so a NaN gate gives
-// two NaN. Four instructions beside the two transcendentals, which take as
-// long: the recurrence reads 4 bytes per value and is held up by instructions
-// as much as by memory (see the tiles).
+// two NaN. Six instructions of a 2-byte row beside the two transcendentals,
+// which take as long: the recurrence reads 4 bytes per value and is held up by
+// instructions as much as by memory (see the tiles).
 // 2-byte rows take the bias into the exponent's multiply-add (nb = -bias
 // log2(e)): e is off by (|g + bias| + |bias|) 2^-24 relative. fp32 rows add
 // first and correct e for the rounding of the product (|g| 2^-24 in e, ten
@@ -94,7 +92,7 @@ struct Gate {
     }
     a = __builtin_amdgcn_rcpf(1.0f + e);
     u = e * a;
-    if constexpr (!std::is_same_v<T, f16_t>) a = e > kClosed ? 0.0f : a;
+    a = e > kClosed ? 0.0f : a;
   }
   // a alone, of a gate without a bias: nothing needs e finite for 2-byte rows.
   static __device__ __forceinline__ float sigmoid(float g) {

@@ -1,0 +1,48 @@
+"""The row operators on the GPU at their edges: values and calls beside the
+sizes and layouts of test_gpu_rows.py."""
+
+import numpy as np
+import pytest
+
+from tests import rows_ref
+from tests.test_gpu_rows import DTYPES, Rows, check, env, host, say   # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [1, 8, 300, 4000])
+def test_scan_closed_gate_leaves_nothing_of_a_large_state(env, dtype, rows):
+    """States are fp32 whatever the rows' type: a gate at the type's lowest
+    value closes behind a state near fp32's largest, in the gradient too, and
+    of an infinite one leaves 0 times infinity."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say(f"scan closes behind a large state {dtype} {rows} rows")
+    dt = getattr(torch, dtype)
+    rng = np.random.default_rng(rows)
+    x, g, dh = (torch.from_numpy(rng.normal(size=(rows + 1, 64))).to(dt).to(dev)
+                for _ in range(3))
+    g[0] = g[rows] = float(torch.finfo(dt).min)
+    off = np.array([0, rows, rows + 1])
+    off_d = torch.from_numpy(off).to(dev)
+    state = torch.full((2, 64), 3e38, device=dev)
+    state[:, 1::2] = -3e38
+    dso = torch.zeros((2, 64), device=dev)
+    dso[1] = 3e38
+    state_out = torch.empty_like(state)
+    ck = torch.empty((lm.logmel_gated_scan_checkpoint_rows(rows + 1), 64), device=dev)
+    h = lm.logmel_gated_scan(plan, x, g, off_d, state=state, state_out=state_out, checkpoints=ck)
+    dx, dg, _, ds = lm.logmel_gated_scan_backward(plan, dh, x, g, off_d, ck, state=state,
+                                                  dstate_out=dso)
+    # the recurrence from a state of 0; what a gate beyond -60 leaves of its
+    # rows is below 1e-20
+    val, tol = rows_ref.scan(host(x), np.maximum(host(g), -60.0), off, dh=host(dh), dtype=dtype)
+    check(h, val["h"], tol["h"] + 1e-20, "h")
+    check(state_out, val["state_out"], tol["state_out"] + 1e-20, "state_out")
+    check(dx[:rows], val["dx"][:rows], tol["dx"][:rows] + 1e-20, "dx")
+    check(dg, np.where(np.isin(np.arange(rows + 1), (0, rows))[:, None], 0.0, val["dgate"]),
+          tol["dgate"] + 1e-20, "dgate")
+    assert (ds == 0.0).all()
+    h = lm.logmel_gated_scan(plan, x, g, off_d, state=torch.full_like(state, float("inf")))
+    assert torch.isnan(h).all()
