@@ -67,12 +67,18 @@ class Operands {
     add({(uintptr_t)p, rows_, channels_ * size_, stride * size_}, output);
   }
 
-  // n rows of `channels` fp32
-  void floats(const float* p, int64_t n, bool output, const void* may_be = nullptr) {
+  // n rows of `channels` fp32; except: the one operand that this output may
+  // be as well (as `at` returned it), none by default
+  void floats(const float* p, int64_t n, bool output, int except = -1) {
     if (status_ || !p) return;
     if ((uintptr_t)p % 4) return fault(LOGMEL_ERR_INVALID_ARGUMENT);
     if (n && channels_ > INT64_MAX / 8 / n) return fault(LOGMEL_ERR_INPUT_TOO_LONG);
-    add({(uintptr_t)p, n, channels_ * 4, channels_ * 4}, output, may_be);
+    add({(uintptr_t)p, n, channels_ * 4, channels_ * 4}, output, except);
+  }
+
+  // the operand at p that was added last; -1 if it is another or none
+  int at(const void* p) const {
+    return n_ && p && span_[n_ - 1].p == (uintptr_t)p ? n_ - 1 : -1;
   }
 
   void bytes(const void* p, int64_t n, bool output) {
@@ -86,10 +92,9 @@ class Operands {
   int status() const { return status_; }
 
  private:
-  void add(const Span& s, bool output, const void* may_be = nullptr) {
+  void add(const Span& s, bool output, int except = -1) {
     for (int i = 0; i < n_; ++i)
-      if ((output || out_[i]) && !(may_be && span_[i].p == (uintptr_t)may_be && s.p == span_[i].p) &&
-          overlap(span_[i], s))
+      if ((output || out_[i]) && !(i == except && s.p == span_[i].p) && overlap(span_[i], s))
         return fault(LOGMEL_ERR_INVALID_ARGUMENT);
     span_[n_] = s;
     out_[n_++] = output;
@@ -183,9 +188,10 @@ int logmel_gated_scan(const logmel_plan* plan, const logmel_scan_input* in, void
   if (!plan || !in) return LOGMEL_ERR_INVALID_ARGUMENT;
   Operands o = scan_operands(*in);
   if (o.status()) return o.status();
+  const int state = o.at(in->d_state);   // the last operand of scan_operands
   const int64_t need = logmel_scan_workspace(*in, 0, cus_of(plan));
   o.row(d_h, h_stride, true, in->n_seq > 0);
-  o.floats(d_state_out, in->n_seq, true, in->d_state);
+  o.floats(d_state_out, in->n_seq, true, state);   // may be the state, and no other operand
   o.floats(d_checkpoints, checkpoint_rows(in->rows), true);
   workspace_operand(o, d_workspace, workspace_bytes, need);
   if (o.status()) return o.status();
