@@ -102,13 +102,10 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
-// Wavefronts per SIMD that the kernels leave room for. The gradient of a gated
-// 2-byte row holds eight values of five operands per lane; where a wavefront
-// takes several rows, whose addresses are then per lane too, that is more than
-// the 128 registers of four (96 us for 191,872 x 128 bf16 with three, 112 with
-// values spilled).
+// Wavefronts per SIMD that the kernels leave room for: the gradient holds eight
+// values of five operands per lane within the 128 registers of four.
 constexpr int front_waves(int lanes) { return lanes > 256 ? 4 : 5; }
-constexpr int back_waves(bool narrow_gated) { return narrow_gated ? 3 : 4; }
+constexpr int kBackWaves = 4;
 
 template <int kLanes>
 constexpr int kThreads = kLanes > 256 ? kLanes : 256;
@@ -154,7 +151,9 @@ struct RowSum {
 // of a width that V does not divide is shifted back to end with the row, so
 // that it is read and written whole: its first values are another lane's too,
 // who writes the same, and only the sums leave them out. Lanes past the row's
-// end hold nothing. (Rows narrower than V go value by value.)
+// end hold nothing. Rows narrower than 16 bytes take V = 1, in kernels of their
+// own: as a branch beside the wide loads, their merged registers made each
+// operand's load be waited for before the next.
 template <int kLanes, int kVecs, int V>
 struct Channels {
   int C;
@@ -166,20 +165,19 @@ struct Channels {
     for (int j = 0; j < kVecs; ++j) {
       const int first = (j * kLanes + (int)(threadIdx.x & (kLanes - 1))) * V;
       on[j] = first < C;
-      c[j] = first + V <= C || C < V ? first : C - V;
+      c[j] = first + V <= C ? first : C - V;
       skip[j] = first - c[j];
     }
   }
   // Whether value i of vector j counts in this lane's sums.
   __device__ __forceinline__ bool counts(int j, int i) const {
-    return on[j] && i >= skip[j] && c[j] + i < C;
+    return on[j] && i >= skip[j];
   }
 };
 
 // A lane's vectors of one row operand, 0 where it holds nothing.
-template <typename T, int kLanes, int kVecs>
+template <typename T, int kLanes, int kVecs, int V>
 struct RowPiece {
-  static constexpr int V = 16 / sizeof(T);
   using Ch = Channels<kLanes, kVecs, V>;
   Packed<T, V> v[kVecs];
 
@@ -187,15 +185,7 @@ struct RowPiece {
 #pragma unroll
     for (int j = 0; j < kVecs; ++j) {
       v[j] = Packed<T, V>{};
-      if (on && k.on[j]) {
-        if (k.C >= V) {
-          v[j] = row_load<T, V>(row + k.c[j]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (i < k.C) v[j].v[i] = row[i];
-        }
-      }
+      if (on && k.on[j]) v[j] = row_load<T, V>(row + k.c[j]);
     }
   }
 
@@ -213,16 +203,8 @@ template <typename T, int kLanes, int kVecs, int V>
 __device__ __forceinline__ void piece_store(T* row, const Channels<kLanes, kVecs, V>& k,
                                             const float (&x)[kVecs][V]) {
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) {
-    if (!k.on[j]) continue;
-    if (k.C >= V) {
-      row_store<T, V>(row + k.c[j], x[j]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i < k.C) row[i] = (T)x[j][i];
-    }
-  }
+  for (int j = 0; j < kVecs; ++j)
+    if (k.on[j]) row_store<T, V>(row + k.c[j], x[j]);
 }
 
 // A lane's channels of a parameter, 1 where it is absent.
@@ -234,15 +216,9 @@ __device__ __forceinline__ void load_params(float (&r)[kVecs][V], const float* p
 #pragma unroll
     for (int i = 0; i < V; ++i) r[j][i] = 1.0f;
     if (!p || !k.on[j]) continue;
-    if (k.C >= V) {
-      const auto v = row_load<float, V>(p + k.c[j]);
+    const auto v = row_load<float, V>(p + k.c[j]);
 #pragma unroll
-      for (int i = 0; i < V; ++i) r[j][i] = v.v[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (i < k.C) r[j][i] = p[i];
-    }
+    for (int i = 0; i < V; ++i) r[j][i] = v.v[i];
   }
 }
 
@@ -267,11 +243,10 @@ __device__ __forceinline__ int group_of() {
   return kLanes >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
 }
 
-template <typename T, int kParts, int kLanes, int kVecs>
+template <typename T, int kParts, int kLanes, int kVecs, int V>
 __global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_norm_kernel(NormArgs<T> p,
                                                                          NormOut<T> out) {
-  using P = RowPiece<T, kLanes, kVecs>;
-  constexpr int V = P::V;
+  using P = RowPiece<T, kLanes, kVecs, V>;
   constexpr int kRows = kThreads<kLanes> / kLanes;
   __shared__ float slots[2][2][kThreads<kLanes> / 64];
   RowSum<kLanes> sum{slots};
@@ -339,21 +314,19 @@ __global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_
 //   dres = G;  e = G act w;  dh = r1 (e - h r1^2 mean(e h));
 //   dgate = G n w slope;  dw_post = scale sum(G n act), dscale = w_post of the
 //   same sum;  dw_pre = sum(dz y r2).
+// Without dz G is dy, and res is not read.
 // Three sums over the row one after the other. The two sums over the lane's
 // rows stay in its registers to the end, then the workgroup's rows are added
 // in LDS and each workgroup writes one part. Eight values per lane keep all of
 // it within 128 registers, so that 16 wavefronts a compute unit have their
 // rows in flight. 64 x 2998 x 512 bf16: 303 us (5.2 TB/s, traffic 1.00 x); with
 // 40 values spilled to memory it took 896. 2998 x 4096 fp32 83 us. fp32 rows of
-// more than 4096 channels hold 8 values a lane in 1024 lanes and spill 35 (4.0
-// TB/s).
-template <typename T, int kParts, int kLanes, int kVecs>
-__global__ __launch_bounds__(kThreads<kLanes>,
-                             back_waves(kParts == kGated && sizeof(T) == 2 &&
-                                        kLanes < 64)) void logmel_norm_backward_kernel(NormArgs<T> p,
-                                                                                       NormGradArgs<T> q) {
-  using P = RowPiece<T, kLanes, kVecs>;
-  constexpr int V = P::V;
+// more than 4096 channels hold 8 values a lane in 1024 lanes and spill 27
+// (3000 x 5000 with its call 211 us, 3.7 TB/s).
+template <typename T, int kParts, bool kDz, int kLanes, int kVecs, int V>
+__global__ __launch_bounds__(kThreads<kLanes>, kBackWaves) void logmel_norm_backward_kernel(
+    NormArgs<T> p, NormGradArgs<T> q) {
+  using P = RowPiece<T, kLanes, kVecs, V>;
   constexpr int kRows = kThreads<kLanes> / kLanes;
   __shared__ float slots[2][2][kThreads<kLanes> / 64];
   RowSum<kLanes> sum{slots};
@@ -368,14 +341,14 @@ __global__ __launch_bounds__(kThreads<kLanes>,
   const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t r = (int64_t)blockIdx.x * kRows + group_of<kLanes>();
   if constexpr (kParts != kNone) load_block_params(w1, p, k);
-  load_params(w2, p.w_pre, k);
+  if constexpr (kDz) load_params(w2, p.w_pre, k);
   for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.rows; first += step, r += step) {
     P res, h, o, dy, dz;
     const bool on = r < p.rows;
     if constexpr (kParts != kNone) h.load(p.h + r * p.hs, k, on);
-    res.load(p.res + r * p.ress, k, on);
+    if constexpr (kDz) res.load(p.res + r * p.ress, k, on);
     if constexpr (kParts == kGated) o.load(p.o + r * p.os, k, on);
-    dz.load(q.dz + r * q.dzs, k, on && q.dz);
+    if constexpr (kDz) dz.load(q.dz + r * q.dzs, k, on);
     dy.load(q.dy + r * q.dys, k, on && q.dy);
     float r1 = 0.0f;
     float y[kVecs][V], sig[kVecs][V];   // sig: sigmoid(gate)
@@ -399,33 +372,39 @@ __global__ __launch_bounds__(kThreads<kLanes>,
     for (int j = 0; j < kVecs; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        y[j][i] = res.at(j, i);
-        if constexpr (kParts != kNone) {
-          if constexpr (kParts == kGated) sig[j][i] = Gate<T>::sigmoid(o.at(j, i));
-          y[j][i] = __builtin_fmaf(h.at(j, i) * r1, w1[j][i] * act(j, i), y[j][i]);
+        if constexpr (kParts == kGated) sig[j][i] = Gate<T>::sigmoid(o.at(j, i));
+        if constexpr (kDz) {
+          y[j][i] = res.at(j, i);
+          if constexpr (kParts != kNone)
+            y[j][i] = __builtin_fmaf(h.at(j, i) * r1, w1[j][i] * act(j, i), y[j][i]);
+          const float yc = k.counts(j, i) ? y[j][i] : 0.0f;
+          s2 = __builtin_fmaf(yc, y[j][i], s2);
+          m2 = __builtin_fmaf(dz.at(j, i) * w2[j][i], yc, m2);
         }
-        const float yc = k.counts(j, i) ? y[j][i] : 0.0f;
-        s2 = __builtin_fmaf(yc, y[j][i], s2);
-        m2 = __builtin_fmaf(dz.at(j, i) * w2[j][i], yc, m2);
       }
     float r2 = 0.0f, k2 = 0.0f;
-    if (q.dz) {
+    if constexpr (kDz) {
       sum(s2, m2, true);
       r2 = on ? inv_root(__builtin_fmaf(s2, inv, p.eps)) : 0.0f;
       k2 = r2 * r2 * (m2 * inv);
       dz.unpack_anew();
     }
-    h.unpack_anew();
-    o.unpack_anew();
+    if constexpr (kParts != kNone) h.unpack_anew();
+    if constexpr (kParts == kGated) o.unpack_anew();
     float m1 = 0.0f;
 #pragma unroll
     for (int j = 0; j < kVecs; ++j)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float z = dz.at(j, i);
-        a2[j][i] = __builtin_fmaf(z * r2, y[j][i], a2[j][i]);
         // y holds G from here on
-        y[j][i] = __builtin_fmaf(r2, __builtin_fmaf(-k2, y[j][i], z * w2[j][i]), dy.at(j, i));
+        if constexpr (kDz) {
+          const float z = dz.at(j, i);
+          a2[j][i] = __builtin_fmaf(z * r2, y[j][i], a2[j][i]);
+          y[j][i] =
+              __builtin_fmaf(r2, __builtin_fmaf(-k2, y[j][i], z * w2[j][i]), dy.at(j, i));
+        } else {
+          y[j][i] = dy.at(j, i);
+        }
         if constexpr (kParts != kNone)
           m1 = k.counts(j, i)
                    ? __builtin_fmaf(y[j][i] * (w1[j][i] * act(j, i)), h.at(j, i), m1)
@@ -476,7 +455,7 @@ __global__ __launch_bounds__(kThreads<kLanes>,
     }
   };
   if constexpr (kParts != kNone) write(a1, 0);
-  write(a2, 1);
+  if constexpr (kDz) write(a2, 1);
 }
 
 template <typename T>
@@ -496,15 +475,16 @@ NormArgs<T> norm_args(const logmel_norm_input& in) {
 }
 
 // The lanes a row takes: the fewest, in powers of two from 16, that hold it
-// with one vector each (8192 fp32 channels: 1024 lanes with two).
+// with one vector each (8192 fp32 channels: 1024 lanes with two), and the
+// values of a vector.
 struct NormShape {
-  int lanes, vecs;
+  int lanes, vecs, values;
 };
 
 NormShape norm_shape(const logmel_norm_input& in) {
   const int v = in.type == LOGMEL_F32 ? 4 : 8;
   const int64_t vecs = (in.channels + v - 1) / v;
-  NormShape s{16, 1};
+  NormShape s{16, 1, in.channels < v ? 1 : v};
   while (s.lanes < vecs && s.lanes < 1024) s.lanes *= 2;
   if (s.lanes < vecs) s.vecs = 2;
   return s;
@@ -517,31 +497,32 @@ NormShape norm_shape(const logmel_norm_input& in) {
 int64_t norm_grid(const logmel_norm_input& in, int cus, bool backward) {
   const int lanes = norm_shape(in).lanes;
   const int threads = lanes > 256 ? lanes : 256;
-  const bool narrow = in.d_gate && in.type != LOGMEL_F32 && lanes < 64;
-  const int waves = backward ? back_waves(narrow) : front_waves(lanes);
+  const int waves = backward ? kBackWaves : front_waves(lanes);
   const int64_t all = (in.rows + threads / lanes - 1) / (threads / lanes);
   const int64_t most = (int64_t)cus * waves * 256 / threads;
   return all < most ? all : most;
 }
 
-// f(type, parts, lanes, vecs) as compile-time constants.
+// f(type, parts, lanes, vecs, values) as compile-time constants.
 template <typename F>
 void norm_dispatch(const logmel_norm_input& in, F&& f) {
   const NormShape s = norm_shape(in);
   auto shape = [&](auto zero, auto parts) {
     using std::integral_constant;
     integral_constant<int, 1> one;
+    integral_constant<int, 16 / (int)sizeof(zero)> v;
+    if (s.values == 1) return f(zero, parts, integral_constant<int, 16>{}, one, one);
     if constexpr (sizeof(zero) == 4)
       if (s.vecs == 2)
-        return f(zero, parts, integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+        return f(zero, parts, integral_constant<int, 1024>{}, integral_constant<int, 2>{}, v);
     switch (s.lanes) {
-      case 16: return f(zero, parts, integral_constant<int, 16>{}, one);
-      case 32: return f(zero, parts, integral_constant<int, 32>{}, one);
-      case 64: return f(zero, parts, integral_constant<int, 64>{}, one);
-      case 128: return f(zero, parts, integral_constant<int, 128>{}, one);
-      case 256: return f(zero, parts, integral_constant<int, 256>{}, one);
-      case 512: return f(zero, parts, integral_constant<int, 512>{}, one);
-      default: return f(zero, parts, integral_constant<int, 1024>{}, one);
+      case 16: return f(zero, parts, integral_constant<int, 16>{}, one, v);
+      case 32: return f(zero, parts, integral_constant<int, 32>{}, one, v);
+      case 64: return f(zero, parts, integral_constant<int, 64>{}, one, v);
+      case 128: return f(zero, parts, integral_constant<int, 128>{}, one, v);
+      case 256: return f(zero, parts, integral_constant<int, 256>{}, one, v);
+      case 512: return f(zero, parts, integral_constant<int, 512>{}, one, v);
+      default: return f(zero, parts, integral_constant<int, 1024>{}, one, v);
     }
   };
   auto parts = [&](auto zero) {
@@ -567,10 +548,10 @@ int64_t logmel_norm_workspace(const logmel_norm_input& in, int cus) {
 hipError_t logmel_launch_norm(const logmel_norm_input& in, void* y, int64_t y_stride, void* z,
                               int64_t z_stride, int cus, hipStream_t stream) {
   using namespace logmel;
-  norm_dispatch(in, [&](auto zero, auto parts, auto lanes, auto vecs) {
+  norm_dispatch(in, [&](auto zero, auto parts, auto lanes, auto vecs, auto values) {
     using T = decltype(zero);
     const NormOut<T> out{static_cast<T*>(y), y_stride, static_cast<T*>(z), z_stride};
-    logmel_norm_kernel<T, parts.value, lanes.value, vecs.value>
+    logmel_norm_kernel<T, parts.value, lanes.value, vecs.value, values.value>
         <<<(unsigned)norm_grid(in, cus, false), kThreads<lanes.value>, 0, stream>>>(
             norm_args<T>(in), out);
   });
@@ -587,7 +568,7 @@ hipError_t logmel_launch_norm_backward(const logmel_norm_input& in, const logmel
   const bool params = g.d_dw_post || g.d_dscale || g.d_dw_pre;
   float* part = params ? static_cast<float*>(ws) : nullptr;
   if (grid)
-    norm_dispatch(in, [&](auto zero, auto parts, auto lanes, auto vecs) {
+    norm_dispatch(in, [&](auto zero, auto parts, auto lanes, auto vecs, auto values) {
       using T = decltype(zero);
       const NormGradArgs<T> q{static_cast<const T*>(g.d_dy),
                               g.dy_stride,
@@ -600,8 +581,12 @@ hipError_t logmel_launch_norm_backward(const logmel_norm_input& in, const logmel
                               static_cast<T*>(g.d_dgate),
                               g.dgate_stride,
                               part};
-      logmel_norm_backward_kernel<T, parts.value, lanes.value, vecs.value>
-          <<<(unsigned)grid, kThreads<lanes.value>, 0, stream>>>(norm_args<T>(in), q);
+      auto go = [&](auto has_dz) {
+        logmel_norm_backward_kernel<T, parts.value, has_dz.value, lanes.value, vecs.value,
+                                    values.value>
+            <<<(unsigned)grid, kThreads<lanes.value>, 0, stream>>>(norm_args<T>(in), q);
+      };
+      g.d_dz ? go(std::true_type{}) : go(std::false_type{});
     });
   if (params) return logmel_launch_part_sums(part, grid, 2, in.channels, sums, stream);
   return hipGetLastError();

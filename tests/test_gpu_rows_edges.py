@@ -46,3 +46,29 @@ def test_scan_closed_gate_leaves_nothing_of_a_large_state(env, dtype, rows):
     assert (ds == 0.0).all()
     h = lm.logmel_gated_scan(plan, x, g, off_d, state=torch.full_like(state, float("inf")))
     assert torch.isnan(h).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("block,gate", [(False, False), (True, False), (True, True)])
+def test_norm_gradient_without_dz_is_independent_of_y(env, dtype, block, gate):
+    """Without dz, y's gradient is dy as it is, and no output depends on res
+    or w_pre: infinities and NaN there change nothing."""
+    lm, plan, torch = env
+    for channels in (5, 96, 700, 2050):
+        say(f"norm gradient of dy alone {dtype} block {block} gate {gate} {channels}")
+        mk = Rows(torch, dtype, 70, channels, "odd", 6)
+        res, dy = mk.normal(), mk.normal()
+        kw = dict(dy=dy)
+        if block:
+            kw.update(h=mk.normal(), w_post=torch.full((channels,), 1.25, device=res.device),
+                      scale=torch.full((channels,), 0.5, device=res.device))
+        if gate:
+            kw.update(gate=mk.normal(2.0))
+        want = lm.logmel_block_norm_backward(plan, res, **kw)
+        assert torch.equal(want["dres"], dy)
+        res2 = res.clone()
+        res2[3, 1], res2[9, 0], res2[66, channels - 1] = float("inf"), float("nan"), -float("inf")
+        w_pre = torch.full((channels,), float("inf"), device=res.device)
+        got = lm.logmel_block_norm_backward(plan, res2, w_pre=w_pre, **kw)
+        for k, t in want.items():
+            assert (got[k] is None) if t is None else torch.equal(got[k], t), k
