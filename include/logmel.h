@@ -473,8 +473,9 @@ int logmel_gated_scan_backward(const logmel_plan* plan, const logmel_scan_input*
  * d_gate NULL: no silu factor. d_w_post, d_scale, d_w_pre NULL: 1. gate,
  * w_post and scale without h are INVALID_ARGUMENT. channels 1..8192
  * (UNSUPPORTED beyond); eps a finite number >= 0. Squares are fp32: a row whose
- * mean square plus eps is 0 or below the smallest normal number gives NaN or
- * infinities, one whose squares overflow a norm of 0. */
+ * mean square plus eps is 0 gives NaN or infinities, one below the smallest
+ * normal number has a norm of fewer digits, and one whose squares overflow a
+ * norm of 0. */
 #define LOGMEL_NORM_MAX_CHANNELS 8192
 typedef struct logmel_norm_input {
   int32_t type;

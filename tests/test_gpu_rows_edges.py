@@ -72,3 +72,51 @@ def test_norm_gradient_without_dz_is_independent_of_y(env, dtype, block, gate):
         got = lm.logmel_block_norm_backward(plan, res2, w_pre=w_pre, **kw)
         for k, t in want.items():
             assert (got[k] is None) if t is None else torch.equal(got[k], t), k
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("scale", [1e-20, 3e-21])
+def test_norm_of_rows_with_subnormal_mean_square(env, dtype, scale):
+    """eps 0 and rows whose squares are subnormal: their mean square has fewer
+    digits, and the norm and its gradient as many."""
+    lm, plan, torch = env
+    for channels in (64, 321, 2050):
+        say(f"norm of rows near {scale} {dtype} {channels}")
+        mk = Rows(torch, dtype, 33, channels, "dense", 7)
+        res, h, gate = mk.normal(scale), mk.normal(scale), mk.normal(2.0)
+        dz, up = mk.normal(), mk.normal()
+        y, z = lm.logmel_block_norm(plan, res, eps=0.0)
+        assert y is None
+        got = lm.logmel_block_norm_backward(plan, res, eps=0.0, dz=dz)
+        val, tol = rows_ref.norm(host(res), eps=0.0, dz=host(dz), grad=True, dtype=dtype)
+        # each of at most 2 channels + 2 roundings of the mean square is half
+        # a subnormal step, 2^-150; the root halves what that is of it, and
+        # the gradient has the root three times (and the mean of dz y, whose
+        # terms are near 1)
+        def lost(rows):
+            ms = (host(rows) ** 2).mean(1, keepdims=True)
+            return (2 * channels + 2) * 2.0 ** -150 / channels / ms + 2.0 ** -150 / ms
+
+        e = lost(res)
+        check(z, val["z"], tol["z"] + e * np.abs(val["z"]), "z")
+        r2 = 1.0 / np.sqrt((host(res) ** 2).mean(1, keepdims=True))
+        parts = np.abs(r2 * host(dz)) + np.abs(host(res)) * r2 ** 3 * np.abs(
+            (host(dz) * host(res)).mean(1, keepdims=True))
+        check(got["dres"], val["dres"], tol["dres"] + 3 * e * parts, "dres")
+        # a block's h of that size: t is of the size of 1 whatever h's is
+        one = mk.normal()
+        y, z = lm.logmel_block_norm(plan, one, h=h, gate=gate, eps=0.0)
+        val, tol = rows_ref.norm(host(one), h=host(h), gate=host(gate), eps=0.0, dtype=dtype)
+        e = lost(h)
+        t = np.abs(val["y"] - host(one))
+        check(y, val["y"], tol["y"] + e * t, "y")
+        assert torch.isfinite(z).all()
+        got = lm.logmel_block_norm_backward(plan, one, h=h, gate=gate, eps=0.0, dy=up)
+        val, tol = rows_ref.norm(host(one), h=host(h), gate=host(gate), eps=0.0, dy=host(up),
+                                 grad=True, dtype=dtype)
+        check(got["dgate"], val["dgate"], tol["dgate"] + e * np.abs(val["dgate"]), "dgate")
+        o = host(gate)
+        q = np.abs(host(up) * o * rows_ref.sigmoid(o))
+        r1 = 1.0 / np.sqrt((host(h) ** 2).mean(1, keepdims=True))
+        parts = r1 * q + np.abs(host(h)) * r1 ** 3 * (q * np.abs(host(h))).mean(1, keepdims=True)
+        check(got["dh"], val["dh"], tol["dh"] + 3 * e * parts, "dh")
