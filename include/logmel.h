@@ -502,9 +502,9 @@ int logmel_block_norm(const logmel_plan* plan, const logmel_norm_input* in, void
  * NULL) the gradients of res, h and gate (row outputs; dh and dgate exactly
  * where h and gate are given, else INVALID_ARGUMENT) and of the parameters
  * ([channels]; each may be NULL, and must be where its factor is absent: no h
- * for dw_post and dscale, no dz for dw_pre). Parameter sums are fp32 over
- * fixed parts of the rows, joined in order. Without dz the gradient of res is dy
- * as it is, and res and w_pre are not read. */
+ * for dw_post and dscale, no dz for dw_pre). Parameter sums are fp32 over at
+ * most 16 rows, joined in fp64 in a fixed order. Without dz the gradient of res
+ * is dy as it is, and res and w_pre are not read. */
 typedef struct logmel_norm_grad {
   const void* d_dy;
   int64_t dy_stride;

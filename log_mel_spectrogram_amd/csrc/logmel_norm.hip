@@ -112,6 +112,10 @@ __device__ __forceinline__ float lane_sum(float v) {
 constexpr int front_waves(int lanes) { return lanes > 256 ? 4 : 5; }
 constexpr int kBackWaves = 4;
 
+// Rows of a lane that are summed in fp32: 16 equal terms are off by 9 roundings
+// at most, as many as a row's own arithmetic, whatever the number of rows.
+constexpr int kHeld = 16;
+
 template <int kLanes>
 constexpr int kThreads = kLanes > 256 ? kLanes : 256;
 
@@ -173,6 +177,13 @@ struct Channels {
       c[j] = first + V <= C ? first : C - V;
       skip[j] = first - c[j];
     }
+  }
+  // Where channel c counts: in which lane, and as which of its values.
+  __device__ __forceinline__ void place(int c, int& lane, int& value) const {
+    const int vec = c / V;
+    const int from = vec * V + V <= C ? vec * V : C - V;
+    lane = vec % kLanes;
+    value = vec / kLanes * V + c - from;
   }
   // Whether value i of vector j counts in this lane's sums.
   __device__ __forceinline__ bool counts(int j, int i) const {
@@ -321,19 +332,21 @@ __global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_
 //   same sum;  dw_pre = sum(dz y r2).
 // Without dz G is dy, and res is not read.
 // Three sums over the row one after the other. The two sums over the lane's
-// rows stay in its registers to the end, then the workgroup's rows are added
-// in LDS and each workgroup writes one part. Eight values per lane keep all of
+// rows stay in its registers for kHeld rows, then go to fp64 places of its own
+// in LDS; at the end the workgroup's rows are added there and each workgroup
+// writes one part. Eight values per lane keep all of
 // it within 128 registers, so that 16 wavefronts a compute unit have their
 // rows in flight. 64 x 2998 x 512 bf16: 303 us (5.2 TB/s, traffic 1.00 x); with
 // 40 values spilled to memory it took 896. 2998 x 4096 fp32 83 us. fp32 rows of
-// more than 4096 channels hold 8 values a lane in 1024 lanes and spill 27
-// (3000 x 5000 with its call 211 us, 3.7 TB/s).
+// more than 4096 channels hold 8 values a lane in 1024 lanes and spill 20
+// (3000 x 5000 with its call 198 us, 3.9 TB/s).
 template <typename T, int kParts, bool kDz, int kLanes, int kVecs, int V>
 __global__ __launch_bounds__(kThreads<kLanes>, kBackWaves) void logmel_norm_backward_kernel(
     NormArgs<T> p, NormGradArgs<T> q) {
   using P = RowPiece<T, kLanes, kVecs, V>;
   constexpr int kRows = kThreads<kLanes> / kLanes;
   __shared__ float slots[2][2][kThreads<kLanes> / 64];
+  __shared__ double sums[2][kVecs * V][kThreads<kLanes>];
   RowSum<kLanes> sum{slots};
   const typename P::Ch k(p.channels);
   const float inv = 1.0f / (float)p.channels;
@@ -343,6 +356,22 @@ __global__ __launch_bounds__(kThreads<kLanes>, kBackWaves) void logmel_norm_back
   for (int j = 0; j < kVecs; ++j)
 #pragma unroll
     for (int i = 0; i < V; ++i) a1[j][i] = a2[j][i] = 0.0f;
+  if (q.part) {
+#pragma unroll
+    for (int n = 0; n < kVecs * V; ++n) sums[0][n][threadIdx.x] = sums[1][n][threadIdx.x] = 0.0;
+  }
+  // the rows since the last time out of the registers, into the lane's places
+  auto flush = [&] {
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (kParts != kNone) sums[0][j * V + i][threadIdx.x] += (double)a1[j][i];
+        if constexpr (kDz) sums[1][j * V + i][threadIdx.x] += (double)a2[j][i];
+        a1[j][i] = a2[j][i] = 0.0f;
+      }
+  };
+  int held = 0;
   const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t r = (int64_t)blockIdx.x * kRows + group_of<kLanes>();
   if constexpr (kParts != kNone) load_block_params(w1, p, k);
@@ -442,25 +471,25 @@ __global__ __launch_bounds__(kThreads<kLanes>, kBackWaves) void logmel_norm_back
           piece_store(q.dgate + r * q.dgates, k, sig);
       }
     }
+    if (q.part && ++held == kHeld) {
+      flush();
+      held = 0;
+    }
   }
   if (!q.part) return;
-  __shared__ float rows[kRows][kLanes * V * kVecs];
-  auto write = [&](float (&a)[kVecs][V], int which) {
-    __syncthreads();
+  flush();
+  __syncthreads();
+  for (int c = threadIdx.x; c < k.C; c += kThreads<kLanes>) {
+    int lane, value;
+    k.place(c, lane, value);
 #pragma unroll
-    for (int j = 0; j < kVecs; ++j)
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (k.counts(j, i)) rows[group_of<kLanes>()][k.c[j] + i] = a[j][i];
-    __syncthreads();
-    for (int c = threadIdx.x; c < k.C; c += kThreads<kLanes>) {
-      float s = 0.0f;
-      for (int g = 0; g < kRows; ++g) s += rows[g][c];
-      q.part[((int64_t)blockIdx.x * 2 + which) * k.C + c] = s;
+    for (int which = 0; which < 2; ++which) {
+      if (which == 0 ? kParts == kNone : !kDz) continue;
+      double s = 0.0;
+      for (int g = 0; g < kRows; ++g) s += sums[which][value][g * kLanes + lane];
+      q.part[((int64_t)blockIdx.x * 2 + which) * k.C + c] = (float)s;
     }
-  };
-  if constexpr (kParts != kNone) write(a1, 0);
-  if constexpr (kDz) write(a2, 1);
+  }
 }
 
 template <typename T>

@@ -120,3 +120,34 @@ def test_norm_of_rows_with_subnormal_mean_square(env, dtype, scale):
         r1 = 1.0 / np.sqrt((host(h) ** 2).mean(1, keepdims=True))
         parts = r1 * q + np.abs(host(h)) * r1 ** 3 * (q * np.abs(host(h))).mean(1, keepdims=True)
         check(got["dh"], val["dh"], tol["dh"] + 3 * e * parts, "dh")
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_norm_parameter_sums_over_millions_of_rows(env, dtype):
+    """The gradients of the parameters over 2^22 rows of equal values, whose
+    sums in fp32 drift by one rounding a row. Rows of ones have a mean square
+    of 1 and give dy and dz themselves as terms; a sum of up to 16 of them in
+    fp32 is off by at most half of 16 roundings and some, (16 + 2) / 2 2^-24,
+    the part of a workgroup and the result by one each."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    rows, channels = 2 ** 22, 64 if dtype == "float32" else 128
+    say(f"norm sums {dtype} {rows} x {channels}")
+    ones = torch.ones((rows, channels), dtype=getattr(torch, dtype), device=dev)
+    # 0.7 and 1.1 in fp32; in bf16 the parameter carries the digits
+    up = torch.full_like(ones, 0.7)
+    w = torch.full((channels,), 1.0, device=dev)
+    got = lm.logmel_block_norm_backward(plan, ones, w_pre=w, eps=0.0, dz=up)
+    want = rows * float(up[0, 0])
+    bound = (9 + 2) * 2.0 ** -24 * want
+    assert (got["dw_pre"].double() - want).abs().max() <= bound
+    del got
+    # t = 1 + 2^-12: a term of fp32 digits out of 2-byte rows needs the gate,
+    # whose silu is the same in every row; the sum of one row tells it
+    gate = torch.full_like(ones, 1.5)
+    kw = dict(w_post=w, scale=w, eps=0.0)
+    one = lm.logmel_block_norm_backward(plan, ones[:1], h=ones[:1], gate=gate[:1], dy=up[:1], **kw)
+    got = lm.logmel_block_norm_backward(plan, ones, h=ones, gate=gate, dy=up, **kw)
+    for k in ("dw_post", "dscale"):
+        term = one[k].double()
+        assert ((got[k].double() - rows * term).abs() <= (9 + 3) * 2.0 ** -24 * rows * term).all()
