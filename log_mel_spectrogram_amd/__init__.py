@@ -679,6 +679,10 @@ def resample(r: Resampler, samples, sample_offsets_host, stream=None):
 
 
 # ----------------------------------------------- operators over packed rows
+#
+# Plain calls, forward and gradient apart, as in the C interface: nothing is
+# recorded for torch's autograd (operands that ask for it are refused), so a
+# differentiable function is a torch.autograd.Function of the two.
 
 _ROW_TYPES: dict = {}
 
@@ -703,6 +707,16 @@ def _on_device(t, what, plan):
         raise ValueError(f"{what} must be on the plan's device {plan.device}, got {t.device}")
 
 
+def _refuse_graph(what):
+    """These calls record nothing for torch's autograd. Rather than return rows
+    that have silently lost their graph, an operand that asks for a gradient is
+    refused while graphs are recorded."""
+    if _torch().is_grad_enabled():
+        raise RuntimeError(f"{what} requires grad, and this call is not recorded by autograd: "
+                           "call it under torch.no_grad(), in a torch.autograd.Function, or "
+                           "on detached tensors (the gradients are calls of their own)")
+
+
 def _rows(t, what, like, plan):
     """(address, row stride) of a row operand [rows, channels] like ``like``;
     (None, 0) for None."""
@@ -711,6 +725,8 @@ def _rows(t, what, like, plan):
     # on the accepted path a single question; what is wrong is told apart after
     if type(t) is not type(like) or t.get_device() != plan.device:
         _on_device(t, what, plan)
+    if t.requires_grad:
+        _refuse_graph(what)
     if t is not like:
         if t.dtype != like.dtype:
             raise TypeError(f"{what} must be {like.dtype}, got {t.dtype}")
@@ -745,6 +761,8 @@ def _params(t, what, shape, plan):
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
+    if t.requires_grad:
+        _refuse_graph(what)
     return t.data_ptr() or None
 
 

@@ -151,3 +151,59 @@ def test_norm_parameter_sums_over_millions_of_rows(env, dtype):
     for k in ("dw_post", "dscale"):
         term = one[k].double()
         assert ((got[k].double() - rows * term).abs() <= (9 + 3) * 2.0 ** -24 * rows * term).all()
+
+
+def test_binding_refuses_to_lose_a_graph(env):
+    """The calls record nothing for torch's autograd: an operand that asks for
+    a gradient while graphs are recorded is refused, and runs where they are
+    not."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    x, g, dh = (torch.randn((6, 8), device=dev) for _ in range(3))
+    w = torch.nn.Parameter(torch.randn(8, device=dev))
+    leaf = x.clone().requires_grad_()
+    off = torch.tensor([0, 6], device=dev)
+    ck = torch.empty((1, 8), device=dev)
+    state = torch.zeros((1, 8), device=dev)
+
+    def calls(x, g, dh, w, state):
+        yield lambda: lm.logmel_gated_scan(plan, x, g, off, bias=w, state=state, checkpoints=ck)
+        yield lambda: lm.logmel_gated_scan_backward(plan, dh, x, g, off, ck, bias=w, state=state)[0]
+        yield lambda: lm.logmel_block_norm(plan, x, h=g, w_pre=w)[1]
+        yield lambda: lm.logmel_block_norm_backward(plan, x, h=g, w_pre=w, dz=dh)["dh"]
+
+    plain = [c() for c in calls(x, g, dh, w.detach(), state)]
+    for args in ((leaf, g, dh, w.detach(), state), (x, leaf, dh, w.detach(), state),
+                 (x, g, dh, w, state)):
+        for c in calls(*args):
+            with pytest.raises(RuntimeError, match="autograd"):
+                c()
+        with torch.no_grad():
+            got = [c() for c in calls(*args)]
+        if args[0] is x and args[1] is g:
+            assert all(torch.equal(a, b) for a, b in zip(got, plain))
+    with pytest.raises(RuntimeError, match="autograd"):
+        lm.logmel_gated_scan(plan, x, g, off, out=torch.empty_like(x).requires_grad_())
+    with pytest.raises(RuntimeError, match="autograd"):
+        lm.logmel_gated_scan(plan, x, g, off, state=state.clone().requires_grad_())
+    with pytest.raises(RuntimeError, match="autograd"):
+        lm.logmel_block_norm_backward(plan, x, dz=leaf)
+
+    class Scan(torch.autograd.Function):
+        """The two calls as one differentiable function: no graph is recorded
+        inside it."""
+
+        @staticmethod
+        def forward(ctx, x, g, b):
+            ck = torch.empty((1, 8), device=dev)
+            ctx.save_for_backward(x, g, b, ck)
+            return lm.logmel_gated_scan(plan, x, g, off, bias=b, checkpoints=ck)
+
+        @staticmethod
+        def backward(ctx, dh):
+            x, g, b, ck = ctx.saved_tensors
+            return lm.logmel_gated_scan_backward(plan, dh, x, g, off, ck, bias=b)[:3]
+
+    Scan.apply(leaf, g, w).backward(dh)
+    want = lm.logmel_gated_scan_backward(plan, dh, x, g, off, ck, bias=w.detach())
+    assert torch.equal(leaf.grad, want[0]) and torch.equal(w.grad, want[2])

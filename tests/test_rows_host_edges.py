@@ -1,6 +1,8 @@
 """Calls of the row operators that are refused on the host, beside those of
 test_rows_host.py."""
 
+import pytest
+
 from tests.test_rows_host import FAKE, _scan, _scan_in, lm   # noqa: F401
 
 
@@ -23,3 +25,14 @@ def test_scan_in_place_excuses_the_state_alone(lm):   # noqa: F811
     grad = lm.logmel_scan_grad(0x300000, 8, None, 0x310000, 8, 0x320000, 8, None, at)
     assert lm._gated_scan_backward(FAKE, _scan_in(lm, **one), 0x500000, grad, 0x400000, 1 << 30,
                                    None) == bad
+
+
+def test_binding_refuses_a_graph_only_while_one_is_recorded(lm):   # noqa: F811
+    import torch
+
+    with pytest.raises(RuntimeError, match="x requires grad.*autograd"):
+        lm._refuse_graph("x")
+    with torch.no_grad():
+        lm._refuse_graph("x")
+    with torch.inference_mode():
+        lm._refuse_graph("x")
