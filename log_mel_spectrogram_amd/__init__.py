@@ -849,18 +849,21 @@ def logmel_gated_scan(plan: Plan, x, gate, seq_offsets, bias=None, state=None, o
 
 def logmel_gated_scan_backward(plan: Plan, dh, x, gate, seq_offsets, checkpoints, bias=None,
                                state=None, dstate_out=None, dx=None, dgate=None,
-                               max_frames: int = 0, stream=None):
+                               max_frames: int = 0, stream=None, want_dstate=None):
     """Gradient of logmel_gated_scan for the same x, gate, seq_offsets, bias
     and state, from dh and dstate_out (None: 0), with the checkpoints the
     forward call wrote; returns (dx, dgate, dbias or None, dstate or None):
-    dbias where bias is given, dstate where state is. Rows from the last
-    offset on stay as they are in dx and dgate."""
+    dbias where bias is given, dstate (fp32 [n_seq, channels]) where state is,
+    or as want_dstate says. Rows from the last offset on stay as they are in dx
+    and dgate."""
     inp = _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames)
     dx = _empty(x.shape, x.dtype, x.device, stream) if dx is None else dx
     dgate = _empty(x.shape, x.dtype, x.device, stream) if dgate is None else dgate
     dbias = None if bias is None else _empty(bias.shape, bias.dtype, x.device, stream)
-    dstate = None if state is None else _empty(state.shape, state.dtype, x.device, stream)
     states = (inp.n_seq, inp.channels)
+    dstate = None
+    if (state is not None) if want_dstate is None else want_dstate:
+        dstate = _empty(states, _torch().float32, x.device, stream)
     pd, sd = _rows(dh, "dh", x, plan)
     px, sx = _rows(dx, "dx", x, plan)
     pg, sg = _rows(dgate, "dgate", x, plan)

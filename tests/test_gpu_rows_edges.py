@@ -207,3 +207,25 @@ def test_binding_refuses_to_lose_a_graph(env):
     Scan.apply(leaf, g, w).backward(dh)
     want = lm.logmel_gated_scan_backward(plan, dh, x, g, off, ck, bias=w.detach())
     assert torch.equal(leaf.grad, want[0]) and torch.equal(w.grad, want[2])
+
+
+def test_scan_gradient_of_the_state_without_a_state(env):
+    """want_dstate asks for the initial state's gradient where the state is
+    left out (0), or leaves it out where there is one."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    off = torch.tensor([0, 300, 300, 411], device=dev)
+    x, g, dh = (torch.randn((411, 66), device=dev) for _ in range(3))
+    zero = torch.zeros((3, 66), device=dev)
+    ck = torch.empty((4, 66), device=dev)
+    lm.logmel_gated_scan(plan, x, g, off, checkpoints=ck)
+    call = lm.logmel_gated_scan_backward
+    want = call(plan, dh, x, g, off, ck, state=zero)
+    got = call(plan, dh, x, g, off, ck, want_dstate=True)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(got[3], want[3])
+    _, tol = rows_ref.scan(host(x), host(g), host(off).astype(int), dh=host(dh))
+    val, _ = rows_ref.scan(host(x), host(g), host(off).astype(int), dh=host(dh))
+    check(got[3], val["dstate"], tol["dstate"], "dstate")
+    assert call(plan, dh, x, g, off, ck)[3] is None
+    assert call(plan, dh, x, g, off, ck, state=zero, want_dstate=False)[3] is None
