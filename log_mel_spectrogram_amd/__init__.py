@@ -766,6 +766,13 @@ def _params(t, what, shape, plan):
     return t.data_ptr() or None
 
 
+def _check_stream(stream, plan):
+    """Before anything is made on a caller's stream: it is the plan's device's."""
+    if stream is not None and stream.device.index != plan.device:
+        raise ValueError(f"stream must be on the plan's device {plan.device}, "
+                         f"got {stream.device}")
+
+
 def _raw_stream(stream, plan):
     """The HIP stream of a call on the plan's device (None: torch's current
     one, asked for without making a stream object)."""
@@ -833,6 +840,7 @@ def logmel_gated_scan(plan: Plan, x, gate, seq_offsets, bias=None, state=None, o
     [logmel_gated_scan_checkpoint_rows(rows), channels], receives what
     logmel_gated_scan_backward needs. max_frames (the longest sequence's rows,
     0: not known) only chooses how the work is split."""
+    _check_stream(stream, plan)
     inp = _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames)
     if out is None:
         out = _empty(x.shape, x.dtype, x.device, stream)
@@ -856,6 +864,7 @@ def logmel_gated_scan_backward(plan: Plan, dh, x, gate, seq_offsets, checkpoints
     dbias where bias is given, dstate (fp32 [n_seq, channels]) where state is,
     or as want_dstate says. Rows from the last offset on stay as they are in dx
     and dgate."""
+    _check_stream(stream, plan)
     inp = _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames)
     dx = _empty(x.shape, x.dtype, x.device, stream) if dx is None else dx
     dgate = _empty(x.shape, x.dtype, x.device, stream) if dgate is None else dgate
@@ -902,6 +911,7 @@ def logmel_block_norm(plan: Plan, res, h=None, gate=None, w_post=None, scale=Non
     contiguous rows at any row stride; w_post, scale, w_pre: fp32 [channels];
     what is None drops out. Without h, y is res and only z is formed. want_y
     and want_z False leave that output out (None)."""
+    _check_stream(stream, plan)
     inp = _norm_input(plan, res, h, gate, w_post, scale, w_pre, eps)
     if y is None and want_y and h is not None:
         y = _empty(res.shape, res.dtype, res.device, stream)
@@ -920,6 +930,7 @@ def logmel_block_norm_backward(plan: Plan, res, h=None, gate=None, w_post=None, 
     """Gradient of logmel_block_norm for the same operands, from dy and dz
     (None: 0, not both); returns a dict with dres, dh, dgate, dw_post, dscale
     and dw_pre, each None where its operand is (dw_pre also where dz is)."""
+    _check_stream(stream, plan)
     inp = _norm_input(plan, res, h, gate, w_post, scale, w_pre, eps)
 
     def rows(t, of):

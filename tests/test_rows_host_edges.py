@@ -36,3 +36,23 @@ def test_binding_refuses_a_graph_only_while_one_is_recorded(lm):   # noqa: F811
         lm._refuse_graph("x")
     with torch.inference_mode():
         lm._refuse_graph("x")
+
+
+def test_binding_refuses_a_stream_of_another_device(lm):   # noqa: F811
+    """The kernels would run on that device, with the plan's memory."""
+    import torch
+
+    class P:
+        handle, device = None, 0
+
+    class Stream:
+        cuda_stream, device = 0, torch.device("cuda", 1)
+
+    x = torch.zeros(4, 8)
+    off = torch.tensor([0, 4])
+    for call in (lambda: lm.logmel_gated_scan(P(), x, x, off, stream=Stream()),
+                 lambda: lm.logmel_gated_scan_backward(P(), x, x, x, off, x[:1], stream=Stream()),
+                 lambda: lm.logmel_block_norm(P(), x, stream=Stream()),
+                 lambda: lm.logmel_block_norm_backward(P(), x, dz=x, stream=Stream())):
+        with pytest.raises(ValueError, match="stream must be on the plan's device 0"):
+            call()
