@@ -388,7 +388,8 @@ int logmel_resample(const logmel_resampler* r, const void* d_samples, int sample
 #define LOGMEL_BF16 3 /* bfloat16, of these operators' rows only */
 
 /* The gated scan. For each sequence and channel, with a_t = sigmoid(gate_t +
- * bias) and u_t = 1 - a_t = sigmoid(-(gate_t + bias)),
+ * bias) (0 from about -87 on down, whatever the rows' type) and u_t = 1 - a_t =
+ * sigmoid(-(gate_t + bias)),
  *     h_t = a_t h_{t-1} + u_t x_t,
  * h_{-1} the sequence's row of d_state (zero if d_state is NULL).
  * Products are plain IEEE: a NaN or infinity in x or gate stays in its
@@ -406,7 +407,11 @@ typedef struct logmel_scan_input {
                                    outside the operands (LOGMEL_VALIDATE=1 checks them, with one
                                    synchronisation) */
   int64_t max_frames;           /* rows of the longest sequence, or 0 if not known: chooses how the
-                                   work is split, never what is computed */
+                                   work is split, never what is computed. 0 is taken as one
+                                   sequence of all rows, with which batches of many sequences take a
+                                   fifth to nine tenths longer: 64 x 2998 x 512 bf16 179 us instead
+                                   of 135 (gradient 283 instead of 232), 512 x 128 rows 66 instead
+                                   of 35 */
   const void* d_x;
   int64_t x_stride;
   const void* d_gate;

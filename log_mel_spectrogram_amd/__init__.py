@@ -839,7 +839,9 @@ def logmel_gated_scan(plan: Plan, x, gate, seq_offsets, bias=None, state=None, o
     after it; may be state) are fp32. checkpoints, fp32
     [logmel_gated_scan_checkpoint_rows(rows), channels], receives what
     logmel_gated_scan_backward needs. max_frames (the longest sequence's rows,
-    0: not known) only chooses how the work is split."""
+    0: not known, taken as one sequence of all rows) only chooses how the work
+    is split; without it batches of many sequences take up to nine tenths
+    longer."""
     _check_stream(stream, plan)
     inp = _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames)
     if out is None:

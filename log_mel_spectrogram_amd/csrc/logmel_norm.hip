@@ -9,10 +9,10 @@
 // its channels' parameters once, and the next rows' values are on their way
 // while a row is worked.
 //
-// Bound by memory: 64 x 2998 x 512 bf16 with gate and both outputs 186 us
-// (5.3 TB/s, the rate of a copy, traffic 1.00 x the bytes), 191,872 x 128 49 us,
-// 2998 x 4096 fp32 46 us. Small calls cost their launch: 4096 x 128 fp16 3.3 us
-// on the device, one row 2.6 us.
+// Bound by memory: 64 x 2998 x 512 bf16 with gate and both outputs 188 us
+// (5.2 TB/s, the rate of a copy, traffic 1.00 x the bytes), 191,872 x 128 42 us,
+// 2998 x 4096 fp32 46 us. Small calls cost their launch: 4096 x 128 fp16 2.9 us
+// on the device, one row 2.4 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -334,12 +334,12 @@ __global__ __launch_bounds__(kThreads<kLanes>, front_waves(kLanes)) void logmel_
 // Three sums over the row one after the other. The two sums over the lane's
 // rows stay in its registers for kHeld rows, then go to fp64 places of its own
 // in LDS; at the end the workgroup's rows are added there and each workgroup
-// writes one part. Eight values per lane keep all of
-// it within 128 registers, so that 16 wavefronts a compute unit have their
-// rows in flight. 64 x 2998 x 512 bf16: 303 us (5.2 TB/s, traffic 1.00 x); with
-// 40 values spilled to memory it took 896. 2998 x 4096 fp32 83 us. fp32 rows of
-// more than 4096 channels hold 8 values a lane in 1024 lanes and spill 20
-// (3000 x 5000 with its call 198 us, 3.9 TB/s).
+// writes one part. Eight values per lane keep all of it within 128 registers,
+// so that 16 wavefronts a compute unit have their rows in flight. 64 x 2998 x
+// 512 bf16: 302 us (5.2 TB/s, traffic 1.00 x); with 40 values spilled to memory
+// it took 896. 2998 x 4096 fp32 82 us. fp32 rows of more than 4096 channels hold
+// 8 values a lane in 1024 lanes and spill 20 (3000 x 5000 with its call 198 us,
+// 3.9 TB/s).
 template <typename T, int kParts, bool kDz, int kLanes, int kVecs, int V>
 __global__ __launch_bounds__(kThreads<kLanes>, kBackWaves) void logmel_norm_backward_kernel(
     NormArgs<T> p, NormGradArgs<T> q) {
