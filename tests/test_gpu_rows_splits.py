@@ -155,6 +155,61 @@ def test_norm_gradient_of_small_and_large_rows(env, dtype, channels):
         norm_case(env, dtype, 23, channels, "dense", eps=0.0, seed=8, scale=scale)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("block,gate,params,dy,dz", [
+    (False, False, True, False, True), (False, False, False, True, False),
+    (True, False, True, True, False), (True, True, False, True, True),
+    (True, True, True, True, False), (True, True, True, True, True)])
+def test_norm_parts_of_rows_below_16_bytes(env, dtype, block, gate, params, dy, dz):
+    """Rows of one value per lane, with several rows per lane."""
+    for channels in (1, 3, 5, 7, 8):
+        say(f"norm {dtype} {channels} block {block} gate {gate} params {params} dy {dy} dz {dz}")
+        norm_case(env, dtype, 20001 if channels == 3 else 65, channels, "odd", block, gate, params,
+                  dy, dz, seed=channels)
+
+
+def test_norm_gradients_in_a_graph(env):
+    """With and without dz, of the narrowest and the widest rows (whose sums
+    take most of a compute unit's LDS), captured together and replayed with
+    other inputs between eager calls."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    gen = torch.Generator(device=dev).manual_seed(12)
+    sets = [[torch.zeros(rows, c, dtype=dt, device=dev) for _ in range(5)]
+            for rows, c, dt in ((50000, 3, torch.float32), (700, 8192, torch.float32),
+                                (5000, 8192, torch.bfloat16))]
+
+    def fill():
+        for ops in sets:
+            for t in ops:
+                t.copy_(torch.randn(t.shape, generator=gen, device=dev))
+
+    def calls():
+        out = []
+        for res, h, gate, dy, dz in sets:
+            w = torch.ones(res.shape[1], device=dev)
+            kw = dict(h=h, gate=gate, w_post=w, scale=w)
+            for up in (dict(w_pre=w, dy=dy, dz=dz), dict(dy=dy)):
+                out += [t for t in lm.logmel_block_norm_backward(plan, res, **kw, **up).values()
+                        if t is not None]
+        return out
+
+    fill()
+    calls()
+    torch.cuda.synchronize()
+    say("capture")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = calls()
+    for rep in range(4):
+        say(f"replay {rep}")
+        fill()
+        want = calls()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 # Sequences, channels and hint of a call in parts, and of one by sequences.
 REACH = {"parts": ([300, 0, 5000, 70, 2500], 40, 0),
          "sequences": (lengths(85, 85).tolist(), 130, 700)}
