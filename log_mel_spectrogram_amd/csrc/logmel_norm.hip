@@ -161,8 +161,9 @@ struct RowSum {
 // that it is read and written whole: its first values are another lane's too,
 // who writes the same, and only the sums leave them out. Lanes past the row's
 // end hold nothing. Rows narrower than 16 bytes take V = 1, in kernels of their
-// own: as a branch beside the wide loads, their merged registers made each
-// operand's load be waited for before the next.
+// own: value by value in a branch beside the wide loads they cost every
+// gradient registers and waits (191,872 x 128 bf16 with its call 136 us, 126
+// without the branch; 3000 x 5000 fp32 255 and 211).
 template <int kLanes, int kVecs, int V>
 struct Channels {
   int C;
