@@ -367,8 +367,8 @@ int logmel_resample(const logmel_resampler* r, const void* d_samples, int sample
 
 /* ---------------------------------------------------------------------------
  * Operators over packed rows, for the layers that take the front end's rows:
- * a gated recurrence along each sequence, and the norms around a block. The
- * rows are those of logmel_compute (clip i's frames are rows
+ * a gated recurrence and linear attention along each sequence, the norms
+ * around a block, and the group norm. The rows are those of logmel_compute (clip i's frames are rows
  * [frame_offsets[i], frame_offsets[i+1])) or of a push (stream j's new frames
  * are rows [fo[j], fo[j+1])), of any width.
  *
@@ -531,6 +531,134 @@ int64_t logmel_block_norm_workspace(const logmel_plan* plan, const logmel_norm_i
 int logmel_block_norm_backward(const logmel_plan* plan, const logmel_norm_input* in,
                                const logmel_norm_grad* grad, void* d_workspace,
                                int64_t workspace_bytes, void* hip_stream);
+
+/* Linear attention with a decay for each head. For each sequence and head h,
+ * with lambda = e^log_decay[h], S a matrix of head_dk by head_dv, and q and k
+ * those of head h qk_heads / heads,
+ *     S_t = lambda S_{t-1} + k_t v_t^T,    o_t = scale q_t S_t,
+ * S_{-1} the sequence's and head's part of d_state (zero if d_state is NULL).
+ * A row operand holds its heads side by side: head h of q is columns
+ * [h head_dk, (h + 1) head_dk).
+ * A NaN or infinity in q stays in its row and head; one in k or v stays in its
+ * sequence and in the heads that read it, from its row on, where an infinity
+ * may come out as NaN. */
+#define LOGMEL_ATTENTION_MAX_HEAD_DIM 128
+typedef struct logmel_attention_input {
+  int32_t type;
+  int64_t rows;                 /* rows of the row operands */
+  int64_t heads;                /* of v, of o, of the decays and of the states */
+  int64_t qk_heads;             /* of q and k; divides heads (INVALID_ARGUMENT where not): heads
+                                   h heads / qk_heads on read the same q and k */
+  int64_t head_dk, head_dv;     /* 1..LOGMEL_ATTENTION_MAX_HEAD_DIM (UNSUPPORTED beyond) */
+  int64_t n_seq;                /* sequences, offsets and hint as logmel_scan_input's */
+  const int64_t* d_seq_offsets;
+  int64_t max_frames;
+  const void* d_q;              /* [rows][qk_heads head_dk], as k */
+  int64_t q_stride;
+  const void* d_k;
+  int64_t k_stride;
+  const void* d_v;              /* [rows][heads head_dv], as o */
+  int64_t v_stride;
+  const float* d_log_decay;     /* [heads], at most 0 (-infinity: nothing is kept; what grows
+                                   with a value above 0 may overflow). A schedule: it has no
+                                   gradient */
+  const float* d_state;         /* [n_seq][heads][head_dk][head_dv] or NULL (0) */
+  float scale;                  /* a finite number */
+} logmel_attention_input;
+
+/* Bytes of device workspace, as logmel_gated_scan_workspace. */
+int64_t logmel_linear_attention_workspace(const logmel_plan* plan,
+                                          const logmel_attention_input* in, int backward);
+
+/* Writes d_o (row operand), and d_state_out where not NULL: each sequence's
+ * last S (its initial state if it is empty), laid out as d_state; may be
+ * d_state itself. INPUT_TOO_LONG if rows * stride or the states' count
+ * overflows. */
+int logmel_linear_attention(const logmel_plan* plan, const logmel_attention_input* in, void* d_o,
+                            int64_t o_stride, float* d_state_out, void* d_workspace,
+                            int64_t workspace_bytes, void* hip_stream);
+
+/* Gradient of logmel_linear_attention for the same inputs. With T_t = lambda
+ * T_{t+1} + scale q_t do_t^T (behind a sequence's last row its part of
+ * d_dstate_out, not decayed, zero if NULL):
+ *     dq = scale S do,  dk = T v,  dv = T^T k,  dstate = lambda T_0 (of an
+ *     empty sequence: its part of dstate_out);
+ * q and k that several heads share get the sum of their heads' gradients.
+ *   d_dq, d_dk, d_dv  row outputs
+ *   d_dstate          as d_state, or NULL */
+typedef struct logmel_attention_grad {
+  const void* d_do;
+  int64_t do_stride;
+  const float* d_dstate_out;
+  void* d_dq;
+  int64_t dq_stride;
+  void* d_dk;
+  int64_t dk_stride;
+  void* d_dv;
+  int64_t dv_stride;
+  float* d_dstate;
+} logmel_attention_grad;
+int logmel_linear_attention_backward(const logmel_plan* plan, const logmel_attention_input* in,
+                                     const logmel_attention_grad* grad, void* d_workspace,
+                                     int64_t workspace_bytes, void* hip_stream);
+
+/* The group norm, channels last, with an activation and a gate. The channels
+ * are `groups` groups side by side; over a group's channels of each row
+ * (d_seq_offsets NULL), or of all rows of each sequence,
+ *     n = (x - mean) / sqrt(var + eps) * weight + bias
+ *     y = act(n) * silu(gate),    silu(g) = g sigmoid(g),
+ * var the mean square of x - mean. d_weight NULL: 1. d_bias NULL: 0. d_gate
+ * NULL: no silu factor. A NaN or infinity in x reaches what its mean does. */
+#define LOGMEL_ACT_NONE 0
+#define LOGMEL_ACT_SILU 1
+typedef struct logmel_group_norm_input {
+  int32_t type;
+  int64_t rows;
+  int64_t channels;             /* 1..LOGMEL_NORM_MAX_CHANNELS (UNSUPPORTED beyond) */
+  int64_t groups;               /* divides channels (INVALID_ARGUMENT where not) */
+  int64_t n_seq;                /* sequences, offsets and hint as logmel_scan_input's; with
+                                   d_seq_offsets NULL both are 0 */
+  const int64_t* d_seq_offsets; /* NULL: each row by itself */
+  int64_t max_frames;
+  const void* d_x;
+  int64_t x_stride;
+  const void* d_gate;
+  int64_t gate_stride;
+  const float* d_weight;        /* [channels], as the next */
+  const float* d_bias;
+  int32_t activation;           /* LOGMEL_ACT_NONE (act(n) = n) or LOGMEL_ACT_SILU */
+  float eps;                    /* a finite number >= 0 */
+} logmel_group_norm_input;
+
+/* Bytes of device workspace, as logmel_gated_scan_workspace. */
+int64_t logmel_group_norm_workspace(const logmel_plan* plan, const logmel_group_norm_input* in,
+                                    int backward);
+
+/* Writes d_y (row operand). d_stats, fp32 [n_seq][groups][2], receives each
+ * sequence's means and 1 / sqrt(var + eps), which the gradient reads; NULL
+ * where they are not wanted and where d_seq_offsets is. */
+int logmel_group_norm(const logmel_plan* plan, const logmel_group_norm_input* in, void* d_y,
+                      int64_t y_stride, float* d_stats, void* d_workspace,
+                      int64_t workspace_bytes, void* hip_stream);
+
+/* Gradient of logmel_group_norm: from d_dy the gradients of x and gate (row
+ * outputs; dgate exactly where gate is given) and of the parameters
+ * ([channels]; each may be NULL, and must be where its parameter is). d_stats
+ * as the forward call wrote it (NULL where d_seq_offsets is). Sums over rows
+ * are joined in fp64 in a fixed order. */
+typedef struct logmel_group_norm_grad {
+  const void* d_dy;
+  int64_t dy_stride;
+  void* d_dx;
+  int64_t dx_stride;
+  void* d_dgate;
+  int64_t dgate_stride;
+  float* d_dweight;
+  float* d_dbias;
+} logmel_group_norm_grad;
+int logmel_group_norm_backward(const logmel_plan* plan, const logmel_group_norm_input* in,
+                               const float* d_stats, const logmel_group_norm_grad* grad,
+                               void* d_workspace, int64_t workspace_bytes, void* hip_stream);
 
 /* Names a status code (a static string; "unknown status" for codes this
  * library does not return). Every failure is an explicit negative code and

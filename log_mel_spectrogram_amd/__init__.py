@@ -40,6 +40,9 @@ LOGMEL_BF16 = 3       # rows of the row operators only
 SCAN_CHECKPOINT = 128   # LOGMEL_SCAN_CHECKPOINT
 SCAN_MAX_CHANNELS = 1 << 26   # LOGMEL_SCAN_MAX_CHANNELS
 NORM_MAX_CHANNELS = 8192   # LOGMEL_NORM_MAX_CHANNELS
+ATTENTION_MAX_HEAD_DIM = 128   # LOGMEL_ATTENTION_MAX_HEAD_DIM
+LOGMEL_ACT_NONE = 0
+LOGMEL_ACT_SILU = 1
 N_FFT = 400
 HOP = 160
 SAMPLE_RATE = 16000
@@ -80,6 +83,32 @@ class logmel_norm_grad(ctypes.Structure):
                 ("d_dres", _p), ("dres_stride", _i64), ("d_dh", _p), ("dh_stride", _i64),
                 ("d_dgate", _p), ("dgate_stride", _i64), ("d_dw_post", _p), ("d_dscale", _p),
                 ("d_dw_pre", _p)]
+
+
+class logmel_attention_input(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("rows", _i64), ("heads", _i64), ("qk_heads", _i64),
+                ("head_dk", _i64), ("head_dv", _i64), ("n_seq", _i64), ("d_seq_offsets", _p),
+                ("max_frames", _i64), ("d_q", _p), ("q_stride", _i64), ("d_k", _p),
+                ("k_stride", _i64), ("d_v", _p), ("v_stride", _i64), ("d_log_decay", _p),
+                ("d_state", _p), ("scale", ctypes.c_float)]
+
+
+class logmel_attention_grad(ctypes.Structure):
+    _fields_ = [("d_do", _p), ("do_stride", _i64), ("d_dstate_out", _p), ("d_dq", _p),
+                ("dq_stride", _i64), ("d_dk", _p), ("dk_stride", _i64), ("d_dv", _p),
+                ("dv_stride", _i64), ("d_dstate", _p)]
+
+
+class logmel_group_norm_input(ctypes.Structure):
+    _fields_ = [("type", ctypes.c_int32), ("rows", _i64), ("channels", _i64), ("groups", _i64),
+                ("n_seq", _i64), ("d_seq_offsets", _p), ("max_frames", _i64), ("d_x", _p),
+                ("x_stride", _i64), ("d_gate", _p), ("gate_stride", _i64), ("d_weight", _p),
+                ("d_bias", _p), ("activation", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class logmel_group_norm_grad(ctypes.Structure):
+    _fields_ = [("d_dy", _p), ("dy_stride", _i64), ("d_dx", _p), ("dx_stride", _i64),
+                ("d_dgate", _p), ("dgate_stride", _i64), ("d_dweight", _p), ("d_dbias", _p)]
 
 
 def _sig(name, res, *args):
@@ -142,6 +171,18 @@ _block_norm = _sig("logmel_block_norm", ctypes.c_int, _p, _norm_in_p, _p, _i64, 
 _block_norm_workspace = _sig("logmel_block_norm_workspace", _i64, _p, _norm_in_p)
 _block_norm_backward = _sig("logmel_block_norm_backward", ctypes.c_int, _p, _norm_in_p,
                             ctypes.POINTER(logmel_norm_grad), _p, _i64, _p)
+_attn_in_p = ctypes.POINTER(logmel_attention_input)
+_group_in_p = ctypes.POINTER(logmel_group_norm_input)
+_linear_attention_workspace = _sig("logmel_linear_attention_workspace", _i64, _p, _attn_in_p,
+                                   ctypes.c_int)
+_linear_attention = _sig("logmel_linear_attention", ctypes.c_int, _p, _attn_in_p, _p, _i64, _p,
+                         _p, _i64, _p)
+_linear_attention_backward = _sig("logmel_linear_attention_backward", ctypes.c_int, _p,
+                                  _attn_in_p, ctypes.POINTER(logmel_attention_grad), _p, _i64, _p)
+_group_norm_workspace = _sig("logmel_group_norm_workspace", _i64, _p, _group_in_p, ctypes.c_int)
+_group_norm = _sig("logmel_group_norm", ctypes.c_int, _p, _group_in_p, _p, _i64, _p, _p, _i64, _p)
+_group_norm_backward = _sig("logmel_group_norm_backward", ctypes.c_int, _p, _group_in_p, _p,
+                            ctypes.POINTER(logmel_group_norm_grad), _p, _i64, _p)
 
 EXPORTED = [
     "logmel_default_config", "logmel_abi_version", "logmel_status_string",
@@ -156,7 +197,9 @@ EXPORTED = [
     "logmel_resampler_info", "logmel_resample", "logmel_stream_push_static",
     "logmel_gated_scan_checkpoint_rows", "logmel_gated_scan_workspace", "logmel_gated_scan",
     "logmel_gated_scan_backward", "logmel_block_norm", "logmel_block_norm_workspace",
-    "logmel_block_norm_backward",
+    "logmel_block_norm_backward", "logmel_linear_attention_workspace",
+    "logmel_linear_attention", "logmel_linear_attention_backward", "logmel_group_norm_workspace",
+    "logmel_group_norm", "logmel_group_norm_backward",
 ]
 
 STATIC_MAX_STREAMS = 512   # LOGMEL_STATIC_MAX_STREAMS
@@ -801,13 +844,9 @@ def _workspace(need, device, stream, what):
     return ws, ws.data_ptr()
 
 
-def _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames):
+def _sequences(seq_offsets, plan):
+    """(sequences, address) of the offsets of a call along sequences."""
     torch = _torch()
-    _on_device(x, "x", plan)
-    ty = _row_type(x.dtype)
-    px, sx = _rows(x, "x", x, plan)
-    pg, sg = _rows(gate, "gate", x, plan)
-    rows, channels = x.shape
     if type(seq_offsets) is not torch.Tensor or seq_offsets.get_device() != plan.device:
         _on_device(seq_offsets, "seq_offsets", plan)
     if seq_offsets.dtype != torch.int64:
@@ -815,7 +854,16 @@ def _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames):
     n_seq = seq_offsets.numel() - 1
     if seq_offsets.dim() != 1 or n_seq < 0 or not seq_offsets.is_contiguous():
         raise ValueError("seq_offsets must be contiguous with n_seq + 1 entries")
-    po = seq_offsets.data_ptr()
+    return n_seq, seq_offsets.data_ptr()
+
+
+def _scan_input(plan, x, gate, seq_offsets, bias, state, max_frames):
+    _on_device(x, "x", plan)
+    ty = _row_type(x.dtype)
+    px, sx = _rows(x, "x", x, plan)
+    pg, sg = _rows(gate, "gate", x, plan)
+    rows, channels = x.shape
+    n_seq, po = _sequences(seq_offsets, plan)
     return logmel_scan_input(ty, rows, channels, n_seq, po, int(max_frames), px, sx, pg, sg,
                              _params(bias, "bias", (channels,), plan),
                              _params(state, "state", (n_seq, channels), plan))
@@ -961,3 +1009,178 @@ def logmel_block_norm_backward(plan: Plan, res, h=None, gate=None, w_post=None, 
                                 _raw_stream(stream, plan)),
            "logmel_block_norm_backward")
     return out
+
+
+def _head_width(t, what, heads, rows, dtype, plan):
+    """(address, row stride, head width) of a row operand that holds ``heads``
+    heads side by side."""
+    _on_device(t, what, plan)
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    p, stride = _rows(t, what, t, plan)
+    if t.shape[0] != rows:
+        raise ValueError(f"{what} must have {rows} rows, got {list(t.shape)}")
+    width = t.shape[1]
+    if width == 0 or width % heads:
+        raise ValueError(f"{what} must hold {heads} heads side by side, got {list(t.shape)}")
+    return p, stride, width // heads
+
+
+def _attention_input(plan, q, k, v, log_decay, seq_offsets, qk_heads, scale, state, max_frames):
+    torch = _torch()
+    _on_device(q, "q", plan)
+    ty = _row_type(q.dtype)
+    if type(log_decay) is not torch.Tensor or log_decay.dim() != 1 or log_decay.numel() == 0:
+        raise ValueError("log_decay must be a tensor [heads]")
+    heads = log_decay.shape[0]
+    pg = _params(log_decay, "log_decay", (heads,), plan)
+    qk_heads = heads if qk_heads is None else int(qk_heads)
+    if qk_heads < 1 or heads % qk_heads:
+        raise ValueError(f"qk_heads must divide the {heads} heads, got {qk_heads}")
+    pq, sq, dk = _head_width(q, "q", qk_heads, q.shape[0] if q.dim() else 0, q.dtype, plan)
+    rows = q.shape[0]
+    pk, sk = _rows(k, "k", q, plan)
+    pv, sv, dv = _head_width(v, "v", heads, rows, q.dtype, plan)
+    n_seq, po = _sequences(seq_offsets, plan)
+    return logmel_attention_input(ty, rows, heads, qk_heads, dk, dv, n_seq, po, int(max_frames),
+                                  pq, sq, pk, sk, pv, sv, pg,
+                                  _params(state, "state", (n_seq, heads, dk, dv), plan),
+                                  float(scale))
+
+
+def logmel_linear_attention(plan: Plan, q, k, v, log_decay, seq_offsets, qk_heads=None,
+                            scale: float = 1.0, state=None, out=None, state_out=None,
+                            max_frames: int = 0, stream=None):
+    """S_t = e^log_decay S_{t-1} + k_t v_t^T and o_t = scale q_t S_t, along each
+    packed sequence and for each head; returns o [rows, heads * dv].
+
+    q, k: [rows, qk_heads * dk], v (and out): [rows, heads * dv], heads side by
+    side, float32, float16 or bfloat16 with contiguous rows at any row stride;
+    dk and dv at most ATTENTION_MAX_HEAD_DIM. log_decay: fp32 [heads], at most 0;
+    it has no gradient. qk_heads (default: heads) divides heads; heads / qk_heads
+    neighbouring heads read the same q and k. seq_offsets and max_frames as in
+    logmel_gated_scan; rows from the last offset on stay as they are in out.
+    state (S before each sequence, default 0) and state_out (S after it; may be
+    state): fp32 [n_seq, heads, dk, dv]."""
+    _check_stream(stream, plan)
+    inp = _attention_input(plan, q, k, v, log_decay, seq_offsets, qk_heads, scale, state,
+                           max_frames)
+    if out is None:
+        out = _empty(v.shape, v.dtype, v.device, stream)
+    po, so = _rows(out, "out", v, plan)
+    pso = _params(state_out, "state_out", (inp.n_seq, inp.heads, inp.head_dk, inp.head_dv), plan)
+    need = _linear_attention_workspace(plan.handle, inp, 0)
+    ws, pws = _workspace(need, q.device, stream, "logmel_linear_attention")
+    _check(_linear_attention(plan.handle, inp, po, so, pso, pws, need,
+                             _raw_stream(stream, plan)), "logmel_linear_attention")
+    return out
+
+
+def logmel_linear_attention_backward(plan: Plan, dout, q, k, v, log_decay, seq_offsets,
+                                     qk_heads=None, scale: float = 1.0, state=None,
+                                     dstate_out=None, dq=None, dk=None, dv=None,
+                                     max_frames: int = 0, stream=None, want_dstate=None):
+    """Gradient of logmel_linear_attention for the same operands, from dout
+    (that of its result) and dstate_out (None: 0); returns (dq, dk, dv, dstate
+    or None): dstate (fp32, like state) where state is given, or as want_dstate
+    says. Rows from the last offset on stay as they are in dq, dk and dv."""
+    _check_stream(stream, plan)
+    inp = _attention_input(plan, q, k, v, log_decay, seq_offsets, qk_heads, scale, state,
+                           max_frames)
+    dq = _empty(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _empty(q.shape, q.dtype, q.device, stream) if dk is None else dk
+    dv = _empty(v.shape, v.dtype, v.device, stream) if dv is None else dv
+    states = (inp.n_seq, inp.heads, inp.head_dk, inp.head_dv)
+    dstate = None
+    if (state is not None) if want_dstate is None else want_dstate:
+        dstate = _empty(states, _torch().float32, q.device, stream)
+    grad = logmel_attention_grad(*_rows(dout, "dout", v, plan),
+                                 _params(dstate_out, "dstate_out", states, plan),
+                                 *_rows(dq, "dq", q, plan), *_rows(dk, "dk", q, plan),
+                                 *_rows(dv, "dv", v, plan),
+                                 _params(dstate, "dstate", states, plan))
+    need = _linear_attention_workspace(plan.handle, inp, 1)
+    ws, pws = _workspace(need, q.device, stream, "logmel_linear_attention_backward")
+    _check(_linear_attention_backward(plan.handle, inp, grad, pws, need,
+                                      _raw_stream(stream, plan)),
+           "logmel_linear_attention_backward")
+    return dq, dk, dv, dstate
+
+
+_ACTIVATIONS = {None: LOGMEL_ACT_NONE, "silu": LOGMEL_ACT_SILU}
+
+
+def _group_input(plan, x, groups, weight, bias, gate, activation, seq_offsets, eps, max_frames):
+    _on_device(x, "x", plan)
+    ty = _row_type(x.dtype)
+    px, sx = _rows(x, "x", x, plan)
+    rows, channels = x.shape
+    pg, sg = _rows(gate, "gate", x, plan)
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None or 'silu', got {activation!r}")
+    groups = int(groups)
+    if groups < 1 or channels % groups:
+        raise ValueError(f"groups must divide the {channels} channels, got {groups}")
+    n_seq, po = (0, None) if seq_offsets is None else _sequences(seq_offsets, plan)
+    return logmel_group_norm_input(ty, rows, channels, groups, n_seq, po, int(max_frames), px, sx,
+                                   pg, sg, _params(weight, "weight", (channels,), plan),
+                                   _params(bias, "bias", (channels,), plan),
+                                   _ACTIVATIONS[activation], float(eps))
+
+
+def logmel_group_norm(plan: Plan, x, groups: int, weight=None, bias=None, gate=None,
+                      activation=None, seq_offsets=None, eps: float = 1e-5, out=None, stats=None,
+                      max_frames: int = 0, stream=None):
+    """y = act((x - mean) / sqrt(var + eps) * weight + bias) * silu(gate), mean
+    and var over each of ``groups`` groups of neighbouring channels: of each
+    row, or with seq_offsets of all rows of each packed sequence; returns y.
+
+    x, gate (and out): [rows, channels] float32, float16 or bfloat16 with
+    contiguous rows at any row stride; weight, bias: fp32 [channels]; what is
+    None drops out. activation: None or "silu". seq_offsets and max_frames as in
+    logmel_gated_scan; rows from the last offset on stay as they are in out.
+    stats, fp32 [n_seq, groups, 2], receives what the gradient over sequences
+    reads."""
+    _check_stream(stream, plan)
+    inp = _group_input(plan, x, groups, weight, bias, gate, activation, seq_offsets, eps,
+                       max_frames)
+    if out is None:
+        out = _empty(x.shape, x.dtype, x.device, stream)
+    po, so = _rows(out, "out", x, plan)
+    pst = _params(stats, "stats", (inp.n_seq, inp.groups, 2), plan)
+    need = _group_norm_workspace(plan.handle, inp, 0)
+    ws, pws = _workspace(need, x.device, stream, "logmel_group_norm")
+    _check(_group_norm(plan.handle, inp, po, so, pst, pws, need, _raw_stream(stream, plan)),
+           "logmel_group_norm")
+    return out
+
+
+def logmel_group_norm_backward(plan: Plan, dy, x, groups: int, stats=None, weight=None, bias=None,
+                               gate=None, activation=None, seq_offsets=None, eps: float = 1e-5,
+                               dx=None, dgate=None, max_frames: int = 0, stream=None):
+    """Gradient of logmel_group_norm for the same operands, from dy; returns a
+    dict with dx, dgate, dweight and dbias, each None where its operand is. stats
+    as the forward call wrote it, exactly where seq_offsets is given."""
+    _check_stream(stream, plan)
+    inp = _group_input(plan, x, groups, weight, bias, gate, activation, seq_offsets, eps,
+                       max_frames)
+    if dx is None:
+        dx = _empty(x.shape, x.dtype, x.device, stream)
+    if dgate is None and gate is not None:
+        dgate = _empty(x.shape, x.dtype, x.device, stream)
+    # the parameters' gradients are rows of one tensor
+    wanted = [k for k, of in (("dweight", weight), ("dbias", bias)) if of is not None]
+    params = dict.fromkeys(("dweight", "dbias"))
+    if wanted:
+        flat = _empty((len(wanted), inp.channels), _torch().float32, x.device, stream)
+        params.update(zip(wanted, flat.unbind(0)))
+    pst = _params(stats, "stats", (inp.n_seq, inp.groups, 2), plan)
+    grad = logmel_group_norm_grad(*_rows(dy, "dy", x, plan), *_rows(dx, "dx", x, plan),
+                                  *_rows(dgate, "dgate", x, plan),
+                                  *(_params(params[k], k, (inp.channels,), plan)
+                                    for k in ("dweight", "dbias")))
+    need = _group_norm_workspace(plan.handle, inp, 1)
+    ws, pws = _workspace(need, x.device, stream, "logmel_group_norm_backward")
+    _check(_group_norm_backward(plan.handle, inp, pst, grad, pws, need,
+                                _raw_stream(stream, plan)), "logmel_group_norm_backward")
+    return dict(dx=dx, dgate=dgate, **params)

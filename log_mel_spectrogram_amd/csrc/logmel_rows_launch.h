@@ -22,6 +22,20 @@ hipError_t logmel_launch_norm(const logmel_norm_input& in, void* y, int64_t y_st
 hipError_t logmel_launch_norm_backward(const logmel_norm_input& in, const logmel_norm_grad& grad,
                                        void* ws, int cus, hipStream_t stream);
 
+int64_t logmel_attention_workspace(const logmel_attention_input& in, int backward, int cus);
+hipError_t logmel_launch_attention(const logmel_attention_input& in, void* o, int64_t o_stride,
+                                   float* state_out, void* ws, int cus, hipStream_t stream);
+hipError_t logmel_launch_attention_backward(const logmel_attention_input& in,
+                                            const logmel_attention_grad& grad, void* ws, int cus,
+                                            hipStream_t stream);
+
+int64_t logmel_group_workspace(const logmel_group_norm_input& in, int backward, int cus);
+hipError_t logmel_launch_group(const logmel_group_norm_input& in, void* y, int64_t y_stride,
+                               float* stats, void* ws, int cus, hipStream_t stream);
+hipError_t logmel_launch_group_backward(const logmel_group_norm_input& in, const float* stats,
+                                        const logmel_group_norm_grad& grad, void* ws, int cus,
+                                        hipStream_t stream);
+
 // One sum of a launch: out[c] = factor[c] times the sum over g of
 // part[g][which][c], part being [parts][sums][channels]; factor null: 1, out
 // null: left out.

@@ -1,0 +1,344 @@
+"""Linear attention on the GPU, with its gradient, against the fp64 form of
+attn_ref.py, whose bounds follow from the number of roundings."""
+
+import numpy as np
+import pytest
+
+from tests import attn_ref
+from tests.test_gpu_rows import DTYPES, Rows, check, env, host, say  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def untouched(torch, t):
+    """Values around a row operand's own, as Rows made them."""
+    base = t._base if t._base is not None else t
+    whole = base.flatten().clone()
+    at = torch.as_strided(torch.arange(whole.numel(), device=t.device), t.shape, t.stride(),
+                          t.storage_offset())
+    whole[at.reshape(-1)] = 7.0
+    return bool((whole == 7.0).all())
+
+
+def decays(heads, kind):
+    if kind == "steps":      # memories of two to two hundred rows
+        return -np.exp2(-8.0 * np.arange(1, heads + 1) / heads)
+    return np.array([0.0, -np.inf, -3.0, -1e-4, -40.0, -1e30] * heads)[:heads]   # extremes
+
+
+def attn_case(env, dtype, lens, heads=2, qk=2, dk=64, dv=64, layout="dense", state=True, behind=0,
+              max_frames=0, seed=0, kind="steps", scale=None, train=True, in_place=False):
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    rows, n, last = int(off[-1]) + behind, len(lens), int(off[-1])
+    mq = Rows(torch, dtype, rows, qk * dk, layout, seed)
+    mv = Rows(torch, dtype, rows, heads * dv, layout, seed + 1000)
+    q, k, v, do = mq.normal(), mq.normal(), mv.normal(), mv.normal()
+    rng = mq.rng
+    scale = dk ** -0.5 if scale is None else scale
+
+    def f32(*shape):
+        return torch.from_numpy(rng.normal(size=shape).astype(np.float32)).to(dev)
+
+    g = torch.from_numpy(decays(heads, kind).astype(np.float32)).to(dev)
+    s0 = f32(n, heads, dk, dv) if state else None
+    dso = f32(n, heads, dk, dv) if state else None
+    off_d = torch.from_numpy(off).to(dev)
+    o, dq, dkk, dvv = mv.empty(), mq.empty(), mq.empty(), mv.empty()
+    so = s0.clone() if in_place else torch.full((n, heads, dk, dv), 7.0, device=dev)
+    more = dict(qk_heads=qk, scale=scale, max_frames=max_frames)
+    lm.logmel_linear_attention(plan, q, k, v, g, off_d, state=so if in_place else s0, out=o,
+                               state_out=so, **more)
+    got = dict(o=o, state_out=so)
+    if train:
+        _, _, _, ds = lm.logmel_linear_attention_backward(
+            plan, do, q, k, v, g, off_d, state=s0, dstate_out=dso, dq=dq, dk=dkk, dv=dvv, **more)
+        got.update(dq=dq, dk=dkk, dv=dvv)
+        if state:
+            got["dstate"] = ds
+    torch.cuda.synchronize()
+    val, tol = attn_ref.attention(
+        host(q), host(k), host(v), host(g), off, qk, scale, None if s0 is None else host(s0),
+        host(do) if train else None, None if dso is None else host(dso), dtype=dtype)
+    for name, t in got.items():
+        if name in ("o", "dq", "dk", "dv"):
+            check(t[:last], val[name][:last], tol[name][:last], name)
+            assert (t[last:] == 7.0).all(), name
+            if layout != "dense":
+                assert untouched(torch, t), name
+        else:
+            check(t, val[name], tol[name], name)
+
+
+SEQS = {
+    "one": [1],
+    "empty_around": [0, 1, 0, 0, 5, 0],
+    "ones": [1] * 70,
+    "edges": [31, 1, 32, 33, 0, 64, 63, 65, 127, 128, 129, 3],
+    "ragged": [300, 2, 0, 233, 41],
+    "long": [1500],
+}
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("seqs", sorted(SEQS))
+def test_attention_lengths(env, dtype, seqs):
+    lens = SEQS[seqs]
+    for max_frames in (0, max(lens)):
+        say(f"attention {dtype} {seqs} max_frames {max_frames}")
+        attn_case(env, dtype, lens, behind=5, max_frames=max_frames)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("layout", ["dense", "slice", "odd"])
+@pytest.mark.parametrize("dk,dv", [(1, 1), (3, 130 - 2), (128, 2), (40, 71), (64, 32), (33, 65),
+                                   (128, 128), (16, 48)])
+def test_attention_widths(env, dtype, layout, dk, dv):
+    for max_frames in (0, 11):
+        say(f"attention {dtype} {layout} {dk} x {dv} max_frames {max_frames}")
+        lens = [150, 0, 77] if max_frames == 0 else [11, 0, 9, 1]
+        attn_case(env, dtype, lens, dk=dk, dv=dv, layout=layout, behind=2, seed=dk,
+                  state=layout != "slice", max_frames=max_frames)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("heads,qk", [(1, 1), (3, 1), (6, 2), (5, 5), (8, 4)])
+def test_attention_heads(env, dtype, heads, qk):
+    say(f"attention {dtype} {heads} heads, {qk} of q and k")
+    attn_case(env, dtype, [90, 3, 0, 70], heads=heads, qk=qk, dk=24, dv=40, behind=3, seed=heads)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lens", [[1, 0, 7], [200, 5, 0, 130]])
+def test_attention_extreme_decays(env, dtype, lens):
+    """Nothing kept, everything kept, and decays whose powers underflow."""
+    say(f"attention extremes {dtype} {lens}")
+    attn_case(env, dtype, lens, heads=6, qk=6, dk=32, dv=32, kind="extremes", seed=3)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lens", [[1, 0, 8, 3], [700, 0, 40]])
+def test_attention_state_in_place(env, dtype, lens):
+    for max_frames in (0, max(lens)):
+        say(f"attention in place {dtype} {lens} {max_frames}")
+        attn_case(env, dtype, lens, train=False, in_place=True, max_frames=max_frames, seed=4)
+
+
+@pytest.mark.parametrize("scale", [0.0, -2.5])
+def test_attention_scales(env, scale):
+    say(f"attention scale {scale}")
+    attn_case(env, "float32", [70, 3], scale=scale, seed=5)
+
+
+@pytest.mark.parametrize("max_frames", [1, 20, 1 << 40])
+def test_attention_wrong_hint_changes_no_result(env, max_frames):
+    say(f"attention hint {max_frames}")
+    for n in (1, 30):
+        attn_case(env, "bfloat16", [170, 3, 0, 65] * n, dk=32, dv=32, max_frames=max_frames,
+                  seed=6)
+
+
+def test_attention_no_sequences_and_no_rows(env):
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say("attention of nothing")
+    q = torch.full((4, 16), 3.0, device=dev)
+    g = torch.zeros(2, device=dev)
+    o = torch.full((4, 16), 7.0, device=dev)
+    lm.logmel_linear_attention(plan, q, q, q, g, torch.zeros(1, dtype=torch.int64, device=dev),
+                               out=o)
+    assert (o == 7.0).all()
+    e = q[:0]
+    s = torch.randn((3, 2, 8, 8), device=dev)
+    so, ds = torch.empty_like(s), None
+    off = torch.zeros(4, dtype=torch.int64, device=dev)
+    lm.logmel_linear_attention(plan, e, e, e, g, off, state=s, state_out=so)
+    _, _, _, ds = lm.logmel_linear_attention_backward(plan, e, e, e, e, g, off, state=s,
+                                                      dstate_out=s)
+    assert torch.equal(so, s) and torch.equal(ds, s)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("max_frames", [0, 100])
+def test_attention_not_finite_stays_behind(env, dtype, max_frames):
+    """A NaN or infinity in q reaches its row and head; one in k or v its
+    sequence and head from its row on: earlier rows keep every bit."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say(f"attention not finite {dtype} {max_frames}")
+    dt = getattr(torch, dtype)
+    rows, heads, d = 300, 3, 32
+    gen = torch.Generator(device=dev).manual_seed(7)
+    q, k, v = (torch.randn((rows, heads * d), generator=gen, device=dev).to(dt) for _ in range(3))
+    off = torch.tensor([0, 100, 200, 300], device=dev)
+    g = torch.tensor([-0.1, -0.01, -1.0], device=dev)
+
+    def call():
+        return lm.logmel_linear_attention(plan, q, k, v, g, off, max_frames=max_frames)
+
+    o = call().clone()
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for x, row, head, whole in ((q, 130, 1, False), (k, 137, 0, True), (v, 190, 2, True),
+                                    (v, 100, 1, True), (k, 163, 1, True)):
+            keep = x[row, head * d + 5].clone()
+            x[row, head * d + 5] = bad
+            b = call()
+            x[row, head * d + 5] = keep
+            same = torch.ones_like(o, dtype=torch.bool)
+            same[row:200 if whole else row + 1, head * d:(head + 1) * d] = False
+            assert torch.equal(b[same], o[same]), (bad, row, head)
+            at = b[row, head * d:(head + 1) * d]
+            assert not torch.isfinite(at).all(), (bad, row, head)
+            if whole:
+                assert not torch.isfinite(b[199, head * d:(head + 1) * d]).all()
+    assert torch.equal(call(), o)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_attention_pushes_equal_the_whole(env, dtype):
+    """Streams fed row by row, then in pushes, with the state carried in place:
+    the rows of the whole sequences, within the bounds of both."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say(f"attention pushes {dtype}")
+    n, total, heads, dk, dv = 5, 50, 2, 24, 40
+    rng = np.random.default_rng(8)
+    dt = getattr(torch, dtype)
+    q, k = (torch.from_numpy(rng.normal(size=(n, total, heads * dk))).to(dt) for _ in range(2))
+    v = torch.from_numpy(rng.normal(size=(n, total, heads * dv))).to(dt)
+    g = -np.array([0.3, 0.02])
+    gd = torch.from_numpy(g.astype(np.float32)).to(dev)
+    state = torch.zeros((n, heads, dk, dv), device=dev)
+    got = []
+    at = 0
+    for push in [1, 1, 1, 8, 8, 1, 30]:
+        rows = [x[:, at:at + push].reshape(n * push, -1).to(dev) for x in (q, k, v)]
+        off = torch.arange(n + 1, device=dev) * push
+        o = lm.logmel_linear_attention(plan, *rows, gd, off, state=state, state_out=state,
+                                       max_frames=push)
+        got.append(o.view(n, push, -1))
+        at += push
+    flat = [x.reshape(n * total, -1) for x in (q, k, v)]
+    val, tol = attn_ref.attention(*(host(x) for x in flat), g.astype(np.float32),
+                                  np.arange(n + 1) * total, heads, 1.0, dtype=dtype)
+    check(torch.cat(got, 1).reshape(n * total, -1), val["o"], tol["o"], "o")
+    check(state, val["state_out"], tol["state_out"], "state")
+
+
+@pytest.mark.parametrize("dtype", ["float32", "float16"])
+@pytest.mark.parametrize("lens,max_frames", [([3, 8, 1], 8), ([200, 70, 0, 130], 0)])
+def test_attention_same_bits_other_stream_and_graph(env, dtype, lens, max_frames):
+    """The same call gives the same bits, on another stream and replayed from
+    a graph with the program's own work between the replays."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say(f"attention graph {dtype} {lens}")
+    dt = getattr(torch, dtype)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), device=dev)
+    rows, heads, dk, dv = int(sum(lens)), 4, 40, 72
+    gen = torch.Generator(device=dev).manual_seed(9)
+    q, k = (torch.randn((rows, 2 * dk), generator=gen, device=dev).to(dt) for _ in range(2))
+    v, do = (torch.randn((rows, heads * dv), generator=gen, device=dev).to(dt) for _ in range(2))
+    g = -torch.rand(heads, generator=gen, device=dev)
+    s0 = torch.randn((len(lens), heads, dk, dv), generator=gen, device=dev)
+
+    def call(stream=None):
+        so = torch.empty_like(s0)
+        more = dict(qk_heads=2, state=s0, max_frames=max_frames, stream=stream)
+        o = lm.logmel_linear_attention(plan, q, k, v, g, off, state_out=so, **more)
+        return [o, so, *lm.logmel_linear_attention_backward(plan, do, q, k, v, g, off,
+                                                            dstate_out=s0, **more)]
+
+    first = [t.clone() for t in call()]
+    assert all(torch.equal(a, b) for a, b in zip(first, call()))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    other = call(side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(first, other))
+    graph, graph2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = call()
+    with torch.cuda.graph(graph2):
+        held2 = call()
+    for _ in range(3):
+        for t in held + held2:
+            t.fill_(3.0)
+        graph.replay()
+        graph2.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, held))
+        assert all(torch.equal(a, b) for a, b in zip(first, held2))
+        assert all(torch.equal(a, b) for a, b in zip(first, call()))
+    v.mul_(2.0)
+    graph.replay()
+    again = call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(held, again))
+
+
+def test_attention_many_sequences(env):
+    """Tens of thousands of short sequences, with and without the hint."""
+    lens = np.random.default_rng(10).integers(0, 4, size=20000).tolist()
+    for max_frames in (0, 3):
+        say(f"attention 20,000 sequences max_frames {max_frames}")
+        attn_case(env, "bfloat16", lens, heads=1, qk=1, dk=8, dv=8, max_frames=max_frames,
+                  behind=1, seed=11)
+
+
+def test_attention_offsets_past_32_bits(env):
+    """Rows whose elements lie past 2^31, against the last rows by themselves."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say("attention past 2^31 elements")
+    rows, wide, d = 70_000, 32_768, 32
+    big = torch.zeros((rows, wide), dtype=torch.bfloat16, device=dev)
+    gen = torch.Generator(device=dev).manual_seed(12)
+    q, k, v = big[:, :d], big[:, wide - d:], big[:, 64:64 + d]
+    small = [torch.randn((300, d), generator=gen, device=dev).to(torch.bfloat16) for _ in range(4)]
+    for x, s in zip((q, k, v), small):
+        x[-300:] = s
+    out = big[:, 1024:1024 + d]
+    g = torch.tensor([-0.05], device=dev)
+    off, off_s = (torch.tensor([0, n], device=dev) for n in (rows, 300))
+    lm.logmel_linear_attention(plan, q, k, v, g, off, out=out)
+    val, tol = attn_ref.attention(*(host(s) for s in small[:3]), host(g), np.array([0, 300]), 1,
+                                  1.0, dtype="bfloat16")
+    check(out[-300:], val["o"], tol["o"], "o")
+    assert (out[:-300] == 0).all()
+    do = big[:, 2048:2048 + d]
+    do[-300:] = small[3]
+    dq, dk, dv, _ = lm.logmel_linear_attention_backward(plan, do, q, k, v, g, off)
+    val, tol = attn_ref.attention(*(host(s) for s in small[:3]), host(g), np.array([0, 300]), 1,
+                                  1.0, do=host(small[3]), dtype="bfloat16")
+    for name, t in dict(dq=dq, dk=dk, dv=dv).items():
+        check(t[-300:], val[name], tol[name], name)
+
+
+def test_attention_refusals_of_the_binding(env):
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say("attention refusals")
+    q, g = torch.zeros((4, 16), device=dev), torch.zeros(2, device=dev)
+    off = torch.tensor([0, 4], device=dev)
+
+    def call(**kw):
+        d = dict(q=q, k=q, v=q, log_decay=g, seq_offsets=off)
+        d.update(kw)
+        more = {k: d.pop(k) for k in list(d) if k not in ("q", "k", "v", "log_decay",
+                                                          "seq_offsets")}
+        return lm.logmel_linear_attention(plan, d["q"], d["k"], d["v"], d["log_decay"],
+                                          d["seq_offsets"], **more)
+
+    call()
+    for kw in (dict(k=q[:3]), dict(k=q[:, :8]), dict(v=q[:3]), dict(v=q[:, :15]),
+               dict(q=q[:, ::2]), dict(log_decay=g[:0]), dict(log_decay=g.view(1, 2)),
+               dict(log_decay=g.cpu()), dict(qk_heads=3), dict(qk_heads=0),
+               dict(state=torch.zeros((1, 2, 8, 9), device=dev)),
+               dict(out=q), dict(seq_offsets=off.int()), dict(log_decay=g.double()),
+               dict(k=q.half()), dict(v=q.half()), dict(scale=float("nan")),
+               dict(log_decay=torch.zeros(2, device=dev, requires_grad=True)),
+               dict(v=torch.zeros((4, 16), device=dev, requires_grad=True))):
+        with pytest.raises((ValueError, TypeError, RuntimeError)):
+            call(**kw)
