@@ -55,6 +55,22 @@ __device__ __forceinline__ Run run_of(const AttnJob<T>& p, int64_t i) {
   return {from, to};
 }
 
+// lambda^n as a sum of two fp32: a state decays through many chunks by the same
+// factor, whose own rounding would grow with them.
+struct Decay {
+  float hi, lo;
+};
+__device__ __forceinline__ Decay decay_of(float g, float n) {
+  if (n == 0.0f) return {1.0f, 0.0f};
+  const float e = expm1f(g * n);
+  if (!(e > -0.5f)) return {expf(g * n), 0.0f};
+  const float hi = 1.0f + e;
+  return {hi, e - (hi - 1.0f)};
+}
+__device__ __forceinline__ float decayed(Decay d, float x) {
+  return __builtin_fmaf(d.lo, x, d.hi * x);
+}
+
 // ------------------------------------------------------- row after row
 //
 // A workgroup holds the 64 columns of a sequence's and head's state that one
@@ -80,7 +96,7 @@ __global__ __launch_bounds__(256) void logmel_attn_rows_kernel(AttnJob<T> p, int
     const int64_t seq = item / slabs / p.heads;
     const Run run = run_of(p, seq);
     const int c0 = slab * kSlab;
-    const float lambda = __expf(p.log_decay[h]);
+    const Decay lambda = decay_of(p.log_decay[h], 1.0f);
     const float* in = p.state ? p.state + (seq * p.heads + h) * p.da * p.dc : nullptr;
     float* out = p.state_out ? p.state_out + (seq * p.heads + h) * p.da * p.dc : nullptr;
     auto at = [&](int a, int c) {
@@ -112,7 +128,7 @@ __global__ __launch_bounds__(256) void logmel_attn_rows_kernel(AttnJob<T> p, int
       }
       __syncthreads();
       for (int t = 0; t < held; ++t) {
-        const float keep = p.back && t0 + t == 0 ? 1.0f : lambda;
+        const Decay keep = p.back && t0 + t == 0 ? Decay{1.0f, 0.0f} : lambda;
         const float4 c = *reinterpret_cast<const float4*>(&sc[t][4 * cg]);
         float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -121,7 +137,7 @@ __global__ __launch_bounds__(256) void logmel_attn_rows_kernel(AttnJob<T> p, int
           const float cv[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            w[u][j] = __builtin_fmaf(keep, w[u][j], b * cv[j]);
+            w[u][j] = __builtin_fmaf(b, cv[j], decayed(keep, w[u][j]));
             o[j] = __builtin_fmaf(a, w[u][j], o[j]);
           }
         }
@@ -148,14 +164,744 @@ __global__ __launch_bounds__(256) void logmel_attn_rows_kernel(AttnJob<T> p, int
       }
     }
     if (!out) continue;
-    const float last = p.back && n > 0 ? lambda : 1.0f;
+    const Decay last = p.back && n > 0 ? lambda : Decay{1.0f, 0.0f};
 #pragma unroll
     for (int u = 0; u < kU; ++u)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int a = ag + 16 * u, c = c0 + 4 * cg + j;
-        if (a < p.da && c < p.dc) out[at(a, c)] = last * w[u][j];
+        if (a < p.da && c < p.dc) out[at(a, c)] = decayed(last, w[u][j]);
       }
+  }
+}
+
+// ------------------------------------------------------- chunk after chunk
+//
+// With a chunk of n rows and E = lambda W before it, the state as its first
+// row meets it,
+//   o_i = beta (gamma sum_{j<=i} lambda^(i-j) (a_i . b_j) c_j + lambda^i a_i E)
+//   E'  = lambda^n E + gamma sum_j lambda^(n-j) b_j c_j^T,
+// four products on the matrix cores. A workgroup of four wavefronts walks the
+// chunks of a sequence's rows and holds 64 columns of E, 16 per wavefront, in
+// its accumulators. The scores of a chunk are formed by the wavefronts
+// together, a few blocks of 16 x 16 each, and exchanged through LDS; every
+// other product is a wavefront's own. The scores come out of the matrix cores
+// with a row i per lane and four neighbouring j in its registers, the state with
+// a column per lane and four neighbouring rows: both are fed back as operands
+// just so, as the order of the summed index is free, if rows of b are taken in
+// the order that `place` gives.
+//
+// The operands are bf16 pieces: a bf16 row one, an fp16 row two (exactly), an
+// fp32 row three (exactly). What the products make is cut into pieces too, by
+// rounding, with the rest to the next: scores and the state that meets a in two
+// for 2-byte rows, which leave 2^-18 of each where the output keeps 2^-9 or
+// 2^-12; three for fp32 rows and for the weighted rows that enter the state,
+// which is fp32 for every type. Products of pieces whose places sum to the
+// count are left out: 2^-18 or 2^-26 of the whole as well.
+//
+// Causality is exact, for NaN and infinities too: a score above the diagonal is
+// left out by a select, and a chunk with a value of b or c that is not finite
+// is cut short before its row, which starts a chunk of its own.
+
+// The same value to a reader, to the compiler a new one: addresses and
+// conditions formed from it are formed where they are used, not held in
+// registers through the walk.
+__device__ __forceinline__ int fresh(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+template <typename T>
+struct Pieces;
+template <>
+struct Pieces<bf16_t> {
+  static constexpr int kIn = 1, kMid = 2, kState = 3, kChunk = 64;
+};
+template <>
+struct Pieces<f16_t> {
+  static constexpr int kIn = 2, kMid = 2, kState = 3, kChunk = 32;
+};
+template <>
+struct Pieces<float> {
+  static constexpr int kIn = 3, kMid = 3, kState = 3, kChunk = 32;
+};
+
+using bf16x2 = __attribute__((ext_vector_type(2))) __bf16;
+using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
+using f32x4 = __attribute__((ext_vector_type(4))) float;
+using u32x2 = __attribute__((ext_vector_type(2))) uint32_t;
+using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
+
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
+__device__ __forceinline__ float low(uint32_t v) { return __builtin_bit_cast(float, v << 16); }
+__device__ __forceinline__ float high(uint32_t v) {
+  return __builtin_bit_cast(float, v & 0xffff0000u);
+}
+
+// M values as N pieces each, packed in pairs; x keeps the rest.
+template <int N, int M>
+__device__ __forceinline__ void cut(float (&x)[M], uint32_t (&piece)[N][M / 2]) {
+#pragma unroll
+  for (int n = 0; n < N; ++n)
+#pragma unroll
+    for (int i = 0; i < M / 2; ++i) {
+      piece[n][i] = pack(x[2 * i], x[2 * i + 1]);
+      if (n + 1 < N) {
+        x[2 * i] -= low(piece[n][i]);
+        x[2 * i + 1] -= high(piece[n][i]);
+      }
+    }
+}
+
+__device__ __forceinline__ bf16x8 frag(const uint32_t (&w)[4]) {
+  return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
+}
+__device__ __forceinline__ bf16x8 frag(const uint16_t* p) {
+  return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p));
+}
+
+// acc += sum over the pairs of pieces whose places sum to less than the count.
+template <int NA, int NB>
+__device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf16x8 (&b)[NB]) {
+  constexpr int kMost = NA > NB ? NA : NB;
+#pragma unroll
+  for (int s = kMost - 1; s >= 0; --s)   // the smallest first
+#pragma unroll
+    for (int i = 0; i <= s; ++i)
+      if (i < NA && s - i < NB)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[s - i], acc, 0, 0, 0);
+}
+
+// Where the block of four rows (columns) 4 i .. 4 i + 3 stands in a tile whose
+// 16-blocks are read as operands of results that are operands again.
+__device__ __forceinline__ int place(int i) { return 32 * (i >> 3) + 16 * (i & 1) + 4 * ((i >> 1) & 3); }
+
+// A tile of kRows rows and kWidth channels in registers, on its way from memory
+// to LDS, in blocks of 4 x 4 values: eight blocks side by side and eight below
+// each other per wavefront, so that memory is read 64 or 128 bytes at a time and
+// LDS is written, along rows and along columns, without bank conflicts.
+template <typename T, int kRows, int kWidth>
+struct Tile {
+  static constexpr int kIn = Pieces<T>::kIn;
+  static constexpr int kBlocks = kRows / 4 * (kWidth / 4);
+  static constexpr int kIts = (kBlocks + 255) / 256;
+  Packed<T, 4> v[kIts][4];
+
+  static __device__ __forceinline__ bool on(int it) {
+    return kBlocks % 256 == 0 || (int)threadIdx.x + 256 * it < kBlocks;
+  }
+  static __device__ __forceinline__ void at(int tid, int it, int& rb, int& cb) {
+    const int i = tid + 256 * it, rest = i >> 6;
+    constexpr int kWide = kWidth / 32;
+    cb = (i & 7) + 8 * (rest % kWide);
+    rb = ((i >> 3) & 7) + 8 * (rest / kWide);
+  }
+
+  // base: the tile's lowest row; up: whether that is its first. Rows from held
+  // on are read as the last one, and blocks at the row's end as its last four
+  // values (there are four): every access is to the tile's own rows. `settle`
+  // makes them what they are.
+  __device__ __forceinline__ void load(const T* base, uint32_t pitch, bool up, int held,
+                                       int width) {
+    const char* from = reinterpret_cast<const char*>(base);
+    const int tid = fresh(threadIdx.x);
+#pragma unroll
+    for (int it = 0; it < kIts; ++it) {
+      int rb, cb;
+      at(tid, it, rb, cb);
+      if (!on(it)) rb = 0;
+      int c = 4 * cb;
+      c = c + 4 <= width ? c : width - 4;
+      const uint32_t side = (uint32_t)c * sizeof(T);
+      if (held == kRows) {
+        uint32_t to = (uint32_t)(up ? 4 * rb : held - 1 - 4 * rb) * pitch + side;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          v[it][r] = row_load<T, 4>(reinterpret_cast<const T*>(from + to));
+          to = up ? to + pitch : to - pitch;
+        }
+      } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          int i = 4 * rb + r;
+          i = i < held ? i : held - 1;
+          i = up ? i : held - 1 - i;
+          v[it][r] = row_load<T, 4>(reinterpret_cast<const T*>(from + ((uint32_t)i * pitch + side)));
+        }
+      }
+    }
+  }
+
+  // The same for rows of fewer than four values.
+  __device__ __forceinline__ void load_narrow(const T* base, uint32_t pitch, bool up, int held,
+                                              int width) {
+    const char* from = reinterpret_cast<const char*>(base);
+    const int tid = fresh(threadIdx.x);
+#pragma unroll
+    for (int it = 0; it < kIts; ++it) {
+      int rb, cb;
+      at(tid, it, rb, cb);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        v[it][r] = Packed<T, 4>{};
+        int i = 4 * rb + r;
+        if (!on(it) || cb || i >= held) continue;
+        if (!up) i = held - 1 - i;
+        const T* p = reinterpret_cast<const T*>(from + (uint32_t)i * pitch);
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (j < width) v[it][r].v[j] = p[j];
+      }
+    }
+  }
+
+  // 0 in rows from held on and in channels from width on.
+  __device__ __forceinline__ void settle(int held, int width) {
+    const int tid = fresh(threadIdx.x);
+#pragma unroll
+    for (int it = 0; it < kIts; ++it) {
+      int rb, cb;
+      at(tid, it, rb, cb);
+      const int skip = 4 * cb + 4 - width;   // values that the block was shifted back by
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        Packed<T, 4> x = v[it][r];
+        if constexpr (sizeof(T) == 2) {
+          uint64_t w = __builtin_bit_cast(uint64_t, x);
+          w = skip > 0 ? (skip < 4 ? w >> (16 * skip) : 0) : w;
+          w = 4 * rb + r < held ? w : 0;
+          x = __builtin_bit_cast(decltype(x), w);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            T y = x.v[j];
+#pragma unroll
+            for (int k = 1; k < 4; ++k) y = skip == k ? (j + k < 4 ? x.v[(j + k) & 3] : T(0)) : y;
+            y = skip < 4 && 4 * rb + r < held ? y : T(0);
+            v[it][r].v[j] = y;
+          }
+          continue;
+        }
+        v[it][r] = x;
+      }
+    }
+  }
+
+  // Whether a value is not finite: the largest of the words without signs is.
+  __device__ __forceinline__ bool any_bad() const {
+    using u16x2 = __attribute__((ext_vector_type(2))) uint16_t;
+    if constexpr (sizeof(T) == 2) {
+      constexpr uint16_t kInf = std::is_same_v<T, bf16_t> ? 0x7f80 : 0x7c00;
+      u16x2 m = {0, 0};
+#pragma unroll
+      for (int it = 0; it < kIts; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const u32x2 w = __builtin_bit_cast(u32x2, v[it][r]) & 0x7fff7fffu;
+          m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, (uint32_t)w[0]));
+          m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, (uint32_t)w[1]));
+        }
+      return m[0] >= kInf || m[1] >= kInf;
+    } else {
+      uint32_t m = 0;
+#pragma unroll
+      for (int it = 0; it < kIts; ++it)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w = __builtin_bit_cast(uint32_t, v[it][r].v[j]) & 0x7fffffffu;
+            m = m > w ? m : w;
+          }
+      return m >= 0x7f800000u;
+    }
+  }
+
+  // The first row with a value that is not finite, or kRows.
+  __device__ __forceinline__ int first_bad() const {
+    const int tid = fresh(threadIdx.x);
+    int first = kRows;
+#pragma unroll
+    for (int it = 0; it < kIts; ++it) {
+      int rb, cb;
+      at(tid, it, rb, cb);
+#pragma unroll
+      for (int r = 3; r >= 0; --r) {
+        bool bad = false;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) bad |= !__builtin_isfinite((float)v[it][r].v[j]);
+        first = bad && on(it) && 4 * rb + r < first ? 4 * rb + r : first;
+      }
+    }
+    return first;
+  }
+
+  // Into LDS: rows [kIn][kRows][kWidth + 8] and columns [kIn][kWidth][kRows + 8],
+  // whichever is not null.
+  __device__ __forceinline__ void store(uint16_t* rows, bool rows_placed, uint16_t* cols,
+                                        bool cols_placed) const {
+    constexpr int kRowPitch = kWidth + 8, kColPitch = kRows + 8;
+    const int tid = fresh(threadIdx.x);
+#pragma unroll
+    for (int it = 0; it < kIts; ++it) {
+      if (!on(it)) continue;
+      int rb, cb;
+      at(tid, it, rb, cb);
+      uint32_t w[4][kIn][2];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (kIn == 1) {
+          const u32x2 x = __builtin_bit_cast(u32x2, v[it][r]);
+          w[r][0][0] = x[0], w[r][0][1] = x[1];
+        } else {
+          float x[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = (float)v[it][r].v[j];
+          cut<kIn, 4>(x, w[r]);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < kIn; ++n) {
+        if (rows) {
+          const int at0 = rows_placed ? place(rb) : 4 * rb;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            *reinterpret_cast<u32x2*>(rows + (n * kRows + at0 + r) * kRowPitch + 4 * cb) =
+                u32x2{w[r][n][0], w[r][n][1]};
+        }
+        if (cols) {
+          const int at0 = cols_placed ? place(cb) : 4 * cb;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
+            *reinterpret_cast<u32x2*>(cols + (n * kWidth + at0 + c) * kColPitch + 4 * rb) =
+                u32x2{__builtin_amdgcn_perm(w[1][n][c / 2], w[0][n][c / 2], sel),
+                      __builtin_amdgcn_perm(w[3][n][c / 2], w[2][n][c / 2], sel)};
+          }
+        }
+      }
+    }
+  }
+};
+
+// How the rows are split: a workgroup per sequence (parts 0), or parts of
+// part_rows packed rows each, whatever sequences they hold. Between parts b and
+// b + 1 stands state b of `between`, as the next row of the sequence there meets
+// it; kept: the initial state of the sequence that starts in part b and leaves
+// it, where state_out may overwrite it.
+struct Walk {
+  int64_t part_rows, parts;
+  float* between;
+  float* kept;
+  int slabs;
+  int64_t items;
+};
+
+// The sequence that holds rows on both sides of `row`: -1 if there is none.
+template <typename T>
+__device__ __forceinline__ int64_t first_from(const AttnJob<T>& p, int64_t row) {
+  int64_t lo = 0, hi = p.n_seq + 1;   // the first offset at or behind row
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (p.off[mid] < row)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+template <typename T>
+__device__ __forceinline__ int64_t across(const AttnJob<T>& p, int64_t row) {
+  const int64_t i = first_from(p, row);
+  return i > 0 && i <= p.n_seq && p.off[i] > row ? i - 1 : -1;
+}
+
+template <typename T, int DA>
+struct ChunkLds {
+  static constexpr int C = Pieces<T>::kChunk, kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid;
+  static constexpr int kScores = C == 64 ? 6 : 2;
+  uint16_t a[kIn][C][DA + 8];
+  uint16_t b[kIn][C][DA + 8];       // rows as `place` has them
+  uint16_t bt[kIn][DA][C + 8];      // columns as `place` has them
+  uint16_t ct[kIn][kSlab][C + 8];
+  uint16_t p[kMid][kScores][64][8];
+  int bad;
+};
+
+template <typename T, int DA, bool kOut>
+__global__ __launch_bounds__(256, 2) void logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
+  constexpr int kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid, kState = Pieces<T>::kState;
+  constexpr int C = Pieces<T>::kChunk, kI = C / 16, kT = C / 32, kS = DA / 32, kU = DA / 16;
+  __shared__ __attribute__((aligned(16))) ChunkLds<T, DA> lds;
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int step = p.back ? -1 : 1;
+  if (tid == 0) lds.bad = C;
+  for (int64_t item = blockIdx.x; item < walk.items; item += gridDim.x) {
+    const int slab = (int)(item % walk.slabs);
+    const int h = (int)(item / walk.slabs % p.heads);
+    const int64_t which = item / walk.slabs / p.heads;   // sequence or part
+    const int c0 = slab * kSlab;
+    const T* pa = p.a + (int64_t)(h / p.share_a) * p.da;
+    const T* pb = p.b + (int64_t)(h / p.share_b) * p.da;
+    const T* pc = p.c + (int64_t)(h / p.share_c) * p.dc + c0;
+    const int wc = p.dc - c0;
+    const float decay = p.log_decay[h];
+    const float log2 = decay * 1.44269504088896340736f;
+    auto power = [&](int i) { return i > 0 ? __builtin_amdgcn_exp2f(log2 * (float)i) : 1.0f; };
+    const int64_t cells = (int64_t)p.da * p.dc;
+
+    // weights of this lane's scores: block (rows 16 bi, columns 32 t and b)
+    constexpr int kMine = C == 64 ? 3 : 1;
+    const int half = wave & 1, pair = wave >> 1;
+    float ws[kMine][4];
+    float enter[kI];
+    if constexpr (kOut) {
+#pragma unroll
+      for (int m = 0; m < kMine; ++m) {
+        const int bi = m ? 2 + pair : pair, t = m == 2;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          ws[m][r] = p.gamma * power(16 * bi + n - (32 * t + 8 * g + 4 * half + r));
+      }
+#pragma unroll
+      for (int i = 0; i < kI; ++i) enter[i] = power(16 * i + n);
+    }
+    // of the rows that enter the state, `left` rows before the next chunk's first
+    float wc_[kT][8];
+    Decay whole;
+    int left = -1;
+    auto weigh = [&](int to) __attribute__((always_inline)) {
+      if (to == left) return;
+      left = to;
+      whole = decay_of(decay, (float)to);
+#pragma unroll
+      for (int t = 0; t < kT; ++t)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int j = 32 * t + 8 * g + e;
+          wc_[t][e] = j <= to ? p.gamma * power(to - j) : 0.0f;
+        }
+    };
+
+    f32x4 w[kU];
+    // f(u, r, cell of the state) for this lane's values w[u][r] that are cells
+    auto cells_of = [&](auto f) __attribute__((always_inline)) {
+      const int c = fresh(c0 + 16 * wave + n), a0 = fresh(8 * g);
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int a = a0 + 32 * (u >> 1) + 4 * (u & 1) + r;
+          if (a < p.da && c < p.dc) f(u, r, p.transposed ? c * p.da + a : a * p.dc + c);
+        }
+    };
+    auto load_state = [&](const float* s, Decay d) __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) w[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (s)
+        cells_of([&](int u, int r, int i) __attribute__((always_inline)) {
+          w[u][r] = decayed(d, s[i]);
+        });
+    };
+    auto store_state = [&](float* s) __attribute__((always_inline)) {
+      cells_of([&](int u, int r, int i) __attribute__((always_inline)) { s[i] = w[u][r]; });
+    };
+
+    // Rows [lo, hi) of one sequence, whose state before them is in w; last:
+    // the state behind them is wanted undecayed.
+    auto segment = [&](int64_t lo, int64_t hi, bool last) __attribute__((always_inline)) {
+      const int64_t rows = hi - lo;
+      const int64_t first = p.back ? hi - 1 : lo;
+      Tile<T, C, DA> ta, tb;
+      Tile<T, C, kSlab> tc;
+      const int wide = wc < kSlab ? wc : kSlab;
+      const uint32_t sa = (uint32_t)(p.as * sizeof(T)), sb = (uint32_t)(p.bs * sizeof(T)),
+                     sc = (uint32_t)(p.cs * sizeof(T));
+      auto load = [&](int64_t at, int held) __attribute__((always_inline)) {
+        const int64_t row = p.back ? first - at - held + 1 : first + at;   // the lowest
+        auto one = [&](auto& t, const T* base, int64_t stride, uint32_t pitch, int width)
+                       __attribute__((always_inline)) {
+          if (width >= 4)
+            t.load(base + row * stride, pitch, !p.back, held, width);
+          else
+            t.load_narrow(base + row * stride, pitch, !p.back, held, width);
+        };
+        if constexpr (kOut) one(ta, pa, p.as, sa, p.da);
+        one(tb, pb, p.bs, sb, p.da);
+        one(tc, pc, p.cs, sc, wide);
+      };
+      auto settle = [&](int held) __attribute__((always_inline)) {
+        if (held < C || p.da < DA) {
+          if constexpr (kOut)
+            if (p.da >= 4) ta.settle(held, p.da);
+          if (p.da >= 4) tb.settle(held, p.da);
+        }
+        if ((held < C || wide < kSlab) && wide >= 4) tc.settle(held, wide);
+      };
+      auto stage = [&]() __attribute__((always_inline)) {
+        if constexpr (kOut) {
+          ta.store(&lds.a[0][0][0], false, nullptr, false);
+          tb.store(&lds.b[0][0][0], true, &lds.bt[0][0][0], true);
+        } else {
+          tb.store(nullptr, false, &lds.bt[0][0][0], true);
+        }
+        tc.store(nullptr, false, &lds.ct[0][0][0], false);
+      };
+      auto held_at = [&](int64_t at) { return (int)(rows - at < C ? rows - at : C); };
+      load(0, held_at(0));
+      for (int64_t at = 0; at < rows;) {
+        int held = held_at(at);
+        for (bool cut_short = false;;) {
+          settle(held);
+          stage();
+          if constexpr (!kOut) break;
+          if (!cut_short && __any(tb.any_bad() || tc.any_bad())) {
+            const int b1 = tb.first_bad(), b2 = tc.first_bad();
+            const int bad = b1 < b2 ? b1 : b2;
+            if (bad < C) atomicMin(&lds.bad, bad);
+          }
+          __syncthreads();
+          const int bad = lds.bad;
+          if (cut_short || bad == C) break;   // for the whole workgroup
+          cut_short = true;
+          held = bad > 0 ? bad : 1;
+          load(at, held);
+          __syncthreads();
+          if (tid == 0) lds.bad = C;
+        }
+        if constexpr (!kOut) __syncthreads();
+        const int64_t next = at + held;
+        if (next < rows) load(next, held_at(next));
+
+        if constexpr (kOut) {
+          // the scores, transposed: block (t, half) of 16 rows of b by rows 16 bi of a
+#pragma unroll
+          for (int m = 0; m < kMine; ++m) {
+            const int bi = m ? 2 + pair : pair, t = m == 2;
+            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < kS; ++s) {
+              bf16x8 fb[kIn], fa[kIn];
+#pragma unroll
+              for (int k = 0; k < kIn; ++k) {
+                fb[k] = frag(&lds.b[k][32 * t + 16 * half + n][32 * s + 8 * g]);
+                fa[k] = frag(&lds.a[k][16 * bi + n][32 * s + 8 * g]);
+              }
+              mma(acc, fb, fa);
+            }
+            float x[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int i = 16 * bi + n, j = 32 * t + 8 * g + 4 * half + r;
+              x[r] = j <= i ? ws[m][r] * acc[r] : 0.0f;
+            }
+            uint32_t piece[kMid][2];
+            cut<kMid, 4>(x, piece);
+            const int f = bi < 2 ? bi : 2 * bi - 2 + t;
+#pragma unroll
+            for (int k = 0; k < kMid; ++k)
+              *reinterpret_cast<u32x2*>(&lds.p[k][f][lane][4 * half]) =
+                  u32x2{piece[k][0], piece[k][1]};
+          }
+          __syncthreads();
+        }
+
+        bf16x8 fc[kT][kIn];
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+          for (int k = 0; k < kIn; ++k)
+            fc[t][k] = frag(&lds.ct[k][16 * wave + n][32 * t + 8 * g]);
+
+        if constexpr (kOut) {
+          f32x4 o[kI];
+#pragma unroll
+          for (int i = 0; i < kI; ++i) o[i] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int s = 0; s < kS; ++s) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = w[2 * s + e / 4][e & 3];
+            uint32_t piece[kMid][4];
+            cut<kMid, 8>(x, piece);
+            bf16x8 fw[kMid];
+#pragma unroll
+            for (int k = 0; k < kMid; ++k) fw[k] = frag(piece[k]);
+#pragma unroll
+            for (int i = 0; i < kI; ++i) {
+              bf16x8 fa[kIn];
+#pragma unroll
+              for (int k = 0; k < kIn; ++k) fa[k] = frag(&lds.a[k][16 * i + n][32 * s + 8 * g]);
+              mma(o[i], fw, fa);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kI; ++i) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[i][r] *= enter[i];
+#pragma unroll
+            for (int t = 0; t <= i / 2; ++t) {
+              bf16x8 fp[kMid];
+              const int f = i < 2 ? i : 2 * i - 2 + t;
+#pragma unroll
+              for (int k = 0; k < kMid; ++k) fp[k] = frag(&lds.p[k][f][lane][0]);
+              mma(o[i], fc[t], fp);
+            }
+            if (16 * i + n < held) {
+              const int64_t row = first + step * (at + 16 * i + n);
+              const int c = 16 * wave + 4 * g;
+              float x[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) x[r] = p.beta * o[i][r];
+              const int64_t to = row * p.os + (int64_t)h * p.dc + c0 + c;
+              auto put = [&](auto* out) {
+                if (c + 4 <= wc) {
+                  row_store(out + to, x);
+                } else {
+#pragma unroll
+                  for (int r = 0; r < 3; ++r)
+                    if (c + r < wc) out[to + r] = (std::decay_t<decltype(*out)>)x[r];
+                }
+              };
+              if (p.of)
+                put(p.of);
+              else
+                put(p.o);
+            }
+          }
+        }
+
+        weigh(last && next == rows ? held - 1 : held);
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) w[u][r] = decayed(whole, w[u][r]);
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[e] = 0.0f;
+#pragma unroll
+            for (int k = kIn - 1; k >= 0; --k) x[e] += (float)fc[t][k][e];
+            x[e] *= wc_[t][e];
+          }
+          uint32_t piece[kState][4];
+          cut<kState, 8>(x, piece);
+          bf16x8 fw[kState];
+#pragma unroll
+          for (int k = 0; k < kState; ++k) fw[k] = frag(piece[k]);
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            bf16x8 fb[kIn];
+#pragma unroll
+            for (int k = 0; k < kIn; ++k) fb[k] = frag(&lds.bt[k][16 * u + n][32 * t + 8 * g]);
+            mma(w[u], fb, fw);
+          }
+        }
+        __syncthreads();   // the tiles are read to the end
+        at = next;
+      }
+    };
+
+    const Decay one = {1.0f, 0.0f}, lambda = decay_of(decay, 1.0f);
+    // Rows [lo, hi) of sequence i, of part b.
+    auto run = [&](int64_t i, int64_t lo, int64_t hi, bool starts, bool ends, int64_t b) __attribute__((always_inline)) {
+      const int64_t of_seq = (i * p.heads + h) * cells;
+      const float* in = p.state ? p.state + of_seq : nullptr;
+      float* out = p.state_out ? p.state_out + of_seq : nullptr;
+      if (lo >= hi) {   // an empty sequence
+        if (starts && ends && out)
+          cells_of([&](int, int, int c) __attribute__((always_inline)) {
+            out[c] = in ? in[c] : 0.0f;
+          });
+        return;
+      }
+      auto slot = [&](float* s, int64_t at) { return s + (at * p.heads + h) * cells; };
+      const bool fresh_start = p.back ? ends : starts;
+      const bool put_by = starts && !ends && walk.kept;
+      const float* from = fresh_start ? (put_by ? slot(walk.kept, b) : in)
+                                      : slot(walk.between, p.back ? b : b - 1);
+      load_state(from, fresh_start && !put_by && !p.back ? lambda : one);
+      segment(lo, hi, !p.back && ends);
+      if ((p.back ? starts : ends) && out) store_state(out);
+    };
+
+    // The sequences of this workgroup's rows, in order: its own, or those of its
+    // part from the one that enters it on.
+    const int64_t r0 = which * walk.part_rows;
+    const int64_t r1 = walk.parts == 0 || r0 + walk.part_rows > p.rows ? p.rows
+                                                                       : r0 + walk.part_rows;
+    auto within = [&](int64_t r) { return r < r0 ? r0 : r > r1 ? r1 : r; };
+    if constexpr (!kOut) {
+      // the state that leaves the part, from the sequence across its end (its
+      // start, backwards)
+      const int64_t i = across(p, p.back ? r0 : r1);
+      if (i < 0) continue;
+      const int64_t from = p.off[i], to = p.off[i + 1];
+      const bool fresh = p.back ? to <= r1 : from >= r0;
+      const int64_t of_seq = (i * p.heads + h) * cells;
+      load_state(fresh && p.state ? p.state + of_seq : nullptr, p.back ? one : lambda);
+      if (fresh && walk.kept) store_state(walk.kept + (which * p.heads + h) * cells);
+      segment(within(from), within(to), false);
+      store_state(walk.between + ((p.back ? which - 1 : which) * p.heads + h) * cells);
+    } else {
+      int64_t i = which;
+      bool enters = false;
+      if (walk.parts) {
+        i = first_from(p, r0);
+        enters = i > 0 && i <= p.n_seq && p.off[i] > r0;
+        i -= enters;
+      }
+      const bool end = walk.parts == 0 || which == walk.parts - 1;
+      do {
+        if (i >= p.n_seq || !(enters || end || p.off[i] < r1)) break;
+        const int64_t lo = enters ? r0 : within(p.off[i]);
+        run(i, lo, within(p.off[i + 1]), !enters, end || p.off[i + 1] <= r1, which);
+        enters = false;
+        ++i;
+      } while (walk.parts);
+    }
+  }
+}
+
+// The states between the parts, from those that each part makes: in order (from
+// the last, backwards), the state that enters a part decays through it where
+// its sequence does not end in it.
+template <typename T>
+__global__ __launch_bounds__(256) void logmel_attn_between_kernel(AttnJob<T> p, Walk walk) {
+  constexpr int kBatch = 8;
+  const int64_t cells = (int64_t)p.da * p.dc, all = cells * p.heads;
+  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (x >= all) return;
+  const float decay = p.log_decay[x / cells];
+  const Decay whole = decay_of(decay, (float)walk.part_rows);
+  const int64_t count = walk.parts - 1;
+  float e = 0.0f;
+  for (int64_t k0 = 0; k0 < count; k0 += kBatch) {
+    float u[kBatch];
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m) {
+      const int64_t k = k0 + m, b = p.back ? count - 1 - k : k;
+      u[m] = k < count ? walk.between[b * all + x] : 0.0f;
+    }
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m) {
+      const int64_t k = k0 + m;
+      if (k >= count) break;
+      const int64_t b = p.back ? count - 1 - k : k;
+      // the sequence across the boundary, and whether it crosses the one before
+      const int64_t i = across(p, (b + 1) * walk.part_rows);
+      if (i < 0) continue;
+      const bool through = p.back ? p.off[i + 1] > (b + 2) * walk.part_rows
+                                  : p.off[i] < b * walk.part_rows;
+      e = k > 0 && through ? u[m] + decayed(whole, e) : u[m];
+      walk.between[b * all + x] = e;
+    }
   }
 }
 
@@ -178,16 +924,96 @@ __global__ __launch_bounds__(256) void logmel_attn_share_kernel(const float* par
   }
 }
 
-template <typename T>
-hipError_t launch_job(const AttnJob<T>& p, hipStream_t stream) {
-  const int slabs = (p.dc + kSlab - 1) / kSlab;
-  const int64_t items = p.n_seq * p.heads * slabs;
-  const unsigned grid = (unsigned)(items < (1 << 22) ? items : 1 << 22);
-  if (p.da <= 64)
-    logmel_attn_rows_kernel<T, 64><<<grid, 256, 0, stream>>>(p, slabs, items);
-  else
-    logmel_attn_rows_kernel<T, 128><<<grid, 256, 0, stream>>>(p, slabs, items);
+int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
+
+// How a job's rows are split over workgroups.
+struct AttnSplit {
+  enum How { kRows, kSequences, kParts } how;
+  int64_t part_rows, parts;
+};
+
+// widest: the longest row stride.
+AttnSplit split_of(const logmel_attention_input& in, int da, int dc, int64_t widest, int cus) {
+  AttnSplit s{AttnSplit::kSequences, 0, 0};
+  const int64_t longest =
+      in.max_frames && in.max_frames < in.rows ? in.max_frames : in.rows;
+  // a chunk's rows are addressed by 32 bits from its lowest one
+  if (longest <= kStepRows || widest >= (int64_t)1 << 22) {
+    s.how = AttnSplit::kRows;
+    return s;
+  }
+  const int64_t chunk = in.type == LOGMEL_BF16 ? 64 : 32;
+  const int64_t lanes = in.heads * ceil_div(dc, kSlab);   // workgroups side by side
+  const int64_t slots = 2 * (int64_t)cus;
+  // in chunks one after the other
+  const int64_t by_seq = ceil_div(longest, chunk);
+  const int64_t seq_all = ceil_div(in.rows, chunk) * lanes / slots;
+  const double seq_time = (double)(by_seq > seq_all ? by_seq : seq_all);
+  int64_t rows = ceil_div(ceil_div(in.rows * lanes, slots), chunk) * chunk;
+  rows = rows < 4 * chunk ? 4 * chunk : rows;
+  const int64_t parts = ceil_div(in.rows, rows);
+  const double part_time =
+      1.6 * (double)(rows / chunk) * (double)ceil_div(parts * lanes, slots) + 0.1 * parts + 4.0;
+  if (parts > 1 && part_time < seq_time) {
+    s.how = AttnSplit::kParts;
+    s.part_rows = rows;
+    s.parts = parts;
+  }
+  return s;
+}
+
+// What the parts of a job need of the workspace, in floats.
+int64_t between_of(const AttnSplit& s, const logmel_attention_input& in) {
+  return s.how == AttnSplit::kParts ? (s.parts - 1) * in.heads * in.head_dk * in.head_dv : 0;
+}
+int64_t kept_of(const AttnSplit& s, const logmel_attention_input& in) {
+  return s.how == AttnSplit::kParts ? s.parts * in.heads * in.head_dk * in.head_dv : 0;
+}
+
+template <typename T, int DA>
+hipError_t launch_chunks(const AttnJob<T>& p, const AttnSplit& s, Walk k, int64_t lanes,
+                         hipStream_t stream) {
+  auto grid = [](int64_t items) { return (unsigned)(items < (1 << 22) ? items : 1 << 22); };
+  if (s.how == AttnSplit::kParts) {
+    k.part_rows = s.part_rows;
+    k.parts = s.parts;
+    k.items = s.parts * lanes;
+    logmel_attn_chunk_kernel<T, DA, false><<<grid(k.items), 256, 0, stream>>>(p, k);
+    const int64_t cells = (int64_t)p.heads * p.da * p.dc;
+    logmel_attn_between_kernel<T>
+        <<<(unsigned)ceil_div(cells, 256), 256, 0, stream>>>(p, k);
+  } else {
+    k.items = p.n_seq * lanes;
+  }
+  logmel_attn_chunk_kernel<T, DA, true><<<grid(k.items), 256, 0, stream>>>(p, k);
   return hipGetLastError();
+}
+
+// ws: what between_of (and in place kept_of, behind it) asks for.
+template <typename T>
+hipError_t launch_job(const AttnJob<T>& p, const logmel_attention_input& in, float* ws,
+                      bool in_place, int cus, hipStream_t stream) {
+  const int slabs = (p.dc + kSlab - 1) / kSlab;
+  int64_t widest = p.as > p.bs ? p.as : p.bs;
+  widest = widest > p.cs ? widest : p.cs;
+  const AttnSplit s = split_of(in, p.da, p.dc, widest, cus);
+  if (s.how == AttnSplit::kRows) {
+    const int64_t items = p.n_seq * p.heads * slabs;
+    const unsigned grid = (unsigned)(items < (1 << 22) ? items : 1 << 22);
+    if (p.da <= 64)
+      logmel_attn_rows_kernel<T, 64><<<grid, 256, 0, stream>>>(p, slabs, items);
+    else
+      logmel_attn_rows_kernel<T, 128><<<grid, 256, 0, stream>>>(p, slabs, items);
+    return hipGetLastError();
+  }
+  Walk k{};
+  k.slabs = slabs;
+  k.between = ws;
+  k.kept = in_place && s.how == AttnSplit::kParts ? ws + between_of(s, in) : nullptr;
+  const int64_t lanes = (int64_t)p.heads * slabs;
+  if (p.da <= 32) return launch_chunks<T, 32>(p, s, k, lanes, stream);
+  if (p.da <= 64) return launch_chunks<T, 64>(p, s, k, lanes, stream);
+  return launch_chunks<T, 128>(p, s, k, lanes, stream);
 }
 
 template <typename T>
@@ -221,7 +1047,8 @@ hipError_t launch_attention(const logmel_attention_input& in, void* o, int64_t o
   p.state_out = state_out;
   p.beta = in.scale;
   p.gamma = 1.0f;
-  return launch_job(p, stream);
+  return launch_job(p, in, static_cast<float*>(ws), state_out && state_out == in.d_state, cus,
+                    stream);
 }
 
 template <typename T>
@@ -234,13 +1061,15 @@ hipError_t launch_attention_backward(const logmel_attention_input& in,
   const T* v = static_cast<const T*>(in.d_v);
   const T* d = static_cast<const T*>(g.d_do);
   const int dk = (int)in.head_dk, dv = (int)in.head_dv;
+  // the shared heads' parts first, then the splits'
   float* part = share > 1 ? static_cast<float*>(ws) : nullptr;
+  float* between = static_cast<float*>(ws) + (part ? in.rows * in.heads * dk : 0);
   // a gradient of q or k: its own rows, or each head's first and then their sums
   auto shared = [&](AttnJob<T>& p, void* out, int64_t stride) {
     p.o = static_cast<T*>(out);
     p.of = part;
     p.os = part ? in.heads * dk : stride;
-    hipError_t e = launch_job(p, stream);
+    hipError_t e = launch_job(p, in, between, false, cus, stream);
     if (e != hipSuccess || !part) return e;
     const int64_t n = in.rows * in.qk_heads * dk;
     const int64_t blocks = (n + 255) / 256;
@@ -280,14 +1109,21 @@ hipError_t launch_attention_backward(const logmel_attention_input& in,
   p.of = nullptr;
   p.o = static_cast<T*>(g.d_dv);
   p.os = g.dv_stride;
-  return launch_job(p, stream);
+  return launch_job(p, in, between, false, cus, stream);
 }
 
 }  // namespace
 }  // namespace logmel
 
 int64_t logmel_attention_workspace(const logmel_attention_input& in, int backward, int cus) {
-  return backward && in.heads > in.qk_heads ? in.rows * in.heads * in.head_dk * 4 : 0;
+  using namespace logmel;
+  if (!in.n_seq) return 0;
+  const int dk = (int)in.head_dk, dv = (int)in.head_dv;
+  const AttnSplit s = split_of(in, dk, dv, 0, cus);   // forward, and dv
+  if (!backward) return (between_of(s, in) + (in.d_state ? kept_of(s, in) : 0)) * 4;
+  const AttnSplit t = split_of(in, dv, dk, 0, cus);   // dq and dk
+  const int64_t a = between_of(s, in), b = between_of(t, in);
+  return ((in.heads > in.qk_heads ? in.rows * in.heads * in.head_dk : 0) + (a > b ? a : b)) * 4;
 }
 
 hipError_t logmel_launch_attention(const logmel_attention_input& in, void* o, int64_t o_stride,
