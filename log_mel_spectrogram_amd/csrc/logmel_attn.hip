@@ -279,131 +279,151 @@ __device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf1
 // 16-blocks are read as operands of results that are operands again.
 __device__ __forceinline__ int place(int i) { return 32 * (i >> 3) + 16 * (i & 1) + 4 * ((i >> 1) & 3); }
 
+// Where a tile of rows of kUnits 16-byte units holds unit u of row r: the units
+// of a 128-byte line change places with the row, so that eight lanes that read
+// one unit of neighbouring rows, and sixteen that write half units, along rows
+// or across them (kAcross), meet 32 different banks each.
+template <int kUnits, bool kAcross>
+__device__ __forceinline__ int unit_at(int r, int u) {
+  if constexpr (kUnits >= 8) {
+    const int h = kAcross ? (r ^ (r >> 3)) & 7
+                          : (r & 7) ^ ((r >> 3) & 1) ^ ((r >> 2) & 4);
+    return r * kUnits + (u ^ h);
+  } else {
+    const int line = r >> 1;
+    const int h = ((line ^ (line >> 2)) & 1) | (line & 2) | ((line >> 1) & 4);
+    return line * 8 + ((((r & 1) << 2) | u) ^ h);
+  }
+}
+
+// The same in bytes for the first of four rows r0 .. r0 + 3 (r0 a multiple of 4)
+// and half a unit, and from there for the others: the places differ by bits of
+// the row alone.
+template <int kUnits, bool kAcross>
+__device__ __forceinline__ uint32_t half_at(int r0, int half) {
+  return 16 * unit_at<kUnits, kAcross>(r0, half >> 1) + 8 * (half & 1);
+}
+template <int kUnits>
+__device__ __forceinline__ uint32_t half_below(uint32_t at, int r) {
+  return kUnits >= 8 ? (at ^ (16 * r)) + r * kUnits * 16
+                     : (at ^ (16 * (((r & 1) << 2) | (r >> 1)))) + (r >> 1) * 128;
+}
+
+// A buffer resource of `bytes` bytes at p: reads behind them give 0, writes
+// there are dropped.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
+}
+
 // A tile of kRows rows and kWidth channels in registers, on its way from memory
 // to LDS, in blocks of 4 x 4 values: eight blocks side by side and eight below
 // each other per wavefront, so that memory is read 64 or 128 bytes at a time and
 // LDS is written, along rows and along columns, without bank conflicts.
-template <typename T, int kRows, int kWidth>
+template <typename T, int kRows, int kWidth, int kThreads>
 struct Tile {
   static constexpr int kIn = Pieces<T>::kIn;
   static constexpr int kBlocks = kRows / 4 * (kWidth / 4);
-  static constexpr int kIts = (kBlocks + 255) / 256;
-  Packed<T, 4> v[kIts][4];
+  static constexpr int kIts = (kBlocks + kThreads - 1) / kThreads;
+  using Word = std::conditional_t<sizeof(T) == 2, u32x2, u32x4>;
+  // Where this lane's blocks lie: in memory from the tile's lowest row on (from
+  // its first row upwards, from its last row downwards), and in LDS.
+  struct Places {
+    uint32_t from[kIts], row[kIts], col[kIts];
+    __device__ __forceinline__ Places(uint32_t pitch, bool up, bool rows_placed, bool cols_placed) {
+#pragma unroll
+      for (int it = 0; it < kIts; ++it) {
+        int rb, cb;
+        at(threadIdx.x, it, rb, cb);
+        const uint32_t down = (uint32_t)(4 * rb) * pitch;
+        from[it] = (up ? down : 0u - down) + (uint32_t)(4 * cb) * (uint32_t)sizeof(T);
+        row[it] = half_at<kWidth / 8, false>(rows_placed ? place(rb) : 4 * rb, cb);
+        col[it] = half_at<kRows / 8, true>(cols_placed ? place(cb) : 4 * cb, rb);
+      }
+    }
+  };
+
+  Word v[kIts][4];
+  T tail;   // the last value in memory of rows of an odd number of 2-byte values: half of a
+            // word that ends behind the buffer
 
   static __device__ __forceinline__ bool on(int it) {
-    return kBlocks % 256 == 0 || (int)threadIdx.x + 256 * it < kBlocks;
+    return kBlocks % kThreads == 0 || (int)threadIdx.x + kThreads * it < kBlocks;
   }
   static __device__ __forceinline__ void at(int tid, int it, int& rb, int& cb) {
-    const int i = tid + 256 * it, rest = i >> 6;
+    const int i = tid + kThreads * it, rest = i >> 6;
     constexpr int kWide = kWidth / 32;
     cb = (i & 7) + 8 * (rest % kWide);
     rb = ((i >> 3) & 7) + 8 * (rest / kWide);
   }
 
-  // base: the tile's lowest row; up: whether that is its first. Rows from held
-  // on are read as the last one, and blocks at the row's end as its last four
-  // values (there are four): every access is to the tile's own rows. `settle`
-  // makes them what they are.
-  __device__ __forceinline__ void load(const T* base, uint32_t pitch, bool up, int held,
-                                       int width) {
-    const char* from = reinterpret_cast<const char*>(base);
+  // base: the tile's lowest row; up: whether that is its first; held: the rows
+  // there are. Rows from held on lie behind the buffer (or, their offsets being
+  // negative, far behind it) and are 0; `settle` sees to the channels.
+  __device__ __forceinline__ void load(const Places& k, const T* base, uint32_t pitch, bool up,
+                                       int held, int width) {
+    const auto buffer =
+        buffer_of(base, (uint32_t)(held - 1) * pitch + (uint32_t)width * (uint32_t)sizeof(T));
+    if constexpr (sizeof(T) == 2)
+      if (width & 1)
+        tail = *reinterpret_cast<const T*>(reinterpret_cast<const char*>(base + width - 1) +
+                                           (uint32_t)(held - 1) * pitch);
+    const uint32_t step = up ? pitch : 0u - pitch;
+    const uint32_t first = up ? 0u : (uint32_t)(held - 1) * pitch;
+#pragma unroll
+    for (int it = 0; it < kIts; ++it) {
+      uint32_t to = k.from[it] + first;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (sizeof(T) == 2)
+          v[it][r] = __builtin_amdgcn_raw_buffer_load_b64(buffer, to, 0, 0);
+        else
+          v[it][r] = __builtin_amdgcn_raw_buffer_load_b128(buffer, to, 0, 0);
+        to += step;
+      }
+    }
+  }
+
+  // 0 in channels from width on, which were read from what lies there; and the
+  // tail.
+  __device__ __forceinline__ void settle(bool up, int held, int width) {
     const int tid = fresh(threadIdx.x);
 #pragma unroll
     for (int it = 0; it < kIts; ++it) {
       int rb, cb;
       at(tid, it, rb, cb);
-      if (!on(it)) rb = 0;
-      int c = 4 * cb;
-      c = c + 4 <= width ? c : width - 4;
-      const uint32_t side = (uint32_t)c * sizeof(T);
-      if (held == kRows) {
-        uint32_t to = (uint32_t)(up ? 4 * rb : held - 1 - 4 * rb) * pitch + side;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          v[it][r] = row_load<T, 4>(reinterpret_cast<const T*>(from + to));
-          to = up ? to + pitch : to - pitch;
-        }
+      const int left = width - 4 * cb;
+      Word keep;
+      if constexpr (sizeof(T) == 2) {
+        keep[0] = left >= 2 ? ~0u : left == 1 ? 0xffffu : 0u;
+        keep[1] = left >= 4 ? ~0u : left == 3 ? 0xffffu : 0u;
       } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          int i = 4 * rb + r;
-          i = i < held ? i : held - 1;
-          i = up ? i : held - 1 - i;
-          v[it][r] = row_load<T, 4>(reinterpret_cast<const T*>(from + ((uint32_t)i * pitch + side)));
-        }
+        for (int j = 0; j < 4; ++j) keep[j] = left > j ? ~0u : 0u;
       }
-    }
-  }
-
-  // The same for rows of fewer than four values.
-  __device__ __forceinline__ void load_narrow(const T* base, uint32_t pitch, bool up, int held,
-                                              int width) {
-    const char* from = reinterpret_cast<const char*>(base);
-    const int tid = fresh(threadIdx.x);
-#pragma unroll
-    for (int it = 0; it < kIts; ++it) {
-      int rb, cb;
-      at(tid, it, rb, cb);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        v[it][r] = Packed<T, 4>{};
-        int i = 4 * rb + r;
-        if (!on(it) || cb || i >= held) continue;
-        if (!up) i = held - 1 - i;
-        const T* p = reinterpret_cast<const T*>(from + (uint32_t)i * pitch);
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-          if (j < width) v[it][r].v[j] = p[j];
-      }
-    }
-  }
-
-  // 0 in rows from held on and in channels from width on.
-  __device__ __forceinline__ void settle(int held, int width) {
-    const int tid = fresh(threadIdx.x);
-#pragma unroll
-    for (int it = 0; it < kIts; ++it) {
-      int rb, cb;
-      at(tid, it, rb, cb);
-      const int skip = 4 * cb + 4 - width;   // values that the block was shifted back by
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        Packed<T, 4> x = v[it][r];
-        if constexpr (sizeof(T) == 2) {
-          uint64_t w = __builtin_bit_cast(uint64_t, x);
-          w = skip > 0 ? (skip < 4 ? w >> (16 * skip) : 0) : w;
-          w = 4 * rb + r < held ? w : 0;
-          x = __builtin_bit_cast(decltype(x), w);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            T y = x.v[j];
-#pragma unroll
-            for (int k = 1; k < 4; ++k) y = skip == k ? (j + k < 4 ? x.v[(j + k) & 3] : T(0)) : y;
-            y = skip < 4 && 4 * rb + r < held ? y : T(0);
-            v[it][r].v[j] = y;
-          }
-          continue;
-        }
-        v[it][r] = x;
+        v[it][r] &= keep;
+        if constexpr (sizeof(T) == 2)
+          if ((width & 1) && 4 * rb + r == (up ? held - 1 : 0) && (left == 1 || left == 3))
+            v[it][r][left / 2] = __builtin_bit_cast(uint16_t, tail);
       }
     }
   }
 
   // Whether a value is not finite: the largest of the words without signs is.
   __device__ __forceinline__ bool any_bad() const {
-    using u16x2 = __attribute__((ext_vector_type(2))) uint16_t;
     if constexpr (sizeof(T) == 2) {
+      using u16x2 = __attribute__((ext_vector_type(2))) uint16_t;
       constexpr uint16_t kInf = std::is_same_v<T, bf16_t> ? 0x7f80 : 0x7c00;
       u16x2 m = {0, 0};
 #pragma unroll
       for (int it = 0; it < kIts; ++it)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const u32x2 w = __builtin_bit_cast(u32x2, v[it][r]) & 0x7fff7fffu;
-          m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, (uint32_t)w[0]));
-          m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, (uint32_t)w[1]));
-        }
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            m = __builtin_elementwise_max(
+                m, __builtin_bit_cast(u16x2, (uint32_t)(v[it][r][j] & 0x7fff7fffu)));
       return m[0] >= kInf || m[1] >= kInf;
     } else {
       uint32_t m = 0;
@@ -413,7 +433,7 @@ struct Tile {
         for (int r = 0; r < 4; ++r)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t w = __builtin_bit_cast(uint32_t, v[it][r].v[j]) & 0x7fffffffu;
+            const uint32_t w = v[it][r][j] & 0x7fffffffu;
             m = m > w ? m : w;
           }
       return m >= 0x7f800000u;
@@ -430,58 +450,54 @@ struct Tile {
       at(tid, it, rb, cb);
 #pragma unroll
       for (int r = 3; r >= 0; --r) {
+        const auto x = __builtin_bit_cast(Packed<T, 4>, v[it][r]);
         bool bad = false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bad |= !__builtin_isfinite((float)v[it][r].v[j]);
+        for (int j = 0; j < 4; ++j) bad |= !__builtin_isfinite((float)x.v[j]);
         first = bad && on(it) && 4 * rb + r < first ? 4 * rb + r : first;
       }
     }
     return first;
   }
 
-  // Into LDS: rows [kIn][kRows][kWidth + 8] and columns [kIn][kWidth][kRows + 8],
+  // Into LDS: rows [kIn][kRows][kWidth] and columns [kIn][kWidth][kRows],
   // whichever is not null.
-  __device__ __forceinline__ void store(uint16_t* rows, bool rows_placed, uint16_t* cols,
-                                        bool cols_placed) const {
-    constexpr int kRowPitch = kWidth + 8, kColPitch = kRows + 8;
-    const int tid = fresh(threadIdx.x);
+  __device__ __forceinline__ void store(const Places& k, uint16_t* rows, uint16_t* cols) const {
 #pragma unroll
     for (int it = 0; it < kIts; ++it) {
       if (!on(it)) continue;
-      int rb, cb;
-      at(tid, it, rb, cb);
       uint32_t w[4][kIn][2];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if constexpr (kIn == 1) {
-          const u32x2 x = __builtin_bit_cast(u32x2, v[it][r]);
-          w[r][0][0] = x[0], w[r][0][1] = x[1];
+          w[r][0][0] = v[it][r][0], w[r][0][1] = v[it][r][1];
         } else {
+          const auto y = __builtin_bit_cast(Packed<T, 4>, v[it][r]);
           float x[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = (float)v[it][r].v[j];
+          for (int j = 0; j < 4; ++j) x[j] = (float)y.v[j];
           cut<kIn, 4>(x, w[r]);
         }
       }
+      constexpr int kBytes = kRows * kWidth * 2;   // of a piece's tile
+      const uint32_t row = fresh(k.row[it]), col = fresh(k.col[it]);
 #pragma unroll
-      for (int n = 0; n < kIn; ++n) {
-        if (rows) {
-          const int at0 = rows_placed ? place(rb) : 4 * rb;
+      for (int r = 0; r < 4; ++r) {
+        char* to = reinterpret_cast<char*>(rows) + half_below<kWidth / 8>(row, r);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            *reinterpret_cast<u32x2*>(rows + (n * kRows + at0 + r) * kRowPitch + 4 * cb) =
-                u32x2{w[r][n][0], w[r][n][1]};
-        }
-        if (cols) {
-          const int at0 = cols_placed ? place(cb) : 4 * cb;
+        for (int n = 0; n < kIn; ++n)
+          if (rows) *reinterpret_cast<u32x2*>(to + n * kBytes) = u32x2{w[r][n][0], w[r][n][1]};
+      }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
-            *reinterpret_cast<u32x2*>(cols + (n * kWidth + at0 + c) * kColPitch + 4 * rb) =
+      for (int c = 0; c < 4; ++c) {
+        char* to = reinterpret_cast<char*>(cols) + half_below<kRows / 8>(col, c);
+        const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
+#pragma unroll
+        for (int n = 0; n < kIn; ++n)
+          if (cols)
+            *reinterpret_cast<u32x2*>(to + n * kBytes) =
                 u32x2{__builtin_amdgcn_perm(w[1][n][c / 2], w[0][n][c / 2], sel),
                       __builtin_amdgcn_perm(w[3][n][c / 2], w[2][n][c / 2], sel)};
-          }
-        }
       }
     }
   }
@@ -519,32 +535,38 @@ __device__ __forceinline__ int64_t across(const AttnJob<T>& p, int64_t row) {
   return i > 0 && i <= p.n_seq && p.off[i] > row ? i - 1 : -1;
 }
 
-template <typename T, int DA>
+template <typename T, int DA, int kWide>
 struct ChunkLds {
   static constexpr int C = Pieces<T>::kChunk, kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid;
   static constexpr int kScores = C == 64 ? 6 : 2;
-  uint16_t a[kIn][C][DA + 8];
-  uint16_t b[kIn][C][DA + 8];       // rows as `place` has them
-  uint16_t bt[kIn][DA][C + 8];      // columns as `place` has them
-  uint16_t ct[kIn][kSlab][C + 8];
+  uint16_t a[kIn][C * DA];
+  uint16_t b[kIn][C * DA];       // rows as `place` has them
+  uint16_t bt[kIn][DA * C];      // columns as `place` has them
+  uint16_t ct[kIn][kWide * C];
   uint16_t p[kMid][kScores][64][8];
   int bad;
 };
 
-template <typename T, int DA, bool kOut>
-__global__ __launch_bounds__(256, 2) void logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
+template <typename T, int DA, int kWaves, bool kOut>
+__global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJob<T> p,
+                                                                           Walk walk) {
+  constexpr int kThreads = 64 * kWaves, kWide = 16 * kWaves;
   constexpr int kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid, kState = Pieces<T>::kState;
   constexpr int C = Pieces<T>::kChunk, kI = C / 16, kT = C / 32, kS = DA / 32, kU = DA / 16;
-  __shared__ __attribute__((aligned(16))) ChunkLds<T, DA> lds;
+  __shared__ __attribute__((aligned(16))) ChunkLds<T, DA, kWide> lds;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int step = p.back ? -1 : 1;
   if (tid == 0) lds.bad = C;
+  const uint32_t sa = (uint32_t)(p.as * sizeof(T)), sb = (uint32_t)(p.bs * sizeof(T)),
+                 sc = (uint32_t)(p.cs * sizeof(T));
+  const typename Tile<T, C, DA, kThreads>::Places la(sa, !p.back, false, false), lb(sb, !p.back, true, true);
+  const typename Tile<T, C, kWide, kThreads>::Places lc(sc, !p.back, false, false);
   for (int64_t item = blockIdx.x; item < walk.items; item += gridDim.x) {
     const int slab = (int)(item % walk.slabs);
     const int h = (int)(item / walk.slabs % p.heads);
     const int64_t which = item / walk.slabs / p.heads;   // sequence or part
-    const int c0 = slab * kSlab;
+    const int c0 = slab * kWide;
     const T* pa = p.a + (int64_t)(h / p.share_a) * p.da;
     const T* pb = p.b + (int64_t)(h / p.share_b) * p.da;
     const T* pc = p.c + (int64_t)(h / p.share_c) * p.dc + c0;
@@ -555,20 +577,26 @@ __global__ __launch_bounds__(256, 2) void logmel_attn_chunk_kernel(AttnJob<T> p,
     const int64_t cells = (int64_t)p.da * p.dc;
 
     // weights of this lane's scores: block (rows 16 bi, columns 32 t and b)
+    // of eight wavefronts the first four take the blocks on the diagonal
     constexpr int kMine = C == 64 ? 3 : 1;
-    const int half = wave & 1, pair = wave >> 1;
-    float ws[kMine][4];
-    float enter[kI];
+    const int half = wave & 1, pair = (wave >> 1) & 1;
+    auto mine = [&](int m) { return kWaves == 4 || (m == 1) == (wave >= 4); };
+    float ws[kMine][4], enter[kI];
+    uint32_t seen[2][4];   // all bits where row j of b is at or before row i of a
+                           // (the blocks on the diagonal: the first and the third)
     if constexpr (kOut) {
 #pragma unroll
       for (int m = 0; m < kMine; ++m) {
         const int bi = m ? 2 + pair : pair, t = m == 2;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          ws[m][r] = p.gamma * power(16 * bi + n - (32 * t + 8 * g + 4 * half + r));
+        for (int r = 0; r < 4; ++r) {
+          const int age = 16 * bi + n - (32 * t + 8 * g + 4 * half + r);
+          ws[m][r] = p.beta * p.gamma * power(age);
+          if (m != 1) seen[m / 2][r] = age >= 0 ? ~0u : 0u;
+        }
       }
 #pragma unroll
-      for (int i = 0; i < kI; ++i) enter[i] = power(16 * i + n);
+      for (int i = 0; i < kI; ++i) enter[i] = p.beta * power(16 * i + n);
     }
     // of the rows that enter the state, `left` rows before the next chunk's first
     float wc_[kT][8];
@@ -585,6 +613,13 @@ __global__ __launch_bounds__(256, 2) void logmel_attn_chunk_kernel(AttnJob<T> p,
           const int j = 32 * t + 8 * g + e;
           wc_[t][e] = j <= to ? p.gamma * power(to - j) : 0.0f;
         }
+    };
+
+    auto row_frag = [&](const uint16_t* tile, int r, int u) __attribute__((always_inline)) {
+      return frag(tile + 8 * unit_at<DA / 8, false>(r, u));
+    };
+    auto col_frag = [&](const uint16_t* tile, int r, int u) __attribute__((always_inline)) {
+      return frag(tile + 8 * unit_at<C / 8, true>(r, u));
     };
 
     f32x4 w[kU];
@@ -616,40 +651,30 @@ __global__ __launch_bounds__(256, 2) void logmel_attn_chunk_kernel(AttnJob<T> p,
     auto segment = [&](int64_t lo, int64_t hi, bool last) __attribute__((always_inline)) {
       const int64_t rows = hi - lo;
       const int64_t first = p.back ? hi - 1 : lo;
-      Tile<T, C, DA> ta, tb;
-      Tile<T, C, kSlab> tc;
-      const int wide = wc < kSlab ? wc : kSlab;
-      const uint32_t sa = (uint32_t)(p.as * sizeof(T)), sb = (uint32_t)(p.bs * sizeof(T)),
-                     sc = (uint32_t)(p.cs * sizeof(T));
+      Tile<T, C, DA, kThreads> ta, tb;
+      Tile<T, C, kWide, kThreads> tc;
+      const int wide = wc < kWide ? wc : kWide;
       auto load = [&](int64_t at, int held) __attribute__((always_inline)) {
         const int64_t row = p.back ? first - at - held + 1 : first + at;   // the lowest
-        auto one = [&](auto& t, const T* base, int64_t stride, uint32_t pitch, int width)
-                       __attribute__((always_inline)) {
-          if (width >= 4)
-            t.load(base + row * stride, pitch, !p.back, held, width);
-          else
-            t.load_narrow(base + row * stride, pitch, !p.back, held, width);
-        };
-        if constexpr (kOut) one(ta, pa, p.as, sa, p.da);
-        one(tb, pb, p.bs, sb, p.da);
-        one(tc, pc, p.cs, sc, wide);
+        if constexpr (kOut) ta.load(la, pa + row * p.as, sa, !p.back, held, p.da);
+        tb.load(lb, pb + row * p.bs, sb, !p.back, held, p.da);
+        tc.load(lc, pc + row * p.cs, sc, !p.back, held, wide);
       };
       auto settle = [&](int held) __attribute__((always_inline)) {
-        if (held < C || p.da < DA) {
-          if constexpr (kOut)
-            if (p.da >= 4) ta.settle(held, p.da);
-          if (p.da >= 4) tb.settle(held, p.da);
+        if (p.da < DA) {
+          if constexpr (kOut) ta.settle(!p.back, held, p.da);
+          tb.settle(!p.back, held, p.da);
         }
-        if ((held < C || wide < kSlab) && wide >= 4) tc.settle(held, wide);
+        if (wide < kWide) tc.settle(!p.back, held, wide);
       };
       auto stage = [&]() __attribute__((always_inline)) {
         if constexpr (kOut) {
-          ta.store(&lds.a[0][0][0], false, nullptr, false);
-          tb.store(&lds.b[0][0][0], true, &lds.bt[0][0][0], true);
+          ta.store(la, lds.a[0], nullptr);
+          tb.store(lb, lds.b[0], lds.bt[0]);
         } else {
-          tb.store(nullptr, false, &lds.bt[0][0][0], true);
+          tb.store(lb, nullptr, lds.bt[0]);
         }
-        tc.store(nullptr, false, &lds.ct[0][0][0], false);
+        tc.store(lc, nullptr, lds.ct[0]);
       };
       auto held_at = [&](int64_t at) { return (int)(rows - at < C ? rows - at : C); };
       load(0, held_at(0));
@@ -681,6 +706,7 @@ __global__ __launch_bounds__(256, 2) void logmel_attn_chunk_kernel(AttnJob<T> p,
           // the scores, transposed: block (t, half) of 16 rows of b by rows 16 bi of a
 #pragma unroll
           for (int m = 0; m < kMine; ++m) {
+            if (!mine(m)) continue;
             const int bi = m ? 2 + pair : pair, t = m == 2;
             f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -688,16 +714,17 @@ __global__ __launch_bounds__(256, 2) void logmel_attn_chunk_kernel(AttnJob<T> p,
               bf16x8 fb[kIn], fa[kIn];
 #pragma unroll
               for (int k = 0; k < kIn; ++k) {
-                fb[k] = frag(&lds.b[k][32 * t + 16 * half + n][32 * s + 8 * g]);
-                fa[k] = frag(&lds.a[k][16 * bi + n][32 * s + 8 * g]);
+                fb[k] = row_frag(lds.b[k], 32 * t + 16 * half + n, 4 * s + g);
+                fa[k] = row_frag(lds.a[k], 16 * bi + n, 4 * s + g);
               }
               mma(acc, fb, fa);
             }
             float x[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const int i = 16 * bi + n, j = 32 * t + 8 * g + 4 * half + r;
-              x[r] = j <= i ? ws[m][r] * acc[r] : 0.0f;
+              x[r] = ws[m][r] * acc[r];
+              if (m != 1)
+                x[r] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x[r]) & seen[m / 2][r]);
             }
             uint32_t piece[kMid][2];
             cut<kMid, 4>(x, piece);
@@ -707,18 +734,10 @@ __global__ __launch_bounds__(256, 2) void logmel_attn_chunk_kernel(AttnJob<T> p,
               *reinterpret_cast<u32x2*>(&lds.p[k][f][lane][4 * half]) =
                   u32x2{piece[k][0], piece[k][1]};
           }
-          __syncthreads();
         }
 
-        bf16x8 fc[kT][kIn];
-#pragma unroll
-        for (int t = 0; t < kT; ++t)
-#pragma unroll
-          for (int k = 0; k < kIn; ++k)
-            fc[t][k] = frag(&lds.ct[k][16 * wave + n][32 * t + 8 * g]);
-
+        f32x4 o[kI];
         if constexpr (kOut) {
-          f32x4 o[kI];
 #pragma unroll
           for (int i = 0; i < kI; ++i) o[i] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -735,45 +754,22 @@ __global__ __launch_bounds__(256, 2) void logmel_attn_chunk_kernel(AttnJob<T> p,
             for (int i = 0; i < kI; ++i) {
               bf16x8 fa[kIn];
 #pragma unroll
-              for (int k = 0; k < kIn; ++k) fa[k] = frag(&lds.a[k][16 * i + n][32 * s + 8 * g]);
+              for (int k = 0; k < kIn; ++k) fa[k] = row_frag(lds.a[k], 16 * i + n, 4 * s + g);
               mma(o[i], fw, fa);
             }
           }
 #pragma unroll
-          for (int i = 0; i < kI; ++i) {
+          for (int i = 0; i < kI; ++i)
 #pragma unroll
             for (int r = 0; r < 4; ++r) o[i][r] *= enter[i];
-#pragma unroll
-            for (int t = 0; t <= i / 2; ++t) {
-              bf16x8 fp[kMid];
-              const int f = i < 2 ? i : 2 * i - 2 + t;
-#pragma unroll
-              for (int k = 0; k < kMid; ++k) fp[k] = frag(&lds.p[k][f][lane][0]);
-              mma(o[i], fc[t], fp);
-            }
-            if (16 * i + n < held) {
-              const int64_t row = first + step * (at + 16 * i + n);
-              const int c = 16 * wave + 4 * g;
-              float x[4];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) x[r] = p.beta * o[i][r];
-              const int64_t to = row * p.os + (int64_t)h * p.dc + c0 + c;
-              auto put = [&](auto* out) {
-                if (c + 4 <= wc) {
-                  row_store(out + to, x);
-                } else {
-#pragma unroll
-                  for (int r = 0; r < 3; ++r)
-                    if (c + r < wc) out[to + r] = (std::decay_t<decltype(*out)>)x[r];
-                }
-              };
-              if (p.of)
-                put(p.of);
-              else
-                put(p.o);
-            }
-          }
         }
+
+        bf16x8 fc[kT][kIn];
+#pragma unroll
+        for (int t = 0; t < kT; ++t)
+#pragma unroll
+          for (int k = 0; k < kIn; ++k)
+            fc[t][k] = col_frag(lds.ct[k], 16 * wave + n, 4 * t + g);
 
         weigh(last && next == rows ? held - 1 : held);
 #pragma unroll
@@ -799,11 +795,69 @@ __global__ __launch_bounds__(256, 2) void logmel_attn_chunk_kernel(AttnJob<T> p,
           for (int u = 0; u < kU; ++u) {
             bf16x8 fb[kIn];
 #pragma unroll
-            for (int k = 0; k < kIn; ++k) fb[k] = frag(&lds.bt[k][16 * u + n][32 * t + 8 * g]);
+            for (int k = 0; k < kIn; ++k) fb[k] = col_frag(lds.bt[k], 16 * u + n, 4 * t + g);
             mma(w[u], fb, fw);
           }
         }
-        __syncthreads();   // the tiles are read to the end
+        // the scores are whole, and the tiles read to the end: the next chunk's may
+        // be written (its scores after a barrier more)
+        __syncthreads();
+
+        if constexpr (kOut) {
+          // rows i of the output: four channels of a row per lane
+          const int64_t row = p.back ? first - at - held + 1 : first + at;   // the lowest
+          const int64_t to = row * p.os + (int64_t)h * p.dc + c0;
+          const uint32_t size = p.of ? 4 : (uint32_t)sizeof(T), pitch = (uint32_t)p.os * size;
+          const auto buffer =
+              buffer_of(p.of ? static_cast<const void*>(p.of + to) : p.o + to,
+                        (uint32_t)(held - 1) * pitch + (uint32_t)(wc < kWide ? wc : kWide) * size);
+          const int c = 16 * wave + 4 * g;
+          const uint32_t side = (uint32_t)c * size;
+          auto at_row = [&](int i) __attribute__((always_inline)) {
+            const int r = 16 * i + n;
+            return (uint32_t)(p.back ? held - 1 - r : r) * pitch + side;
+          };
+#pragma unroll
+          for (int i = 0; i < kI; ++i) {
+#pragma unroll
+            for (int t = 0; t <= i / 2; ++t) {
+              bf16x8 fp[kMid];
+              const int f = i < 2 ? i : 2 * i - 2 + t;
+#pragma unroll
+              for (int k = 0; k < kMid; ++k) fp[k] = frag(&lds.p[k][f][lane][0]);
+              mma(o[i], fc[t], fp);
+            }
+          }
+          if (wc < kWide) {   // value by value, those that there are
+#pragma unroll
+            for (int i = 0; i < kI; ++i)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t to = c + j < wc && 16 * i + n < held ? at_row(i) + j * size : ~0u - 3u;
+                const float y = o[i][j];
+                if (p.of || sizeof(T) == 4)
+                  __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, y), buffer,
+                                                        to, 0, 0);
+                else if constexpr (sizeof(T) == 2)
+                  __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)y),
+                                                        buffer, to, 0, 0);
+              }
+          } else if (p.of || sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < kI; ++i)
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[i]), buffer,
+                                                     at_row(i), 0, 0);
+          } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < kI; ++i) {
+              Packed<T, 4> y;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y.v[j] = (T)o[i][j];
+              __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), buffer,
+                                                    at_row(i), 0, 0);
+            }
+          }
+        }
         at = next;
       }
     };
@@ -943,13 +997,14 @@ AttnSplit split_of(const logmel_attention_input& in, int da, int dc, int64_t wid
     return s;
   }
   const int64_t chunk = in.type == LOGMEL_BF16 ? 64 : 32;
-  const int64_t lanes = in.heads * ceil_div(dc, kSlab);   // workgroups side by side
-  const int64_t slots = 2 * (int64_t)cus;
+  const int64_t lanes = in.heads;                          // workgroups side by side
+  const int64_t slots = (dc > 64 ? 1 : 2) * (int64_t)cus;  // resident ones
   // in chunks one after the other
   const int64_t by_seq = ceil_div(longest, chunk);
   const int64_t seq_all = ceil_div(in.rows, chunk) * lanes / slots;
   const double seq_time = (double)(by_seq > seq_all ? by_seq : seq_all);
-  int64_t rows = ceil_div(ceil_div(in.rows * lanes, slots), chunk) * chunk;
+  const int64_t most = slots / lanes;   // parts in one round of workgroups
+  int64_t rows = ceil_div(ceil_div(in.rows, most < 1 ? 1 : most), chunk) * chunk;
   rows = rows < 4 * chunk ? 4 * chunk : rows;
   const int64_t parts = ceil_div(in.rows, rows);
   const double part_time =
@@ -970,7 +1025,7 @@ int64_t kept_of(const AttnSplit& s, const logmel_attention_input& in) {
   return s.how == AttnSplit::kParts ? s.parts * in.heads * in.head_dk * in.head_dv : 0;
 }
 
-template <typename T, int DA>
+template <typename T, int DA, int kWaves>
 hipError_t launch_chunks(const AttnJob<T>& p, const AttnSplit& s, Walk k, int64_t lanes,
                          hipStream_t stream) {
   auto grid = [](int64_t items) { return (unsigned)(items < (1 << 22) ? items : 1 << 22); };
@@ -978,14 +1033,16 @@ hipError_t launch_chunks(const AttnJob<T>& p, const AttnSplit& s, Walk k, int64_
     k.part_rows = s.part_rows;
     k.parts = s.parts;
     k.items = s.parts * lanes;
-    logmel_attn_chunk_kernel<T, DA, false><<<grid(k.items), 256, 0, stream>>>(p, k);
+    logmel_attn_chunk_kernel<T, DA, kWaves, false>
+        <<<grid(k.items), 64 * kWaves, 0, stream>>>(p, k);
     const int64_t cells = (int64_t)p.heads * p.da * p.dc;
     logmel_attn_between_kernel<T>
         <<<(unsigned)ceil_div(cells, 256), 256, 0, stream>>>(p, k);
   } else {
     k.items = p.n_seq * lanes;
   }
-  logmel_attn_chunk_kernel<T, DA, true><<<grid(k.items), 256, 0, stream>>>(p, k);
+  logmel_attn_chunk_kernel<T, DA, kWaves, true>
+      <<<grid(k.items), 64 * kWaves, 0, stream>>>(p, k);
   return hipGetLastError();
 }
 
@@ -996,6 +1053,7 @@ hipError_t launch_job(const AttnJob<T>& p, const logmel_attention_input& in, flo
   const int slabs = (p.dc + kSlab - 1) / kSlab;
   int64_t widest = p.as > p.bs ? p.as : p.bs;
   widest = widest > p.cs ? widest : p.cs;
+  widest = widest > p.os ? widest : p.os;
   const AttnSplit s = split_of(in, p.da, p.dc, widest, cus);
   if (s.how == AttnSplit::kRows) {
     const int64_t items = p.n_seq * p.heads * slabs;
@@ -1007,13 +1065,17 @@ hipError_t launch_job(const AttnJob<T>& p, const logmel_attention_input& in, flo
     return hipGetLastError();
   }
   Walk k{};
-  k.slabs = slabs;
+  k.slabs = 1;
   k.between = ws;
   k.kept = in_place && s.how == AttnSplit::kParts ? ws + between_of(s, in) : nullptr;
-  const int64_t lanes = (int64_t)p.heads * slabs;
-  if (p.da <= 32) return launch_chunks<T, 32>(p, s, k, lanes, stream);
-  if (p.da <= 64) return launch_chunks<T, 64>(p, s, k, lanes, stream);
-  return launch_chunks<T, 128>(p, s, k, lanes, stream);
+  const int64_t lanes = p.heads;
+  auto go = [&](auto waves) {
+    constexpr int W = decltype(waves)::value;
+    if (p.da <= 32) return launch_chunks<T, 32, W>(p, s, k, lanes, stream);
+    if (p.da <= 64) return launch_chunks<T, 64, W>(p, s, k, lanes, stream);
+    return launch_chunks<T, 128, W>(p, s, k, lanes, stream);
+  };
+  return p.dc <= 64 ? go(std::integral_constant<int, 4>{}) : go(std::integral_constant<int, 8>{});
 }
 
 template <typename T>
