@@ -10,6 +10,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
 #include <type_traits>
 
 #include "logmel_rows.h"
@@ -75,12 +76,13 @@ __device__ __forceinline__ float decayed(Decay d, float x) {
 //
 // A workgroup holds the 64 columns of a sequence's and head's state that one
 // slab of c makes: lane (ag, cg) of 16 x 16 holds four columns of every
-// sixteenth row. 16 rows at a time are laid out in LDS, worked one after the
+// sixteenth row. Eight rows at a time are laid out in LDS, worked one after the
 // other, and their products with the state joined at the end. Right for any
 // length; the form for single rows and short pushes, whose time is that of
 // reading and writing the states.
-constexpr int kStepRows = 16;
+constexpr int kStepRows = 8;
 constexpr int kSlab = 64;
+constexpr int kShort = 16;   // rows of the longest sequence that this form is taken for
 
 template <typename T, int DA>
 __global__ __launch_bounds__(256) void logmel_attn_rows_kernel(AttnJob<T> p, int slabs,
@@ -96,45 +98,54 @@ __global__ __launch_bounds__(256) void logmel_attn_rows_kernel(AttnJob<T> p, int
     const int64_t seq = item / slabs / p.heads;
     const Run run = run_of(p, seq);
     const int c0 = slab * kSlab;
-    const Decay lambda = decay_of(p.log_decay[h], 1.0f);
     const float* in = p.state ? p.state + (seq * p.heads + h) * p.da * p.dc : nullptr;
     float* out = p.state_out ? p.state_out + (seq * p.heads + h) * p.da * p.dc : nullptr;
-    auto at = [&](int a, int c) {
-      return p.transposed ? (int64_t)c * p.da + a : (int64_t)a * p.dc + c;
-    };
+    const int c = c0 + 4 * cg;
+    auto at = [&](int a, int j) { return p.transposed ? (c + j) * p.da + a : a * p.dc + c + j; };
+    const bool whole = !p.transposed && c + 4 <= p.dc;   // four neighbours in memory
     float w[kU][4];
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+    for (int u = 0; u < kU; ++u) {
+      const int a = ag + 16 * u;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int a = ag + 16 * u, c = c0 + 4 * cg + j;
-        w[u][j] = in && a < p.da && c < p.dc ? in[at(a, c)] : 0.0f;
+      for (int j = 0; j < 4; ++j) w[u][j] = 0.0f;
+      if (!in || a >= p.da) continue;
+      if (whole) {
+        const auto v = row_load<float, 4>(in + at(a, 0));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[u][j] = v.v[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c + j < p.dc) w[u][j] = in[at(a, j)];
       }
+    }
+    const Decay lambda = decay_of(p.log_decay[h], 1.0f);
     const int64_t n = run.to > run.from ? run.to - run.from : 0;
     for (int64_t t0 = 0; t0 < n; t0 += kStepRows) {
       const int held = (int)(n - t0 < kStepRows ? n - t0 : kStepRows);
       auto row = [&](int t) { return p.back ? run.to - 1 - t0 - t : run.from + t0 + t; };
       __syncthreads();   // the rows before are read to the end
-      for (int i = tid; i < kStepRows * DA; i += 256) {
+      for (int i = tid; i < held * DA; i += 256) {
         const int t = i / DA, d = i % DA;
-        const bool on = t < held && d < p.da;
+        const bool on = d < p.da;
         sa[t][d] = on ? (float)p.a[row(t) * p.as + h / p.share_a * p.da + d] : 0.0f;
         sb[t][d] = on ? (float)p.b[row(t) * p.bs + h / p.share_b * p.da + d] * p.gamma : 0.0f;
       }
-      for (int i = tid; i < kStepRows * kSlab; i += 256) {
+      for (int i = tid; i < held * kSlab; i += 256) {
         const int t = i / kSlab, d = i % kSlab;
-        const bool on = t < held && c0 + d < p.dc;
+        const bool on = c0 + d < p.dc;
         sc[t][d] = on ? (float)p.c[row(t) * p.cs + h / p.share_c * p.dc + c0 + d] : 0.0f;
       }
       __syncthreads();
       for (int t = 0; t < held; ++t) {
         const Decay keep = p.back && t0 + t == 0 ? Decay{1.0f, 0.0f} : lambda;
-        const float4 c = *reinterpret_cast<const float4*>(&sc[t][4 * cg]);
+        const float4 cv4 = *reinterpret_cast<const float4*>(&sc[t][4 * cg]);
+        const float cv[4] = {cv4.x, cv4.y, cv4.z, cv4.w};
         float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const float a = sa[t][ag + 16 * u], b = sb[t][ag + 16 * u];
-          const float cv[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             w[u][j] = __builtin_fmaf(b, cv[j], decayed(keep, w[u][j]));
@@ -166,12 +177,20 @@ __global__ __launch_bounds__(256) void logmel_attn_rows_kernel(AttnJob<T> p, int
     if (!out) continue;
     const Decay last = p.back && n > 0 ? lambda : Decay{1.0f, 0.0f};
 #pragma unroll
-    for (int u = 0; u < kU; ++u)
+    for (int u = 0; u < kU; ++u) {
+      const int a = ag + 16 * u;
+      if (a >= p.da) continue;
+      float x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int a = ag + 16 * u, c = c0 + 4 * cg + j;
-        if (a < p.da && c < p.dc) out[at(a, c)] = decayed(last, w[u][j]);
+      for (int j = 0; j < 4; ++j) x[j] = decayed(last, w[u][j]);
+      if (whole) {
+        row_store(out + at(a, 0), x);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (c + j < p.dc) out[at(a, j)] = x[j];
       }
+    }
   }
 }
 
@@ -319,7 +338,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint3
 // to LDS, in blocks of 4 x 4 values: eight blocks side by side and eight below
 // each other per wavefront, so that memory is read 64 or 128 bytes at a time and
 // LDS is written, along rows and along columns, without bank conflicts.
-template <typename T, int kRows, int kWidth, int kThreads>
+// kFirst: the thread that takes its first block, so that several tiles that do
+// not fill the workgroup are spread over it.
+template <typename T, int kRows, int kWidth, int kThreads, int kFirst>
 struct Tile {
   static constexpr int kIn = Pieces<T>::kIn;
   static constexpr int kBlocks = kRows / 4 * (kWidth / 4);
@@ -346,11 +367,16 @@ struct Tile {
   T tail;   // the last value in memory of rows of an odd number of 2-byte values: half of a
             // word that ends behind the buffer
 
+  // For a wavefront as a whole: blocks come in 64s.
   static __device__ __forceinline__ bool on(int it) {
-    return kBlocks % kThreads == 0 || (int)threadIdx.x + kThreads * it < kBlocks;
+    static_assert(kBlocks % 64 == 0);
+    if (kBlocks % kThreads == 0) return true;
+    const int first = __builtin_amdgcn_readfirstlane(
+        ((int)threadIdx.x + kThreads - kFirst) % kThreads & ~63);
+    return first + kThreads * it < kBlocks;
   }
   static __device__ __forceinline__ void at(int tid, int it, int& rb, int& cb) {
-    const int i = tid + kThreads * it, rest = i >> 6;
+    const int i = (tid + kThreads - kFirst) % kThreads + kThreads * it, rest = i >> 6;
     constexpr int kWide = kWidth / 32;
     cb = (i & 7) + 8 * (rest % kWide);
     rb = ((i >> 3) & 7) + 8 * (rest / kWide);
@@ -371,6 +397,9 @@ struct Tile {
     const uint32_t first = up ? 0u : (uint32_t)(held - 1) * pitch;
 #pragma unroll
     for (int it = 0; it < kIts; ++it) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[it][r] = Word{};
+      if (!on(it)) continue;
       uint32_t to = k.from[it] + first;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
@@ -512,6 +541,8 @@ struct Walk {
   int64_t part_rows, parts;
   float* between;
   float* kept;
+  int* through;   // of each such place: 0 no sequence lies across it, 1 one does, 2 the one that
+                  // lies across the place before (behind it, backwards) too
   int slabs;
   int64_t items;
 };
@@ -560,8 +591,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
   if (tid == 0) lds.bad = C;
   const uint32_t sa = (uint32_t)(p.as * sizeof(T)), sb = (uint32_t)(p.bs * sizeof(T)),
                  sc = (uint32_t)(p.cs * sizeof(T));
-  const typename Tile<T, C, DA, kThreads>::Places la(sa, !p.back, false, false), lb(sb, !p.back, true, true);
-  const typename Tile<T, C, kWide, kThreads>::Places lc(sc, !p.back, false, false);
+  using TileA = Tile<T, C, DA, kThreads, 0>;
+  using TileB = Tile<T, C, DA, kThreads, TileA::kBlocks % kThreads>;
+  using TileC = Tile<T, C, kWide, kThreads, 2 * TileA::kBlocks % kThreads>;
+  const typename TileA::Places la(sa, !p.back, false, false);
+  const typename TileB::Places lb(sb, !p.back, true, true);
+  const typename TileC::Places lc(sc, !p.back, false, false);
   for (int64_t item = blockIdx.x; item < walk.items; item += gridDim.x) {
     const int slab = (int)(item % walk.slabs);
     const int h = (int)(item / walk.slabs % p.heads);
@@ -571,6 +606,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
     const T* pb = p.b + (int64_t)(h / p.share_b) * p.da;
     const T* pc = p.c + (int64_t)(h / p.share_c) * p.dc + c0;
     const int wc = p.dc - c0;
+    const bool works = 16 * wave < wc;   // has columns of the state
     const float decay = p.log_decay[h];
     const float log2 = decay * 1.44269504088896340736f;
     auto power = [&](int i) { return i > 0 ? __builtin_amdgcn_exp2f(log2 * (float)i) : 1.0f; };
@@ -651,8 +687,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
     auto segment = [&](int64_t lo, int64_t hi, bool last) __attribute__((always_inline)) {
       const int64_t rows = hi - lo;
       const int64_t first = p.back ? hi - 1 : lo;
-      Tile<T, C, DA, kThreads> ta, tb;
-      Tile<T, C, kWide, kThreads> tc;
+      TileA ta;
+      TileB tb;
+      TileC tc;
       const int wide = wc < kWide ? wc : kWide;
       auto load = [&](int64_t at, int held) __attribute__((always_inline)) {
         const int64_t row = p.back ? first - at - held + 1 : first + at;   // the lowest
@@ -711,6 +748,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
             f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int s = 0; s < kS; ++s) {
+              if (s && 32 * s >= p.da) break;
               bf16x8 fb[kIn], fa[kIn];
 #pragma unroll
               for (int k = 0; k < kIn; ++k) {
@@ -737,73 +775,76 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
         }
 
         f32x4 o[kI];
-        if constexpr (kOut) {
+        bf16x8 fc[kT][kIn];
+        if (works) {
+          if constexpr (kOut) {
 #pragma unroll
-          for (int i = 0; i < kI; ++i) o[i] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int i = 0; i < kI; ++i) o[i] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-          for (int s = 0; s < kS; ++s) {
+            for (int s = 0; s < kS; ++s) {
+              if (s && 32 * s >= p.da) break;
+              float x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = w[2 * s + e / 4][e & 3];
+              uint32_t piece[kMid][4];
+              cut<kMid, 8>(x, piece);
+              bf16x8 fw[kMid];
+#pragma unroll
+              for (int k = 0; k < kMid; ++k) fw[k] = frag(piece[k]);
+#pragma unroll
+              for (int i = 0; i < kI; ++i) {
+                bf16x8 fa[kIn];
+#pragma unroll
+                for (int k = 0; k < kIn; ++k) fa[k] = row_frag(lds.a[k], 16 * i + n, 4 * s + g);
+                mma(o[i], fw, fa);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < kI; ++i)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) o[i][r] *= enter[i];
+          }
+
+#pragma unroll
+          for (int t = 0; t < kT; ++t)
+#pragma unroll
+            for (int k = 0; k < kIn; ++k)
+              fc[t][k] = col_frag(lds.ct[k], 16 * wave + n, 4 * t + g);
+
+          weigh(last && next == rows ? held - 1 : held);
+#pragma unroll
+          for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) w[u][r] = decayed(whole, w[u][r]);
+#pragma unroll
+          for (int t = 0; t < kT; ++t) {
             float x[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = w[2 * s + e / 4][e & 3];
-            uint32_t piece[kMid][4];
-            cut<kMid, 8>(x, piece);
-            bf16x8 fw[kMid];
+            for (int e = 0; e < 8; ++e) {
+              x[e] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kMid; ++k) fw[k] = frag(piece[k]);
-#pragma unroll
-            for (int i = 0; i < kI; ++i) {
-              bf16x8 fa[kIn];
-#pragma unroll
-              for (int k = 0; k < kIn; ++k) fa[k] = row_frag(lds.a[k], 16 * i + n, 4 * s + g);
-              mma(o[i], fw, fa);
+              for (int k = kIn - 1; k >= 0; --k) x[e] += (float)fc[t][k][e];
+              x[e] *= wc_[t][e];
             }
-          }
+            uint32_t piece[kState][4];
+            cut<kState, 8>(x, piece);
+            bf16x8 fw[kState];
 #pragma unroll
-          for (int i = 0; i < kI; ++i)
+            for (int k = 0; k < kState; ++k) fw[k] = frag(piece[k]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) o[i][r] *= enter[i];
-        }
-
-        bf16x8 fc[kT][kIn];
+            for (int u = 0; u < kU; ++u) {
+              bf16x8 fb[kIn];
 #pragma unroll
-        for (int t = 0; t < kT; ++t)
-#pragma unroll
-          for (int k = 0; k < kIn; ++k)
-            fc[t][k] = col_frag(lds.ct[k], 16 * wave + n, 4 * t + g);
-
-        weigh(last && next == rows ? held - 1 : held);
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) w[u][r] = decayed(whole, w[u][r]);
-#pragma unroll
-        for (int t = 0; t < kT; ++t) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[e] = 0.0f;
-#pragma unroll
-            for (int k = kIn - 1; k >= 0; --k) x[e] += (float)fc[t][k][e];
-            x[e] *= wc_[t][e];
-          }
-          uint32_t piece[kState][4];
-          cut<kState, 8>(x, piece);
-          bf16x8 fw[kState];
-#pragma unroll
-          for (int k = 0; k < kState; ++k) fw[k] = frag(piece[k]);
-#pragma unroll
-          for (int u = 0; u < kU; ++u) {
-            bf16x8 fb[kIn];
-#pragma unroll
-            for (int k = 0; k < kIn; ++k) fb[k] = col_frag(lds.bt[k], 16 * u + n, 4 * t + g);
-            mma(w[u], fb, fw);
+              for (int k = 0; k < kIn; ++k) fb[k] = col_frag(lds.bt[k], 16 * u + n, 4 * t + g);
+              mma(w[u], fb, fw);
+            }
           }
         }
         // the scores are whole, and the tiles read to the end: the next chunk's may
         // be written (its scores after a barrier more)
         __syncthreads();
 
-        if constexpr (kOut) {
+        if constexpr (kOut) if (works) {
           // rows i of the output: four channels of a row per lane
           const int64_t row = p.back ? first - at - held + 1 : first + at;   // the lowest
           const int64_t to = row * p.os + (int64_t)h * p.dc + c0;
@@ -894,21 +935,23 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
     if constexpr (!kOut) {
       // the state that leaves the part, from the sequence across its end (its
       // start, backwards)
-      const int64_t i = across(p, p.back ? r0 : r1);
-      if (i < 0) continue;
-      const int64_t from = p.off[i], to = p.off[i + 1];
+      const int64_t i = across(p, p.back ? r0 : r1), place = p.back ? which - 1 : which;
+      const int64_t from = i < 0 ? 0 : p.off[i], to = i < 0 ? 0 : p.off[i + 1];
       const bool fresh = p.back ? to <= r1 : from >= r0;
+      if (place < 0 || place >= walk.parts - 1) continue;
+      if (tid == 0 && h == 0) walk.through[place] = i < 0 ? 0 : fresh ? 1 : 2;
+      if (i < 0) continue;
       const int64_t of_seq = (i * p.heads + h) * cells;
       load_state(fresh && p.state ? p.state + of_seq : nullptr, p.back ? one : lambda);
       if (fresh && walk.kept) store_state(walk.kept + (which * p.heads + h) * cells);
       segment(within(from), within(to), false);
-      store_state(walk.between + ((p.back ? which - 1 : which) * p.heads + h) * cells);
+      store_state(walk.between + (place * p.heads + h) * cells);
     } else {
       int64_t i = which;
       bool enters = false;
       if (walk.parts) {
         i = first_from(p, r0);
-        enters = i > 0 && i <= p.n_seq && p.off[i] > r0;
+        enters = which > 0 && i > 0 && i <= p.n_seq && p.off[i] > r0;
         i -= enters;
       }
       const bool end = walk.parts == 0 || which == walk.parts - 1;
@@ -925,35 +968,31 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
 
 // The states between the parts, from those that each part makes: in order (from
 // the last, backwards), the state that enters a part decays through it where
-// its sequence does not end in it.
+// its sequence does not end in it. A lane per cell; 32 places are read at a time.
 template <typename T>
-__global__ __launch_bounds__(256) void logmel_attn_between_kernel(AttnJob<T> p, Walk walk) {
-  constexpr int kBatch = 8;
+__global__ __launch_bounds__(64) void logmel_attn_between_kernel(AttnJob<T> p, Walk walk) {
+  constexpr int kBatch = 32;
   const int64_t cells = (int64_t)p.da * p.dc, all = cells * p.heads;
-  const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t x = (int64_t)blockIdx.x * 64 + threadIdx.x;
   if (x >= all) return;
-  const float decay = p.log_decay[x / cells];
-  const Decay whole = decay_of(decay, (float)walk.part_rows);
+  const Decay whole = decay_of(p.log_decay[x / cells], (float)walk.part_rows);
   const int64_t count = walk.parts - 1;
   float e = 0.0f;
   for (int64_t k0 = 0; k0 < count; k0 += kBatch) {
     float u[kBatch];
+    int how[kBatch];
 #pragma unroll
     for (int m = 0; m < kBatch; ++m) {
-      const int64_t k = k0 + m, b = p.back ? count - 1 - k : k;
-      u[m] = k < count ? walk.between[b * all + x] : 0.0f;
+      const int64_t k = k0 + m < count ? k0 + m : count - 1, b = p.back ? count - 1 - k : k;
+      how[m] = walk.through[b];
+      u[m] = walk.between[b * all + x];   // what it holds is used where a sequence lies across
     }
 #pragma unroll
     for (int m = 0; m < kBatch; ++m) {
-      const int64_t k = k0 + m;
+      const int64_t k = k0 + m, b = p.back ? count - 1 - k : k;
       if (k >= count) break;
-      const int64_t b = p.back ? count - 1 - k : k;
-      // the sequence across the boundary, and whether it crosses the one before
-      const int64_t i = across(p, (b + 1) * walk.part_rows);
-      if (i < 0) continue;
-      const bool through = p.back ? p.off[i + 1] > (b + 2) * walk.part_rows
-                                  : p.off[i] < b * walk.part_rows;
-      e = k > 0 && through ? u[m] + decayed(whole, e) : u[m];
+      if (how[m] == 0) continue;
+      e = how[m] == 2 ? u[m] + decayed(whole, e) : u[m];
       walk.between[b * all + x] = e;
     }
   }
@@ -980,35 +1019,37 @@ __global__ __launch_bounds__(256) void logmel_attn_share_kernel(const float* par
 
 int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
 
-// How a job's rows are split over workgroups.
+// How a call's rows are split over workgroups.
 struct AttnSplit {
   enum How { kRows, kSequences, kParts } how;
   int64_t part_rows, parts;
 };
 
-// widest: the longest row stride.
-AttnSplit split_of(const logmel_attention_input& in, int da, int dc, int64_t widest, int cus) {
+// dc: the widest c of the call's jobs; widest: the longest row stride.
+AttnSplit split_of(const logmel_attention_input& in, int64_t dc, int64_t widest, int cus) {
   AttnSplit s{AttnSplit::kSequences, 0, 0};
   const int64_t longest =
       in.max_frames && in.max_frames < in.rows ? in.max_frames : in.rows;
   // a chunk's rows are addressed by 32 bits from its lowest one
-  if (longest <= kStepRows || widest >= (int64_t)1 << 22) {
+  if (longest <= kShort || widest >= (int64_t)1 << 22) {
     s.how = AttnSplit::kRows;
     return s;
   }
   const int64_t chunk = in.type == LOGMEL_BF16 ? 64 : 32;
   const int64_t lanes = in.heads;                          // workgroups side by side
-  const int64_t slots = (dc > 64 ? 1 : 2) * (int64_t)cus;  // resident ones
+  const int64_t slots = 2 * (int64_t)cus;                  // (of eight wavefronts half as many
+                                                           // are resident, which take turns)
   // in chunks one after the other
   const int64_t by_seq = ceil_div(longest, chunk);
-  const int64_t seq_all = ceil_div(in.rows, chunk) * lanes / slots;
+  const int64_t seq_all = ceil_div(in.rows, chunk) * lanes / slots * (dc > 64 ? 2 : 1);
   const double seq_time = (double)(by_seq > seq_all ? by_seq : seq_all);
   const int64_t most = slots / lanes;   // parts in one round of workgroups
   int64_t rows = ceil_div(ceil_div(in.rows, most < 1 ? 1 : most), chunk) * chunk;
   rows = rows < 4 * chunk ? 4 * chunk : rows;
   const int64_t parts = ceil_div(in.rows, rows);
   const double part_time =
-      1.6 * (double)(rows / chunk) * (double)ceil_div(parts * lanes, slots) + 0.1 * parts + 4.0;
+      1.6 * (double)(rows / chunk) * (double)ceil_div(parts * lanes, slots) * (dc > 64 ? 2 : 1) +
+      0.1 * parts + 4.0;
   if (parts > 1 && part_time < seq_time) {
     s.how = AttnSplit::kParts;
     s.part_rows = rows;
@@ -1017,45 +1058,49 @@ AttnSplit split_of(const logmel_attention_input& in, int da, int dc, int64_t wid
   return s;
 }
 
-// What the parts of a job need of the workspace, in floats.
-int64_t between_of(const AttnSplit& s, const logmel_attention_input& in) {
-  return s.how == AttnSplit::kParts ? (s.parts - 1) * in.heads * in.head_dk * in.head_dv : 0;
-}
-int64_t kept_of(const AttnSplit& s, const logmel_attention_input& in) {
-  return s.how == AttnSplit::kParts ? s.parts * in.heads * in.head_dk * in.head_dv : 0;
-}
+// Where the parts of a call have what in its workspace, in floats: the states
+// between them (of one job at a time), their `through`, the initial states kept.
+struct PartSpace {
+  int64_t between, through, kept;
+  PartSpace(const AttnSplit& s, const logmel_attention_input& in, bool keep)
+      : between(0), through(0), kept(0) {
+    if (s.how != AttnSplit::kParts) return;
+    const int64_t state = in.heads * in.head_dk * in.head_dv;
+    between = (s.parts - 1) * state;
+    through = s.parts;
+    kept = keep ? s.parts * state : 0;
+  }
+  int64_t all() const { return between + through + kept; }
+};
 
 template <typename T, int DA, int kWaves>
-hipError_t launch_chunks(const AttnJob<T>& p, const AttnSplit& s, Walk k, int64_t lanes,
+hipError_t launch_chunks(const AttnJob<T>& p, const AttnSplit& s, Walk k, bool between,
                          hipStream_t stream) {
   auto grid = [](int64_t items) { return (unsigned)(items < (1 << 22) ? items : 1 << 22); };
   if (s.how == AttnSplit::kParts) {
     k.part_rows = s.part_rows;
     k.parts = s.parts;
-    k.items = s.parts * lanes;
-    logmel_attn_chunk_kernel<T, DA, kWaves, false>
-        <<<grid(k.items), 64 * kWaves, 0, stream>>>(p, k);
-    const int64_t cells = (int64_t)p.heads * p.da * p.dc;
-    logmel_attn_between_kernel<T>
-        <<<(unsigned)ceil_div(cells, 256), 256, 0, stream>>>(p, k);
+    k.items = s.parts * p.heads;
+    if (between) {
+      logmel_attn_chunk_kernel<T, DA, kWaves, false>
+          <<<grid(k.items), 64 * kWaves, 0, stream>>>(p, k);
+      logmel_attn_between_kernel<T>
+          <<<(unsigned)ceil_div((int64_t)p.heads * p.da * p.dc, 64), 64, 0, stream>>>(p, k);
+    }
   } else {
-    k.items = p.n_seq * lanes;
+    k.items = p.n_seq * p.heads;
   }
   logmel_attn_chunk_kernel<T, DA, kWaves, true>
       <<<grid(k.items), 64 * kWaves, 0, stream>>>(p, k);
   return hipGetLastError();
 }
 
-// ws: what between_of (and in place kept_of, behind it) asks for.
+// One job. between: whether the states between its parts are yet to be formed.
 template <typename T>
-hipError_t launch_job(const AttnJob<T>& p, const logmel_attention_input& in, float* ws,
-                      bool in_place, int cus, hipStream_t stream) {
-  const int slabs = (p.dc + kSlab - 1) / kSlab;
-  int64_t widest = p.as > p.bs ? p.as : p.bs;
-  widest = widest > p.cs ? widest : p.cs;
-  widest = widest > p.os ? widest : p.os;
-  const AttnSplit s = split_of(in, p.da, p.dc, widest, cus);
+hipError_t launch_job(const AttnJob<T>& p, const AttnSplit& s, const PartSpace& space, float* ws,
+                      bool between, hipStream_t stream) {
   if (s.how == AttnSplit::kRows) {
+    const int slabs = (p.dc + kSlab - 1) / kSlab;
     const int64_t items = p.n_seq * p.heads * slabs;
     const unsigned grid = (unsigned)(items < (1 << 22) ? items : 1 << 22);
     if (p.da <= 64)
@@ -1067,15 +1112,21 @@ hipError_t launch_job(const AttnJob<T>& p, const logmel_attention_input& in, flo
   Walk k{};
   k.slabs = 1;
   k.between = ws;
-  k.kept = in_place && s.how == AttnSplit::kParts ? ws + between_of(s, in) : nullptr;
-  const int64_t lanes = p.heads;
+  k.through = reinterpret_cast<int*>(ws + space.between);
+  k.kept = space.kept ? ws + space.between + space.through : nullptr;
   auto go = [&](auto waves) {
     constexpr int W = decltype(waves)::value;
-    if (p.da <= 32) return launch_chunks<T, 32, W>(p, s, k, lanes, stream);
-    if (p.da <= 64) return launch_chunks<T, 64, W>(p, s, k, lanes, stream);
-    return launch_chunks<T, 128, W>(p, s, k, lanes, stream);
+    if (p.da <= 32) return launch_chunks<T, 32, W>(p, s, k, between, stream);
+    if (p.da <= 64) return launch_chunks<T, 64, W>(p, s, k, between, stream);
+    return launch_chunks<T, 128, W>(p, s, k, between, stream);
   };
   return p.dc <= 64 ? go(std::integral_constant<int, 4>{}) : go(std::integral_constant<int, 8>{});
+}
+
+int64_t longest_of(std::initializer_list<int64_t> strides) {
+  int64_t most = 0;
+  for (int64_t s : strides) most = s > most ? s : most;
+  return most;
 }
 
 template <typename T>
@@ -1109,8 +1160,10 @@ hipError_t launch_attention(const logmel_attention_input& in, void* o, int64_t o
   p.state_out = state_out;
   p.beta = in.scale;
   p.gamma = 1.0f;
-  return launch_job(p, in, static_cast<float*>(ws), state_out && state_out == in.d_state, cus,
-                    stream);
+  const AttnSplit s = split_of(
+      in, p.dc, longest_of({in.q_stride, in.k_stride, in.v_stride, o_stride}), cus);
+  const PartSpace space(s, in, state_out && state_out == in.d_state);
+  return launch_job(p, s, space, static_cast<float*>(ws), true, stream);
 }
 
 template <typename T>
@@ -1123,6 +1176,12 @@ hipError_t launch_attention_backward(const logmel_attention_input& in,
   const T* v = static_cast<const T*>(in.d_v);
   const T* d = static_cast<const T*>(g.d_do);
   const int dk = (int)in.head_dk, dv = (int)in.head_dv;
+  const AttnSplit s =
+      split_of(in, dk > dv ? dk : dv,
+               longest_of({in.q_stride, in.k_stride, in.v_stride, g.do_stride, g.dq_stride,
+                           g.dk_stride, g.dv_stride, share > 1 ? in.heads * dk : 0}),
+               cus);
+  const PartSpace space(s, in, false);
   // the shared heads' parts first, then the splits'
   float* part = share > 1 ? static_cast<float*>(ws) : nullptr;
   float* between = static_cast<float*>(ws) + (part ? in.rows * in.heads * dk : 0);
@@ -1131,7 +1190,7 @@ hipError_t launch_attention_backward(const logmel_attention_input& in,
     p.o = static_cast<T*>(out);
     p.of = part;
     p.os = part ? in.heads * dk : stride;
-    hipError_t e = launch_job(p, in, between, false, cus, stream);
+    hipError_t e = launch_job(p, s, space, between, true, stream);
     if (e != hipSuccess || !part) return e;
     const int64_t n = in.rows * in.qk_heads * dk;
     const int64_t blocks = (n + 255) / 256;
@@ -1171,7 +1230,7 @@ hipError_t launch_attention_backward(const logmel_attention_input& in,
   p.of = nullptr;
   p.o = static_cast<T*>(g.d_dv);
   p.os = g.dv_stride;
-  return launch_job(p, in, between, false, cus, stream);
+  return launch_job(p, s, space, between, false, stream);   // its states are those of dk
 }
 
 }  // namespace
@@ -1180,12 +1239,11 @@ hipError_t launch_attention_backward(const logmel_attention_input& in,
 int64_t logmel_attention_workspace(const logmel_attention_input& in, int backward, int cus) {
   using namespace logmel;
   if (!in.n_seq) return 0;
-  const int dk = (int)in.head_dk, dv = (int)in.head_dv;
-  const AttnSplit s = split_of(in, dk, dv, 0, cus);   // forward, and dv
-  if (!backward) return (between_of(s, in) + (in.d_state ? kept_of(s, in) : 0)) * 4;
-  const AttnSplit t = split_of(in, dv, dk, 0, cus);   // dq and dk
-  const int64_t a = between_of(s, in), b = between_of(t, in);
-  return ((in.heads > in.qk_heads ? in.rows * in.heads * in.head_dk : 0) + (a > b ? a : b)) * 4;
+  const int64_t dk = in.head_dk, dv = in.head_dv;
+  const AttnSplit s = split_of(in, backward && dk > dv ? dk : dv, 0, cus);
+  const int64_t share =
+      backward && in.heads > in.qk_heads ? in.rows * in.heads * in.head_dk : 0;
+  return (share + PartSpace(s, in, !backward && in.d_state).all()) * 4;
 }
 
 hipError_t logmel_launch_attention(const logmel_attention_input& in, void* o, int64_t o_stride,
