@@ -234,15 +234,15 @@ template <typename T>
 struct Pieces;
 template <>
 struct Pieces<bf16_t> {
-  static constexpr int kIn = 1, kMid = 2, kState = 3, kChunk = 64;
+  static constexpr int kIn = 1, kMid = 2, kState = 3;
 };
 template <>
 struct Pieces<f16_t> {
-  static constexpr int kIn = 2, kMid = 2, kState = 3, kChunk = 32;
+  static constexpr int kIn = 2, kMid = 2, kState = 3;
 };
 template <>
 struct Pieces<float> {
-  static constexpr int kIn = 3, kMid = 3, kState = 3, kChunk = 32;
+  static constexpr int kIn = 3, kMid = 3, kState = 3;
 };
 
 using bf16x2 = __attribute__((ext_vector_type(2))) __bf16;
@@ -347,16 +347,21 @@ struct Tile {
   static constexpr int kIts = (kBlocks + kThreads - 1) / kThreads;
   using Word = std::conditional_t<sizeof(T) == 2, u32x2, u32x4>;
   // Where this lane's blocks lie: in memory from the tile's lowest row on (from
-  // its first row upwards, from its last row downwards), and in LDS.
+  // its first row upwards, from its last row downwards), and in LDS. 2-byte values
+  // are read in blocks that do not pass the row's end (a word that does would be 0
+  // at the buffer's), so that the last ones are shifted back.
+  static constexpr bool back_from_end() { return sizeof(T) == 2; }
   struct Places {
     uint32_t from[kIts], row[kIts], col[kIts];
-    __device__ __forceinline__ Places(uint32_t pitch, bool up, bool rows_placed, bool cols_placed) {
+    __device__ __forceinline__ Places(uint32_t pitch, bool up, int width, bool rows_placed,
+                                      bool cols_placed) {
 #pragma unroll
       for (int it = 0; it < kIts; ++it) {
         int rb, cb;
         at(threadIdx.x, it, rb, cb);
         const uint32_t down = (uint32_t)(4 * rb) * pitch;
-        from[it] = (up ? down : 0u - down) + (uint32_t)(4 * cb) * (uint32_t)sizeof(T);
+        const int c = back_from_end() && 4 * cb > width - 4 ? width - 4 : 4 * cb;
+        from[it] = (up ? down : 0u - down) + (uint32_t)c * (uint32_t)sizeof(T);
         row[it] = half_at<kWidth / 8, false>(rows_placed ? place(rb) : 4 * rb, cb);
         col[it] = half_at<kRows / 8, true>(cols_placed ? place(cb) : 4 * cb, rb);
       }
@@ -364,8 +369,6 @@ struct Tile {
   };
 
   Word v[kIts][4];
-  T tail;   // the last value in memory of rows of an odd number of 2-byte values: half of a
-            // word that ends behind the buffer
 
   // For a wavefront as a whole: blocks come in 64s.
   static __device__ __forceinline__ bool on(int it) {
@@ -383,16 +386,13 @@ struct Tile {
   }
 
   // base: the tile's lowest row; up: whether that is its first; held: the rows
-  // there are. Rows from held on lie behind the buffer (or, their offsets being
-  // negative, far behind it) and are 0; `settle` sees to the channels.
+  // there are, which may be none. Rows from held on lie behind the buffer (or,
+  // their offsets being negative, far behind it) and are 0; `settle` sees to the
+  // channels.
   __device__ __forceinline__ void load(const Places& k, const T* base, uint32_t pitch, bool up,
                                        int held, int width) {
-    const auto buffer =
-        buffer_of(base, (uint32_t)(held - 1) * pitch + (uint32_t)width * (uint32_t)sizeof(T));
-    if constexpr (sizeof(T) == 2)
-      if (width & 1)
-        tail = *reinterpret_cast<const T*>(reinterpret_cast<const char*>(base + width - 1) +
-                                           (uint32_t)(held - 1) * pitch);
+    const auto buffer = buffer_of(
+        base, held > 0 ? (uint32_t)(held - 1) * pitch + (uint32_t)width * (uint32_t)sizeof(T) : 0u);
     const uint32_t step = up ? pitch : 0u - pitch;
     const uint32_t first = up ? 0u : (uint32_t)(held - 1) * pitch;
 #pragma unroll
@@ -412,29 +412,29 @@ struct Tile {
     }
   }
 
-  // 0 in channels from width on, which were read from what lies there; and the
-  // tail.
-  __device__ __forceinline__ void settle(bool up, int held, int width) {
+  // 0 in channels from width on, in whose place stands what lies there, and the
+  // last ones where they belong.
+  __device__ __forceinline__ void settle(int width) {
     const int tid = fresh(threadIdx.x);
 #pragma unroll
     for (int it = 0; it < kIts; ++it) {
       int rb, cb;
       at(tid, it, rb, cb);
       const int left = width - 4 * cb;
-      Word keep;
       if constexpr (sizeof(T) == 2) {
-        keep[0] = left >= 2 ? ~0u : left == 1 ? 0xffffu : 0u;
-        keep[1] = left >= 4 ? ~0u : left == 3 ? 0xffffu : 0u;
+        const int by = left >= 4 ? 0 : left > 0 ? 16 * (4 - left) : 0;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint64_t x = left > 0 ? __builtin_bit_cast(uint64_t, v[it][r]) >> by : 0;
+          v[it][r] = __builtin_bit_cast(Word, x);
+        }
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) keep[j] = left > j ? ~0u : 0u;
-      }
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t keep = left > j ? ~0u : 0u;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        v[it][r] &= keep;
-        if constexpr (sizeof(T) == 2)
-          if ((width & 1) && 4 * rb + r == (up ? held - 1 : 0) && (left == 1 || left == 3))
-            v[it][r][left / 2] = __builtin_bit_cast(uint16_t, tail);
+          for (int r = 0; r < 4; ++r) v[it][r][j] &= keep;
+        }
       }
     }
   }
@@ -566,9 +566,18 @@ __device__ __forceinline__ int64_t across(const AttnJob<T>& p, int64_t row) {
   return i > 0 && i <= p.n_seq && p.off[i] > row ? i - 1 : -1;
 }
 
-template <typename T, int DA, int kWide>
+// Rows of a chunk: its barriers and the trips to LDS between them take as long
+// for 32 rows as for 64, so 64 wherever two workgroups of four wavefronts (one of
+// eight) fit the LDS.
+template <typename T, int DA, int kWaves>
+constexpr int kChunk = Pieces<T>::kIn == 1 || DA == 32 ||
+                               (Pieces<T>::kIn == 2 && (DA == 64 || kWaves == 8))
+                           ? 64
+                           : 32;
+
+template <typename T, int DA, int kWide, int C>
 struct ChunkLds {
-  static constexpr int C = Pieces<T>::kChunk, kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid;
+  static constexpr int kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid;
   static constexpr int kScores = C == 64 ? 6 : 2;
   uint16_t a[kIn][C * DA];
   uint16_t b[kIn][C * DA];       // rows as `place` has them
@@ -583,8 +592,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
                                                                            Walk walk) {
   constexpr int kThreads = 64 * kWaves, kWide = 16 * kWaves;
   constexpr int kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid, kState = Pieces<T>::kState;
-  constexpr int C = Pieces<T>::kChunk, kI = C / 16, kT = C / 32, kS = DA / 32, kU = DA / 16;
-  __shared__ __attribute__((aligned(16))) ChunkLds<T, DA, kWide> lds;
+  constexpr int kAhead = 1;
+  constexpr int C = kChunk<T, DA, kWaves>, kI = C / 16, kT = C / 32, kS = DA / 32, kU = DA / 16;
+  __shared__ __attribute__((aligned(16))) ChunkLds<T, DA, kWide, C> lds;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int step = p.back ? -1 : 1;
@@ -594,9 +604,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
   using TileA = Tile<T, C, DA, kThreads, 0>;
   using TileB = Tile<T, C, DA, kThreads, TileA::kBlocks % kThreads>;
   using TileC = Tile<T, C, kWide, kThreads, 2 * TileA::kBlocks % kThreads>;
-  const typename TileA::Places la(sa, !p.back, false, false);
-  const typename TileB::Places lb(sb, !p.back, true, true);
-  const typename TileC::Places lc(sc, !p.back, false, false);
   for (int64_t item = blockIdx.x; item < walk.items; item += gridDim.x) {
     const int slab = (int)(item % walk.slabs);
     const int h = (int)(item / walk.slabs % p.heads);
@@ -607,6 +614,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
     const T* pc = p.c + (int64_t)(h / p.share_c) * p.dc + c0;
     const int wc = p.dc - c0;
     const bool works = 16 * wave < wc;   // has columns of the state
+    const int wide = wc < kWide ? wc : kWide;
+    const typename TileA::Places la(sa, !p.back, p.da, false, false);
+    const typename TileB::Places lb(sb, !p.back, p.da, true, true);
+    const typename TileC::Places lc(sc, !p.back, wide, false, false);
     const float decay = p.log_decay[h];
     const float log2 = decay * 1.44269504088896340736f;
     auto power = [&](int i) { return i > 0 ? __builtin_amdgcn_exp2f(log2 * (float)i) : 1.0f; };
@@ -687,42 +698,52 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
     auto segment = [&](int64_t lo, int64_t hi, bool last) __attribute__((always_inline)) {
       const int64_t rows = hi - lo;
       const int64_t first = p.back ? hi - 1 : lo;
-      TileA ta;
-      TileB tb;
-      TileC tc;
-      const int wide = wc < kWide ? wc : kWide;
-      auto load = [&](int64_t at, int held) __attribute__((always_inline)) {
-        const int64_t row = p.back ? first - at - held + 1 : first + at;   // the lowest
-        if constexpr (kOut) ta.load(la, pa + row * p.as, sa, !p.back, held, p.da);
-        tb.load(lb, pb + row * p.bs, sb, !p.back, held, p.da);
-        tc.load(lc, pc + row * p.cs, sc, !p.back, held, wide);
+      // Chunks on their way: as many as there are registers for.
+      struct Ahead {
+        TileA a;
+        TileB b;
+        TileC c;
+        int64_t at;   // the chunk's first row
+      } ahead[kAhead];
+      auto held_at = [&](int64_t at) { return (int)(rows - at < C ? rows - at : C); };   // may be < 0
+      // The number of memory instructions in flight is the same on every usual way
+      // through the loop, so that a wait leaves the ones behind it alone; the rare
+      // ways end with a wait for all.
+      auto wait_all = [] { __builtin_amdgcn_s_waitcnt(0x0f70); };
+      auto load = [&](Ahead& x, int64_t at, int held) __attribute__((always_inline)) {
+        const int64_t row = held <= 0 ? first : p.back ? first - at - held + 1 : first + at;
+        if constexpr (kOut) x.a.load(la, pa + row * p.as, sa, !p.back, held, p.da);
+        x.b.load(lb, pb + row * p.bs, sb, !p.back, held, p.da);
+        x.c.load(lc, pc + row * p.cs, sc, !p.back, held, wide);
+        x.at = at;
       };
-      auto settle = [&](int held) __attribute__((always_inline)) {
+      auto stage = [&](Ahead& x) __attribute__((always_inline)) {
         if (p.da < DA) {
-          if constexpr (kOut) ta.settle(!p.back, held, p.da);
-          tb.settle(!p.back, held, p.da);
+          if constexpr (kOut) x.a.settle(p.da);
+          x.b.settle(p.da);
         }
-        if (wide < kWide) tc.settle(!p.back, held, wide);
-      };
-      auto stage = [&]() __attribute__((always_inline)) {
+        if (wide < kWide) x.c.settle(wide);
         if constexpr (kOut) {
-          ta.store(la, lds.a[0], nullptr);
-          tb.store(lb, lds.b[0], lds.bt[0]);
+          x.a.store(la, lds.a[0], nullptr);
+          x.b.store(lb, lds.b[0], lds.bt[0]);
         } else {
-          tb.store(lb, nullptr, lds.bt[0]);
+          x.b.store(lb, nullptr, lds.bt[0]);
         }
-        tc.store(lc, nullptr, lds.ct[0]);
+        x.c.store(lc, nullptr, lds.ct[0]);
       };
-      auto held_at = [&](int64_t at) { return (int)(rows - at < C ? rows - at : C); };
-      load(0, held_at(0));
-      for (int64_t at = 0; at < rows;) {
+      // The chunk at row `at`, whose values are (or are brought) in x; returns
+      // where the next one starts.
+      auto chunk = [&](Ahead& x, int64_t at) __attribute__((always_inline)) {
         int held = held_at(at);
+        if (kAhead > 1 && x.at != at) {   // a chunk before was cut short
+          load(x, at, held);
+          wait_all();
+        }
         for (bool cut_short = false;;) {
-          settle(held);
-          stage();
+          stage(x);
           if constexpr (!kOut) break;
-          if (!cut_short && __any(tb.any_bad() || tc.any_bad())) {
-            const int b1 = tb.first_bad(), b2 = tc.first_bad();
+          if (!cut_short && __any(x.b.any_bad() || x.c.any_bad())) {
+            const int b1 = x.b.first_bad(), b2 = x.c.first_bad();
             const int bad = b1 < b2 ? b1 : b2;
             if (bad < C) atomicMin(&lds.bad, bad);
           }
@@ -731,13 +752,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
           if (cut_short || bad == C) break;   // for the whole workgroup
           cut_short = true;
           held = bad > 0 ? bad : 1;
-          load(at, held);
+          load(x, at, held);
+          wait_all();
           __syncthreads();
           if (tid == 0) lds.bad = C;
         }
         if constexpr (!kOut) __syncthreads();
-        const int64_t next = at + held;
-        if (next < rows) load(next, held_at(next));
+        const int64_t next = at + held, then = next + (kAhead - 1) * C;
+        load(x, then, held_at(then));   // none behind the last
 
         if constexpr (kOut) {
           // the scores, transposed: block (t, half) of 16 rows of b by rows 16 bi of a
@@ -844,7 +866,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
         // be written (its scores after a barrier more)
         __syncthreads();
 
-        if constexpr (kOut) if (works) {
+        if constexpr (kOut) {
           // rows i of the output: four channels of a row per lane
           const int64_t row = p.back ? first - at - held + 1 : first + at;   // the lowest
           const int64_t to = row * p.os + (int64_t)h * p.dc + c0;
@@ -852,29 +874,48 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
           const auto buffer =
               buffer_of(p.of ? static_cast<const void*>(p.of + to) : p.o + to,
                         (uint32_t)(held - 1) * pitch + (uint32_t)(wc < kWide ? wc : kWide) * size);
+          constexpr uint32_t kNowhere = 0u - 16u;   // behind any buffer
           const int c = 16 * wave + 4 * g;
           const uint32_t side = (uint32_t)c * size;
           auto at_row = [&](int i) __attribute__((always_inline)) {
             const int r = 16 * i + n;
             return (uint32_t)(p.back ? held - 1 - r : r) * pitch + side;
           };
+          if (works) {
 #pragma unroll
-          for (int i = 0; i < kI; ++i) {
+            for (int i = 0; i < kI; ++i) {
 #pragma unroll
-            for (int t = 0; t <= i / 2; ++t) {
-              bf16x8 fp[kMid];
-              const int f = i < 2 ? i : 2 * i - 2 + t;
+              for (int t = 0; t <= i / 2; ++t) {
+                bf16x8 fp[kMid];
+                const int f = i < 2 ? i : 2 * i - 2 + t;
 #pragma unroll
-              for (int k = 0; k < kMid; ++k) fp[k] = frag(&lds.p[k][f][lane][0]);
-              mma(o[i], fc[t], fp);
+                for (int k = 0; k < kMid; ++k) fp[k] = frag(&lds.p[k][f][lane][0]);
+                mma(o[i], fc[t], fp);
+              }
             }
           }
-          if (wc < kWide) {   // value by value, those that there are
+          // four channels at a time where there are four, else behind the buffer
+          const bool quad = c + 4 <= wc;   // (not in a wavefront without columns)
+#pragma unroll
+          for (int i = 0; i < kI; ++i) {
+            const uint32_t to = quad ? at_row(i) : kNowhere;
+            if (p.of || sizeof(T) == 4) {
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[i]), buffer, to,
+                                                     0, 0);
+            } else if constexpr (sizeof(T) == 2) {
+              Packed<T, 4> y;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y.v[j] = (T)o[i][j];
+              __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), buffer, to, 0, 0);
+            }
+          }
+          if ((wc & 3) && 16 * wave + 16 > wc) {   // up to three at the end of the columns
 #pragma unroll
             for (int i = 0; i < kI; ++i)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t to = c + j < wc && 16 * i + n < held ? at_row(i) + j * size : ~0u - 3u;
+              for (int j = 0; j < 3; ++j) {
+                const bool on = !quad && c + j < wc && 16 * i + n < held;
+                const uint32_t to = on ? at_row(i) + j * size : kNowhere;
                 const float y = o[i][j];
                 if (p.of || sizeof(T) == 4)
                   __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, y), buffer,
@@ -883,23 +924,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
                   __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)y),
                                                         buffer, to, 0, 0);
               }
-          } else if (p.of || sizeof(T) == 4) {
-#pragma unroll
-            for (int i = 0; i < kI; ++i)
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[i]), buffer,
-                                                     at_row(i), 0, 0);
-          } else if constexpr (sizeof(T) == 2) {
-#pragma unroll
-            for (int i = 0; i < kI; ++i) {
-              Packed<T, 4> y;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) y.v[j] = (T)o[i][j];
-              __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), buffer,
-                                                    at_row(i), 0, 0);
-            }
           }
         }
-        at = next;
+        return next;
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) load(ahead[i], i * C, held_at(i * C));
+      for (int64_t at = 0; at < rows;) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (at < rows) at = chunk(ahead[i], at);
       }
     };
 
@@ -1031,11 +1065,12 @@ AttnSplit split_of(const logmel_attention_input& in, int64_t dc, int64_t widest,
   const int64_t longest =
       in.max_frames && in.max_frames < in.rows ? in.max_frames : in.rows;
   // a chunk's rows are addressed by 32 bits from its lowest one
-  if (longest <= kShort || widest >= (int64_t)1 << 22) {
+  // in blocks of four values
+  if (longest <= kShort || widest >= (int64_t)1 << 22 || in.head_dk < 4 || in.head_dv < 4) {
     s.how = AttnSplit::kRows;
     return s;
   }
-  const int64_t chunk = in.type == LOGMEL_BF16 ? 64 : 32;
+  const int64_t chunk = in.type == LOGMEL_F32 ? 32 : 64;
   const int64_t lanes = in.heads;                          // workgroups side by side
   const int64_t slots = 2 * (int64_t)cus;                  // (of eight wavefronts half as many
                                                            // are resident, which take turns)
