@@ -278,8 +278,9 @@ __device__ __forceinline__ void cut(float (&x)[M], uint32_t (&piece)[N][M / 2]) 
 __device__ __forceinline__ bf16x8 frag(const uint32_t (&w)[4]) {
   return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
 }
-__device__ __forceinline__ bf16x8 frag(const uint16_t* p) {
-  return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p));
+__device__ __forceinline__ bf16x8 frag(const uint16_t* tile, uint32_t at) {
+  return __builtin_bit_cast(
+      bf16x8, *reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(tile) + at));
 }
 
 // acc += sum over the pairs of pieces whose places sum to less than the count.
@@ -315,6 +316,14 @@ __device__ __forceinline__ int unit_at(int r, int u) {
   }
 }
 
+// The same in bytes for unit u + 4 s of row r + 16 i, r below 16 and u below 4,
+// from that of r and u.
+template <int kUnits, bool kAcross>
+__device__ __forceinline__ uint32_t operand_at(uint32_t at, int i, int s) {
+  const uint32_t turn = kUnits >= 8 && kAcross ? (2 * i) & 7 : 4 * (i & 1);
+  return (at ^ (16 * (turn ^ (uint32_t)(4 * s)))) + (uint32_t)i * (kUnits * 256);
+}
+
 // The same in bytes for the first of four rows r0 .. r0 + 3 (r0 a multiple of 4)
 // and half a unit, and from there for the others: the places differ by bits of
 // the row alone.
@@ -338,8 +347,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint3
 // to LDS, in blocks of 4 x 4 values: eight blocks side by side and eight below
 // each other per wavefront, so that memory is read 64 or 128 bytes at a time and
 // LDS is written, along rows and along columns, without bank conflicts.
-// kFirst: the thread that takes its first block, so that several tiles that do
-// not fill the workgroup are spread over it.
+// kThreads: those that bring it, a number that divides the workgroup's; kFirst:
+// the one that takes the first block, so that several tiles that do not fill them
+// are spread over them.
 template <typename T, int kRows, int kWidth, int kThreads, int kFirst>
 struct Tile {
   static constexpr int kIn = Pieces<T>::kIn;
@@ -375,11 +385,11 @@ struct Tile {
     static_assert(kBlocks % 64 == 0);
     if (kBlocks % kThreads == 0) return true;
     const int first = __builtin_amdgcn_readfirstlane(
-        ((int)threadIdx.x + kThreads - kFirst) % kThreads & ~63);
+        ((int)threadIdx.x % kThreads + kThreads - kFirst) % kThreads & ~63);
     return first + kThreads * it < kBlocks;
   }
   static __device__ __forceinline__ void at(int tid, int it, int& rb, int& cb) {
-    const int i = (tid + kThreads - kFirst) % kThreads + kThreads * it, rest = i >> 6;
+    const int i = (tid % kThreads + kThreads - kFirst) % kThreads + kThreads * it, rest = i >> 6;
     constexpr int kWide = kWidth / 32;
     cb = (i & 7) + 8 * (rest % kWide);
     rb = ((i >> 3) & 7) + 8 * (rest / kWide);
@@ -543,7 +553,6 @@ struct Walk {
   float* kept;
   int* through;   // of each such place: 0 no sequence lies across it, 1 one does, 2 the one that
                   // lies across the place before (behind it, backwards) too
-  int slabs;
   int64_t items;
 };
 
@@ -566,15 +575,6 @@ __device__ __forceinline__ int64_t across(const AttnJob<T>& p, int64_t row) {
   return i > 0 && i <= p.n_seq && p.off[i] > row ? i - 1 : -1;
 }
 
-// Rows of a chunk: its barriers and the trips to LDS between them take as long
-// for 32 rows as for 64, so 64 wherever two workgroups of four wavefronts (one of
-// eight) fit the LDS.
-template <typename T, int DA, int kWaves>
-constexpr int kChunk = Pieces<T>::kIn == 1 || DA == 32 ||
-                               (Pieces<T>::kIn == 2 && (DA == 64 || kWaves == 8))
-                           ? 64
-                           : 32;
-
 template <typename T, int DA, int kWide, int C>
 struct ChunkLds {
   static constexpr int kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid;
@@ -584,185 +584,190 @@ struct ChunkLds {
   uint16_t bt[kIn][DA * C];      // columns as `place` has them
   uint16_t ct[kIn][kWide * C];
   uint16_t p[kMid][kScores][64][8];
+  float from_state[kWide / 16][C / 16][64][4];
+  float weight[kWide / 16][C];   // of a chunk's rows as they enter the state, a copy per wavefront
   int bad;
 };
 
+// Rows of a chunk: 64 where a compute unit's LDS holds 16 wavefronts' tiles so
+// (two workgroups of four columns' wavefronts, one of eight), else 32.
+template <typename T, int DA, int kWaves>
+constexpr int kChunk =
+    sizeof(ChunkLds<T, DA, 16 * kWaves, 64>) <= (kWaves == 4 ? 80 : 160) * 1024 ? 64 : 32;
+
+// A workgroup is kWaves wavefronts that see to the scores and kWaves that hold
+// the state, 16 columns of it each; a wavefront alone waits for half of its time,
+// for LDS and for the other wavefronts. Of a chunk
+//   the first bring a and b, form the scores, and join them with c and with what
+//   comes from the state to the output's rows;
+//   the second bring c, multiply the state with a, and take b and c into it.
+// Two barriers: the tiles are written; the scores and the state's part are
+// written and the tiles read.
 template <typename T, int DA, int kWaves, bool kOut>
-__global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJob<T> p,
-                                                                           Walk walk) {
-  constexpr int kThreads = 64 * kWaves, kWide = 16 * kWaves;
+__global__ __launch_bounds__(128 * kWaves, 4) void logmel_attn_chunk_kernel(AttnJob<T> p,
+                                                                            Walk walk) {
+  constexpr int kThreads = 64 * kWaves, kWide = 16 * kWaves;   // of each half
   constexpr int kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid, kState = Pieces<T>::kState;
-  constexpr int kAhead = 1;
   constexpr int C = kChunk<T, DA, kWaves>, kI = C / 16, kT = C / 32, kS = DA / 32, kU = DA / 16;
-  __shared__ __attribute__((aligned(16))) ChunkLds<T, DA, kWide, C> lds;
-  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int step = p.back ? -1 : 1;
-  if (tid == 0) lds.bad = C;
-  const uint32_t sa = (uint32_t)(p.as * sizeof(T)), sb = (uint32_t)(p.bs * sizeof(T)),
-                 sc = (uint32_t)(p.cs * sizeof(T));
   using TileA = Tile<T, C, DA, kThreads, 0>;
   using TileB = Tile<T, C, DA, kThreads, TileA::kBlocks % kThreads>;
-  using TileC = Tile<T, C, kWide, kThreads, 2 * TileA::kBlocks % kThreads>;
+  using TileC = Tile<T, C, kWide, kThreads, 0>;
+  __shared__ __attribute__((aligned(16))) ChunkLds<T, DA, kWide, C> lds;
+  const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % kWaves;
+  const bool of_scores = __builtin_amdgcn_readfirstlane(tid >> 6) < kWaves;
+  const int64_t cells = (int64_t)p.da * p.dc;
+  if (tid == 0) lds.bad = C;
+
+  // A lane's operand: unit 4 s + g of row 16 i + n of a tile of rows, or of columns
+  const uint32_t row_base = 16 * unit_at<DA / 8, false>(n, g);
+  const uint32_t col_base = 16 * unit_at<C / 8, true>(n, g);
+  // The memory instructions in flight are as many on every usual way through a
+  // loop, so that a wait leaves the ones behind it alone; the rare way ends with a
+  // wait for all.
+  auto wait_all = [] { __builtin_amdgcn_s_waitcnt(0x0f70); };
+
+  // Rows [lo, hi) of one sequence, chunk by chunk: both halves of the workgroup
+  // go through this, each with its own parts. bring(row, held): the chunk whose
+  // lowest row is `row` on its way (held rows; none: nothing); put(): into LDS;
+  // bad(): the first row brought with a value that is not finite, or C; work(row,
+  // held, end): between the barriers; after(row, held): behind them.
+  auto chunks = [&](int64_t lo, int64_t hi, auto bring, auto put, auto bad, auto work,
+                    auto after) __attribute__((always_inline)) {
+    const int64_t rows = hi - lo;
+    auto lowest = [&](int64_t at, int held) {
+      return held <= 0 ? lo : p.back ? hi - at - held : lo + at;
+    };
+    auto held_at = [&](int64_t at) {   // not above 0 behind the last
+      return (int)(rows - at < C ? rows - at : C);
+    };
+    bring(lowest(0, held_at(0)), held_at(0));
+    for (int64_t at = 0; at < rows;) {
+      int held = held_at(at);
+      for (bool cut_short = false;;) {
+        put();
+        if constexpr (kOut)
+          if (!cut_short) {
+            const int first = bad();
+            if (first < C) atomicMin(&lds.bad, first);
+          }
+        __syncthreads();
+        if constexpr (!kOut) break;
+        const int first = lds.bad;
+        if (cut_short || first == C) break;   // for the whole workgroup
+        cut_short = true;
+        held = first > 0 ? first : 1;
+        bring(lowest(at, held), held);
+        wait_all();
+        __syncthreads();
+        if (tid == 0) lds.bad = C;
+      }
+      const int64_t next = at + held;
+      const int64_t row = lowest(at, held);
+      bring(lowest(next, held_at(next)), held_at(next));
+      work(held, next == rows);
+      __syncthreads();
+      after(row, held);
+      at = next;
+    }
+  };
+
   for (int64_t item = blockIdx.x; item < walk.items; item += gridDim.x) {
-    const int slab = (int)(item % walk.slabs);
-    const int h = (int)(item / walk.slabs % p.heads);
-    const int64_t which = item / walk.slabs / p.heads;   // sequence or part
-    const int c0 = slab * kWide;
-    const T* pa = p.a + (int64_t)(h / p.share_a) * p.da;
-    const T* pb = p.b + (int64_t)(h / p.share_b) * p.da;
-    const T* pc = p.c + (int64_t)(h / p.share_c) * p.dc + c0;
-    const int wc = p.dc - c0;
-    const bool works = 16 * wave < wc;   // has columns of the state
-    const int wide = wc < kWide ? wc : kWide;
-    const typename TileA::Places la(sa, !p.back, p.da, false, false);
-    const typename TileB::Places lb(sb, !p.back, p.da, true, true);
-    const typename TileC::Places lc(sc, !p.back, wide, false, false);
+    const int h = (int)(item % p.heads);
+    const int64_t which = item / p.heads;   // sequence or part
     const float decay = p.log_decay[h];
     const float log2 = decay * 1.44269504088896340736f;
     auto power = [&](int i) { return i > 0 ? __builtin_amdgcn_exp2f(log2 * (float)i) : 1.0f; };
-    const int64_t cells = (int64_t)p.da * p.dc;
+    const int wide = p.dc;               // columns of c and of the output
+    const bool works = 16 * wave < wide;   // has some of them
 
-    // weights of this lane's scores: block (rows 16 bi, columns 32 t and b)
-    // of eight wavefronts the first four take the blocks on the diagonal
-    constexpr int kMine = C == 64 ? 3 : 1;
-    const int half = wave & 1, pair = (wave >> 1) & 1;
-    auto mine = [&](int m) { return kWaves == 4 || (m == 1) == (wave >= 4); };
-    float ws[kMine][4], enter[kI];
-    uint32_t seen[2][4];   // all bits where row j of b is at or before row i of a
-                           // (the blocks on the diagonal: the first and the third)
-    if constexpr (kOut) {
+    // f(sequence, from, to, starts, ends): the sequences of this workgroup's rows,
+    // in order: its own, or those of its part from the one that enters it on.
+    const int64_t r0 = which * walk.part_rows;
+    const int64_t r1 = walk.parts == 0 || r0 + walk.part_rows > p.rows ? p.rows
+                                                                       : r0 + walk.part_rows;
+    auto within = [&](int64_t r) { return r < r0 ? r0 : r > r1 ? r1 : r; };
+    auto each = [&](auto f) __attribute__((always_inline)) {
+      if constexpr (!kOut) {
+        // the one across the part's end (its start, backwards), whose state leaves it
+        const int64_t i = across(p, p.back ? r0 : r1), place = p.back ? which - 1 : which;
+        if (place < 0 || place >= walk.parts - 1) return;
+        const int64_t from = i < 0 ? 0 : p.off[i], to = i < 0 ? 0 : p.off[i + 1];
+        const bool starts = from >= r0, ends = to <= r1;
+        if (tid == 0 && h == 0) walk.through[place] = i < 0 ? 0 : (p.back ? ends : starts) ? 1 : 2;
+        if (i >= 0) f(i, within(from), within(to), starts, ends);
+      } else {
+        int64_t i = which;
+        bool enters = false;
+        if (walk.parts) {
+          i = first_from(p, r0);
+          enters = which > 0 && i > 0 && i <= p.n_seq && p.off[i] > r0;
+          i -= enters;
+        }
+        const bool end = walk.parts == 0 || which == walk.parts - 1;
+        do {
+          if (i >= p.n_seq || !(enters || end || p.off[i] < r1)) break;
+          const int64_t lo = enters ? r0 : within(p.off[i]);
+          f(i, lo, within(p.off[i + 1]), !enters, end || p.off[i + 1] <= r1);
+          enters = false;
+          ++i;
+        } while (walk.parts);
+      }
+    };
+
+    if (of_scores) {
+      const T* pa = p.a + (int64_t)(h / p.share_a) * p.da;
+      const T* pb = p.b + (int64_t)(h / p.share_b) * p.da;
+      const uint32_t sa = (uint32_t)(p.as * sizeof(T)), sb = (uint32_t)(p.bs * sizeof(T));
+      const typename TileA::Places la(sa, !p.back, p.da, false, false);
+      const typename TileB::Places lb(sb, !p.back, p.da, true, true);
+      // this lane's weights of the scores: block (rows 16 bi, columns 32 t and half);
+      // of eight wavefronts the first four take the blocks on the diagonal
+      constexpr int kMine = C == 64 ? 3 : 1;
+      const int half = wave & 1, pair = (wave >> 1) & 1;
+      auto mine = [&](int m) { return kWaves == 4 || (m == 1) == (wave >= 4); };
+      float ws[kMine][4];
+      // where row j of b is at or before row i of a in the blocks on the diagonal (the
+      // first and the third): from this register on
+      const int after = 8 * g + 4 * half - (16 * pair + n);
+      if constexpr (kOut) {
 #pragma unroll
-      for (int m = 0; m < kMine; ++m) {
-        const int bi = m ? 2 + pair : pair, t = m == 2;
+        for (int m = 0; m < kMine; ++m) {
+          const int bi = m ? 2 + pair : pair, t = m == 2;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int age = 16 * bi + n - (32 * t + 8 * g + 4 * half + r);
-          ws[m][r] = p.beta * p.gamma * power(age);
-          if (m != 1) seen[m / 2][r] = age >= 0 ? ~0u : 0u;
+          for (int r = 0; r < 4; ++r) {
+            const int age = 16 * bi + n - (32 * t + 8 * g + 4 * half + r);
+            ws[m][r] = p.beta * p.gamma * power(age);
+          }
         }
       }
-#pragma unroll
-      for (int i = 0; i < kI; ++i) enter[i] = p.beta * power(16 * i + n);
-    }
-    // of the rows that enter the state, `left` rows before the next chunk's first
-    float wc_[kT][8];
-    Decay whole;
-    int left = -1;
-    auto weigh = [&](int to) __attribute__((always_inline)) {
-      if (to == left) return;
-      left = to;
-      whole = decay_of(decay, (float)to);
-#pragma unroll
-      for (int t = 0; t < kT; ++t)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int j = 32 * t + 8 * g + e;
-          wc_[t][e] = j <= to ? p.gamma * power(to - j) : 0.0f;
-        }
-    };
+      TileA ta;
+      TileB tb;
+      bf16x8 fc[kT][kIn];
 
-    auto row_frag = [&](const uint16_t* tile, int r, int u) __attribute__((always_inline)) {
-      return frag(tile + 8 * unit_at<DA / 8, false>(r, u));
-    };
-    auto col_frag = [&](const uint16_t* tile, int r, int u) __attribute__((always_inline)) {
-      return frag(tile + 8 * unit_at<C / 8, true>(r, u));
-    };
-
-    f32x4 w[kU];
-    // f(u, r, cell of the state) for this lane's values w[u][r] that are cells
-    auto cells_of = [&](auto f) __attribute__((always_inline)) {
-      const int c = fresh(c0 + 16 * wave + n), a0 = fresh(8 * g);
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int a = a0 + 32 * (u >> 1) + 4 * (u & 1) + r;
-          if (a < p.da && c < p.dc) f(u, r, p.transposed ? c * p.da + a : a * p.dc + c);
-        }
-    };
-    auto load_state = [&](const float* s, Decay d) __attribute__((always_inline)) {
-#pragma unroll
-      for (int u = 0; u < kU; ++u) w[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (s)
-        cells_of([&](int u, int r, int i) __attribute__((always_inline)) {
-          w[u][r] = decayed(d, s[i]);
-        });
-    };
-    auto store_state = [&](float* s) __attribute__((always_inline)) {
-      cells_of([&](int u, int r, int i) __attribute__((always_inline)) { s[i] = w[u][r]; });
-    };
-
-    // Rows [lo, hi) of one sequence, whose state before them is in w; last:
-    // the state behind them is wanted undecayed.
-    auto segment = [&](int64_t lo, int64_t hi, bool last) __attribute__((always_inline)) {
-      const int64_t rows = hi - lo;
-      const int64_t first = p.back ? hi - 1 : lo;
-      // Chunks on their way: as many as there are registers for.
-      struct Ahead {
-        TileA a;
-        TileB b;
-        TileC c;
-        int64_t at;   // the chunk's first row
-      } ahead[kAhead];
-      auto held_at = [&](int64_t at) { return (int)(rows - at < C ? rows - at : C); };   // may be < 0
-      // The number of memory instructions in flight is the same on every usual way
-      // through the loop, so that a wait leaves the ones behind it alone; the rare
-      // ways end with a wait for all.
-      auto wait_all = [] { __builtin_amdgcn_s_waitcnt(0x0f70); };
-      auto load = [&](Ahead& x, int64_t at, int held) __attribute__((always_inline)) {
-        const int64_t row = held <= 0 ? first : p.back ? first - at - held + 1 : first + at;
-        if constexpr (kOut) x.a.load(la, pa + row * p.as, sa, !p.back, held, p.da);
-        x.b.load(lb, pb + row * p.bs, sb, !p.back, held, p.da);
-        x.c.load(lc, pc + row * p.cs, sc, !p.back, held, wide);
-        x.at = at;
+      auto bring = [&](int64_t row, int held) __attribute__((always_inline)) {
+        if constexpr (kOut) ta.load(la, pa + row * p.as, sa, !p.back, held, p.da);
+        tb.load(lb, pb + row * p.bs, sb, !p.back, held, p.da);
       };
-      auto stage = [&](Ahead& x) __attribute__((always_inline)) {
+      auto put = [&]() __attribute__((always_inline)) {
         if (p.da < DA) {
-          if constexpr (kOut) x.a.settle(p.da);
-          x.b.settle(p.da);
+          if constexpr (kOut) ta.settle(p.da);
+          tb.settle(p.da);
         }
-        if (wide < kWide) x.c.settle(wide);
         if constexpr (kOut) {
-          x.a.store(la, lds.a[0], nullptr);
-          x.b.store(lb, lds.b[0], lds.bt[0]);
+          ta.store(la, lds.a[0], nullptr);
+          tb.store(lb, lds.b[0], lds.bt[0]);
         } else {
-          x.b.store(lb, nullptr, lds.bt[0]);
+          tb.store(lb, nullptr, lds.bt[0]);
         }
-        x.c.store(lc, nullptr, lds.ct[0]);
       };
-      // The chunk at row `at`, whose values are (or are brought) in x; returns
-      // where the next one starts.
-      auto chunk = [&](Ahead& x, int64_t at) __attribute__((always_inline)) {
-        int held = held_at(at);
-        if (kAhead > 1 && x.at != at) {   // a chunk before was cut short
-          load(x, at, held);
-          wait_all();
-        }
-        for (bool cut_short = false;;) {
-          stage(x);
-          if constexpr (!kOut) break;
-          if (!cut_short && __any(x.b.any_bad() || x.c.any_bad())) {
-            const int b1 = x.b.first_bad(), b2 = x.c.first_bad();
-            const int bad = b1 < b2 ? b1 : b2;
-            if (bad < C) atomicMin(&lds.bad, bad);
-          }
-          __syncthreads();
-          const int bad = lds.bad;
-          if (cut_short || bad == C) break;   // for the whole workgroup
-          cut_short = true;
-          held = bad > 0 ? bad : 1;
-          load(x, at, held);
-          wait_all();
-          __syncthreads();
-          if (tid == 0) lds.bad = C;
-        }
-        if constexpr (!kOut) __syncthreads();
-        const int64_t next = at + held, then = next + (kAhead - 1) * C;
-        load(x, then, held_at(then));   // none behind the last
-
+      auto bad = [&]() __attribute__((always_inline)) {
+        return __any(tb.any_bad()) ? tb.first_bad() : C;
+      };
+      auto scores = [&](int, bool) __attribute__((always_inline)) {
         if constexpr (kOut) {
-          // the scores, transposed: block (t, half) of 16 rows of b by rows 16 bi of a
+          const uint32_t at_row = fresh(row_base), at_col = fresh(col_base);
+          // transposed: block (t, half) of 16 rows of b by rows 16 bi of a
 #pragma unroll
           for (int m = 0; m < kMine; ++m) {
             if (!mine(m)) continue;
@@ -774,8 +779,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
               bf16x8 fb[kIn], fa[kIn];
 #pragma unroll
               for (int k = 0; k < kIn; ++k) {
-                fb[k] = row_frag(lds.b[k], 32 * t + 16 * half + n, 4 * s + g);
-                fa[k] = row_frag(lds.a[k], 16 * bi + n, 4 * s + g);
+                fb[k] = frag(lds.b[k], operand_at<DA / 8, false>(at_row, 2 * t + half, s));
+                fa[k] = frag(lds.a[k], operand_at<DA / 8, false>(at_row, bi, s));
               }
               mma(acc, fb, fa);
             }
@@ -783,8 +788,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               x[r] = ws[m][r] * acc[r];
-              if (m != 1)
-                x[r] = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, x[r]) & seen[m / 2][r]);
+              if (m != 1) x[r] = after + r <= 0 ? x[r] : 0.0f;
             }
             uint32_t piece[kMid][2];
             cut<kMid, 4>(x, piece);
@@ -794,208 +798,232 @@ __global__ __launch_bounds__(64 * kWaves, 2) void logmel_attn_chunk_kernel(AttnJ
               *reinterpret_cast<u32x2*>(&lds.p[k][f][lane][4 * half]) =
                   u32x2{piece[k][0], piece[k][1]};
           }
-        }
-
-        f32x4 o[kI];
-        bf16x8 fc[kT][kIn];
-        if (works) {
-          if constexpr (kOut) {
-#pragma unroll
-            for (int i = 0; i < kI; ++i) o[i] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int s = 0; s < kS; ++s) {
-              if (s && 32 * s >= p.da) break;
-              float x[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = w[2 * s + e / 4][e & 3];
-              uint32_t piece[kMid][4];
-              cut<kMid, 8>(x, piece);
-              bf16x8 fw[kMid];
-#pragma unroll
-              for (int k = 0; k < kMid; ++k) fw[k] = frag(piece[k]);
-#pragma unroll
-              for (int i = 0; i < kI; ++i) {
-                bf16x8 fa[kIn];
-#pragma unroll
-                for (int k = 0; k < kIn; ++k) fa[k] = row_frag(lds.a[k], 16 * i + n, 4 * s + g);
-                mma(o[i], fw, fa);
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < kI; ++i)
-#pragma unroll
-              for (int r = 0; r < 4; ++r) o[i][r] *= enter[i];
-          }
-
 #pragma unroll
           for (int t = 0; t < kT; ++t)
 #pragma unroll
             for (int k = 0; k < kIn; ++k)
-              fc[t][k] = col_frag(lds.ct[k], 16 * wave + n, 4 * t + g);
-
-          weigh(last && next == rows ? held - 1 : held);
+              fc[t][k] = frag(lds.ct[k], operand_at<C / 8, true>(at_col, wave, t));
+        }
+      };
+      auto output = [&](int64_t row, int held) __attribute__((always_inline)) {
+        if constexpr (kOut) {
+          f32x4 o[kI];
 #pragma unroll
-          for (int u = 0; u < kU; ++u)
+          for (int i = 0; i < kI; ++i) {
+            o[i] = *reinterpret_cast<const f32x4*>(lds.from_state[wave][i][lane]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) w[u][r] = decayed(whole, w[u][r]);
+            for (int t = 0; t <= i / 2; ++t) {
+              bf16x8 fp[kMid];
+              const int f = i < 2 ? i : 2 * i - 2 + t;
 #pragma unroll
-          for (int t = 0; t < kT; ++t) {
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              x[e] = 0.0f;
-#pragma unroll
-              for (int k = kIn - 1; k >= 0; --k) x[e] += (float)fc[t][k][e];
-              x[e] *= wc_[t][e];
-            }
-            uint32_t piece[kState][4];
-            cut<kState, 8>(x, piece);
-            bf16x8 fw[kState];
-#pragma unroll
-            for (int k = 0; k < kState; ++k) fw[k] = frag(piece[k]);
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-              bf16x8 fb[kIn];
-#pragma unroll
-              for (int k = 0; k < kIn; ++k) fb[k] = col_frag(lds.bt[k], 16 * u + n, 4 * t + g);
-              mma(w[u], fb, fw);
+              for (int k = 0; k < kMid; ++k) fp[k] = frag(lds.p[k][f][lane], 0);
+              mma(o[i], fc[t], fp);
             }
           }
-        }
-        // the scores are whole, and the tiles read to the end: the next chunk's may
-        // be written (its scores after a barrier more)
-        __syncthreads();
-
-        if constexpr (kOut) {
-          // rows i of the output: four channels of a row per lane
-          const int64_t row = p.back ? first - at - held + 1 : first + at;   // the lowest
-          const int64_t to = row * p.os + (int64_t)h * p.dc + c0;
+          // rows i of the output: four channels of a row per lane where there are
+          // four, else behind the buffer
+          const int64_t to = row * p.os + (int64_t)h * p.dc;
           const uint32_t size = p.of ? 4 : (uint32_t)sizeof(T), pitch = (uint32_t)p.os * size;
-          const auto buffer =
-              buffer_of(p.of ? static_cast<const void*>(p.of + to) : p.o + to,
-                        (uint32_t)(held - 1) * pitch + (uint32_t)(wc < kWide ? wc : kWide) * size);
-          constexpr uint32_t kNowhere = 0u - 16u;   // behind any buffer
+          const auto buffer = buffer_of(p.of ? static_cast<const void*>(p.of + to) : p.o + to,
+                                        (uint32_t)(held - 1) * pitch + (uint32_t)wide * size);
+          constexpr uint32_t kNowhere = 0u - 16u;
           const int c = 16 * wave + 4 * g;
           const uint32_t side = (uint32_t)c * size;
           auto at_row = [&](int i) __attribute__((always_inline)) {
             const int r = 16 * i + n;
             return (uint32_t)(p.back ? held - 1 - r : r) * pitch + side;
           };
-          if (works) {
-#pragma unroll
-            for (int i = 0; i < kI; ++i) {
-#pragma unroll
-              for (int t = 0; t <= i / 2; ++t) {
-                bf16x8 fp[kMid];
-                const int f = i < 2 ? i : 2 * i - 2 + t;
-#pragma unroll
-                for (int k = 0; k < kMid; ++k) fp[k] = frag(&lds.p[k][f][lane][0]);
-                mma(o[i], fc[t], fp);
-              }
-            }
-          }
-          // four channels at a time where there are four, else behind the buffer
-          const bool quad = c + 4 <= wc;   // (not in a wavefront without columns)
+          const bool quad = c + 4 <= wide;
 #pragma unroll
           for (int i = 0; i < kI; ++i) {
-            const uint32_t to = quad ? at_row(i) : kNowhere;
+            const uint32_t at = quad ? at_row(i) : kNowhere;
             if (p.of || sizeof(T) == 4) {
-              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[i]), buffer, to,
+              __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[i]), buffer, at,
                                                      0, 0);
             } else if constexpr (sizeof(T) == 2) {
               Packed<T, 4> y;
 #pragma unroll
               for (int j = 0; j < 4; ++j) y.v[j] = (T)o[i][j];
-              __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), buffer, to, 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, y), buffer, at, 0, 0);
             }
           }
-          if ((wc & 3) && 16 * wave + 16 > wc) {   // up to three at the end of the columns
+          if ((wide & 3) && works && 16 * wave + 16 > wide) {   // up to three at the end
 #pragma unroll
             for (int i = 0; i < kI; ++i)
 #pragma unroll
               for (int j = 0; j < 3; ++j) {
-                const bool on = !quad && c + j < wc && 16 * i + n < held;
-                const uint32_t to = on ? at_row(i) + j * size : kNowhere;
+                const bool on = !quad && c + j < wide && 16 * i + n < held;
+                const uint32_t at = on ? at_row(i) + j * size : kNowhere;
                 const float y = o[i][j];
                 if (p.of || sizeof(T) == 4)
                   __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, y), buffer,
-                                                        to, 0, 0);
+                                                        at, 0, 0);
                 else if constexpr (sizeof(T) == 2)
                   __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (T)y),
-                                                        buffer, to, 0, 0);
+                                                        buffer, at, 0, 0);
               }
           }
         }
-        return next;
       };
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) load(ahead[i], i * C, held_at(i * C));
-      for (int64_t at = 0; at < rows;) {
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          if (at < rows) at = chunk(ahead[i], at);
-      }
-    };
-
-    const Decay one = {1.0f, 0.0f}, lambda = decay_of(decay, 1.0f);
-    // Rows [lo, hi) of sequence i, of part b.
-    auto run = [&](int64_t i, int64_t lo, int64_t hi, bool starts, bool ends, int64_t b) __attribute__((always_inline)) {
-      const int64_t of_seq = (i * p.heads + h) * cells;
-      const float* in = p.state ? p.state + of_seq : nullptr;
-      float* out = p.state_out ? p.state_out + of_seq : nullptr;
-      if (lo >= hi) {   // an empty sequence
-        if (starts && ends && out)
-          cells_of([&](int, int, int c) __attribute__((always_inline)) {
-            out[c] = in ? in[c] : 0.0f;
-          });
-        return;
-      }
-      auto slot = [&](float* s, int64_t at) { return s + (at * p.heads + h) * cells; };
-      const bool fresh_start = p.back ? ends : starts;
-      const bool put_by = starts && !ends && walk.kept;
-      const float* from = fresh_start ? (put_by ? slot(walk.kept, b) : in)
-                                      : slot(walk.between, p.back ? b : b - 1);
-      load_state(from, fresh_start && !put_by && !p.back ? lambda : one);
-      segment(lo, hi, !p.back && ends);
-      if ((p.back ? starts : ends) && out) store_state(out);
-    };
-
-    // The sequences of this workgroup's rows, in order: its own, or those of its
-    // part from the one that enters it on.
-    const int64_t r0 = which * walk.part_rows;
-    const int64_t r1 = walk.parts == 0 || r0 + walk.part_rows > p.rows ? p.rows
-                                                                       : r0 + walk.part_rows;
-    auto within = [&](int64_t r) { return r < r0 ? r0 : r > r1 ? r1 : r; };
-    if constexpr (!kOut) {
-      // the state that leaves the part, from the sequence across its end (its
-      // start, backwards)
-      const int64_t i = across(p, p.back ? r0 : r1), place = p.back ? which - 1 : which;
-      const int64_t from = i < 0 ? 0 : p.off[i], to = i < 0 ? 0 : p.off[i + 1];
-      const bool fresh = p.back ? to <= r1 : from >= r0;
-      if (place < 0 || place >= walk.parts - 1) continue;
-      if (tid == 0 && h == 0) walk.through[place] = i < 0 ? 0 : fresh ? 1 : 2;
-      if (i < 0) continue;
-      const int64_t of_seq = (i * p.heads + h) * cells;
-      load_state(fresh && p.state ? p.state + of_seq : nullptr, p.back ? one : lambda);
-      if (fresh && walk.kept) store_state(walk.kept + (which * p.heads + h) * cells);
-      segment(within(from), within(to), false);
-      store_state(walk.between + (place * p.heads + h) * cells);
+      each([&](int64_t, int64_t lo, int64_t hi, bool, bool) __attribute__((always_inline)) {
+        chunks(lo, hi, bring, put, bad, scores, output);
+      });
     } else {
-      int64_t i = which;
-      bool enters = false;
-      if (walk.parts) {
-        i = first_from(p, r0);
-        enters = which > 0 && i > 0 && i <= p.n_seq && p.off[i] > r0;
-        i -= enters;
+      const T* pc = p.c + (int64_t)(h / p.share_c) * p.dc;
+      const uint32_t sc = (uint32_t)(p.cs * sizeof(T));
+      const typename TileC::Places lc(sc, !p.back, wide, false, false);
+      float enter[kI];
+      if constexpr (kOut) {
+#pragma unroll
+        for (int i = 0; i < kI; ++i) enter[i] = p.beta * power(16 * i + n);
       }
-      const bool end = walk.parts == 0 || which == walk.parts - 1;
-      do {
-        if (i >= p.n_seq || !(enters || end || p.off[i] < r1)) break;
-        const int64_t lo = enters ? r0 : within(p.off[i]);
-        run(i, lo, within(p.off[i + 1]), !enters, end || p.off[i + 1] <= r1, which);
-        enters = false;
-        ++i;
-      } while (walk.parts);
+      // of the rows that enter the state, `left` rows before the next chunk's first
+      Decay whole;
+      int left = -1;
+      auto weigh = [&](int to) __attribute__((always_inline)) {
+        if (to == left) return;
+        left = to;
+        whole = decay_of(decay, (float)to);
+        if (lane < C) lds.weight[wave][lane] = lane <= to ? p.gamma * power(to - lane) : 0.0f;
+      };
+
+      f32x4 w[kU];
+      // f(u, r, cell of the state) for this lane's values w[u][r] that are cells
+      auto cells_of = [&](auto f) __attribute__((always_inline)) {
+        const int c = fresh(16 * wave + n), a0 = fresh(8 * g);
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int a = a0 + 32 * (u >> 1) + 4 * (u & 1) + r;
+            if (a < p.da && c < p.dc) f(u, r, p.transposed ? c * p.da + a : a * p.dc + c);
+          }
+      };
+      auto load_state = [&](const float* s, Decay d) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) w[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (s)
+          cells_of([&](int u, int r, int i) __attribute__((always_inline)) {
+            w[u][r] = decayed(d, s[i]);
+          });
+      };
+      auto store_state = [&](float* s) __attribute__((always_inline)) {
+        cells_of([&](int u, int r, int i) __attribute__((always_inline)) { s[i] = w[u][r]; });
+      };
+      TileC tc;
+      bool undecayed = false;   // the state behind the segment's last row is wanted so
+
+      auto bring = [&](int64_t row, int held) __attribute__((always_inline)) {
+        tc.load(lc, pc + row * p.cs, sc, !p.back, held, wide);
+      };
+      auto put = [&]() __attribute__((always_inline)) {
+        if (wide < kWide) tc.settle(wide);
+        tc.store(lc, nullptr, lds.ct[0]);
+      };
+      auto bad = [&]() __attribute__((always_inline)) {
+        return __any(tc.any_bad()) ? tc.first_bad() : C;
+      };
+      auto update = [&](int held, bool end) __attribute__((always_inline)) {
+        if (!works) return;
+        const uint32_t at_row = fresh(row_base), at_col = fresh(col_base);
+        if constexpr (kOut) {
+          f32x4 o[kI];
+#pragma unroll
+          for (int i = 0; i < kI; ++i) o[i] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int s = 0; s < kS; ++s) {
+            if (s && 32 * s >= p.da) break;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = w[2 * s + e / 4][e & 3];
+            uint32_t piece[kMid][4];
+            cut<kMid, 8>(x, piece);
+            bf16x8 fw[kMid];
+#pragma unroll
+            for (int k = 0; k < kMid; ++k) fw[k] = frag(piece[k]);
+#pragma unroll
+            for (int i = 0; i < kI; ++i) {
+              bf16x8 fa[kIn];
+#pragma unroll
+              for (int k = 0; k < kIn; ++k)
+                fa[k] = frag(lds.a[k], operand_at<DA / 8, false>(at_row, i, s));
+              mma(o[i], fw, fa);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kI; ++i) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) o[i][r] *= enter[i];
+            *reinterpret_cast<f32x4*>(lds.from_state[wave][i][lane]) = o[i];
+          }
+        }
+        weigh(undecayed && end ? held - 1 : held);
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) w[u][r] = decayed(whole, w[u][r]);
+#pragma unroll
+        for (int t = 0; t < kT; ++t) {
+          bf16x8 fc[kIn];
+#pragma unroll
+          for (int k = 0; k < kIn; ++k)
+            fc[k] = frag(lds.ct[k], operand_at<C / 8, true>(at_col, wave, t));
+          const f32x4* weights =
+              reinterpret_cast<const f32x4*>(&lds.weight[wave][32 * t + 8 * g]);
+          const f32x4 w0 = weights[0], w1 = weights[1];
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[e] = 0.0f;
+#pragma unroll
+            for (int k = kIn - 1; k >= 0; --k) x[e] += (float)fc[k][e];
+            x[e] *= e < 4 ? w0[e & 3] : w1[e & 3];
+          }
+          uint32_t piece[kState][4];
+          cut<kState, 8>(x, piece);
+          bf16x8 fw[kState];
+#pragma unroll
+          for (int k = 0; k < kState; ++k) fw[k] = frag(piece[k]);
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            bf16x8 fb[kIn];
+#pragma unroll
+            for (int k = 0; k < kIn; ++k)
+              fb[k] = frag(lds.bt[k], operand_at<C / 8, true>(at_col, u, t));
+            mma(w[u], fb, fw);
+          }
+        }
+      };
+      const Decay one = {1.0f, 0.0f}, lambda = decay_of(decay, 1.0f);
+      each([&](int64_t i, int64_t lo, int64_t hi, bool starts, bool ends)
+               __attribute__((always_inline)) {
+        const int64_t of_seq = (i * p.heads + h) * cells;
+        const float* in = p.state ? p.state + of_seq : nullptr;
+        float* out = p.state_out ? p.state_out + of_seq : nullptr;
+        if (kOut && lo >= hi) {   // an empty sequence
+          if (starts && ends && out)
+            cells_of([&](int, int, int c) __attribute__((always_inline)) {
+              out[c] = in ? in[c] : 0.0f;
+            });
+          return;
+        }
+        // the state before the first row worked: the sequence's own, as its first row
+        // meets it, or that of the place between two parts
+        auto slot = [&](float* s, int64_t at) { return s + (at * p.heads + h) * cells; };
+        const bool own = p.back ? ends : starts;
+        const bool put_by = kOut && starts && !ends && walk.kept;
+        const float* from = own ? (put_by ? slot(walk.kept, which) : in)
+                            : kOut ? slot(walk.between, p.back ? which : which - 1)
+                                   : nullptr;
+        load_state(from, own && !put_by && !p.back ? lambda : one);
+        if (!kOut && own && walk.kept) store_state(slot(walk.kept, which));
+        undecayed = kOut && !p.back && ends;
+        chunks(lo, hi, bring, put, bad, update, [](int64_t, int) {});
+        if constexpr (!kOut)
+          store_state(slot(walk.between, p.back ? which - 1 : which));
+        else if ((p.back ? starts : ends) && out)
+          store_state(out);
+      });
     }
   }
 }
@@ -1070,7 +1098,7 @@ AttnSplit split_of(const logmel_attention_input& in, int64_t dc, int64_t widest,
     s.how = AttnSplit::kRows;
     return s;
   }
-  const int64_t chunk = in.type == LOGMEL_F32 ? 32 : 64;
+  const int64_t chunk = in.type == LOGMEL_BF16 ? 64 : 32;
   const int64_t lanes = in.heads;                          // workgroups side by side
   const int64_t slots = 2 * (int64_t)cus;                  // (of eight wavefronts half as many
                                                            // are resident, which take turns)
@@ -1118,7 +1146,7 @@ hipError_t launch_chunks(const AttnJob<T>& p, const AttnSplit& s, Walk k, bool b
     k.items = s.parts * p.heads;
     if (between) {
       logmel_attn_chunk_kernel<T, DA, kWaves, false>
-          <<<grid(k.items), 64 * kWaves, 0, stream>>>(p, k);
+          <<<grid(k.items), 128 * kWaves, 0, stream>>>(p, k);
       logmel_attn_between_kernel<T>
           <<<(unsigned)ceil_div((int64_t)p.heads * p.da * p.dc, 64), 64, 0, stream>>>(p, k);
     }
@@ -1126,7 +1154,7 @@ hipError_t launch_chunks(const AttnJob<T>& p, const AttnSplit& s, Walk k, bool b
     k.items = p.n_seq * p.heads;
   }
   logmel_attn_chunk_kernel<T, DA, kWaves, true>
-      <<<grid(k.items), 64 * kWaves, 0, stream>>>(p, k);
+      <<<grid(k.items), 128 * kWaves, 0, stream>>>(p, k);
   return hipGetLastError();
 }
 
@@ -1145,7 +1173,6 @@ hipError_t launch_job(const AttnJob<T>& p, const AttnSplit& s, const PartSpace& 
     return hipGetLastError();
   }
   Walk k{};
-  k.slabs = 1;
   k.between = ws;
   k.through = reinterpret_cast<int*>(ws + space.between);
   k.kept = space.kept ? ws + space.between + space.through : nullptr;
