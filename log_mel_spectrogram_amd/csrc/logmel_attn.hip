@@ -306,12 +306,13 @@ __device__ __forceinline__ int place(int i) { return 32 * (i >> 3) + 16 * (i & 1
 template <int kUnits, bool kAcross>
 __device__ __forceinline__ int unit_at(int r, int u) {
   if constexpr (kUnits >= 8) {
-    const int h = kAcross ? (r ^ (r >> 3)) & 7
+    const int h = kAcross ? ((r ^ (r >> 3)) & 7) ^ ((r >> 4) & 2)
                           : (r & 7) ^ ((r >> 3) & 1) ^ ((r >> 2) & 4);
     return r * kUnits + (u ^ h);
   } else {
     const int line = r >> 1;
-    const int h = ((line ^ (line >> 2)) & 1) | (line & 2) | ((line >> 1) & 4);
+    const int h = (((line ^ (line >> 2)) & 1) | (line & 2) | ((line >> 1) & 4)) ^
+                  (6 * ((line >> 4) & 1));
     return line * 8 + ((((r & 1) << 2) | u) ^ h);
   }
 }
@@ -320,7 +321,8 @@ __device__ __forceinline__ int unit_at(int r, int u) {
 // from that of r and u.
 template <int kUnits, bool kAcross>
 __device__ __forceinline__ uint32_t operand_at(uint32_t at, int i, int s) {
-  const uint32_t turn = kUnits >= 8 && kAcross ? (2 * i) & 7 : 4 * (i & 1);
+  const uint32_t turn = kUnits >= 8 ? (kAcross ? (2 * (i & 1)) ^ (6 * ((i >> 1) & 1)) : 4 * (i & 1))
+                                    : (4 * (i & 1)) ^ (6 * ((i >> 1) & 1));
   return (at ^ (16 * (turn ^ (uint32_t)(4 * s)))) + (uint32_t)i * (kUnits * 256);
 }
 
@@ -343,200 +345,257 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint3
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000);
 }
 
-// A tile of kRows rows and kWidth channels in registers, on its way from memory
-// to LDS, in blocks of 4 x 4 values: eight blocks side by side and eight below
-// each other per wavefront, so that memory is read 64 or 128 bytes at a time and
-// LDS is written, along rows and along columns, without bank conflicts.
-// kThreads: those that bring it, a number that divides the workgroup's; kFirst:
-// the one that takes the first block, so that several tiles that do not fill them
-// are spread over them.
-template <typename T, int kRows, int kWidth, int kThreads, int kFirst>
-struct Tile {
+// A tile's place in memory and LDS.
+template <typename T>
+struct TileAt {
+  const T* base;      // its lowest row
+  uint32_t pitch;     // bytes between rows
+  int width;          // channels there are
+  uint16_t* rows;     // where it goes, along rows and along columns
+  uint16_t* cols;
+};
+
+// kTiles (one or two) tiles of kRows rows and kWidth channels in registers, on
+// their way from memory to LDS, in blocks of four rows by 16 bytes: up to eight
+// blocks side by side in a wavefront, so that memory is read 128 bytes at a time
+// and LDS is written, along rows and along columns, without bank conflicts. Each
+// block is a thread's, each wavefront's blocks are of one tile; kThreads bring
+// them, a number that divides the workgroup's. Of two tiles the first goes to LDS
+// along its rows, the second along both; one goes along its columns. kSkip: the
+// first of two is not wanted, nor the second's rows.
+template <typename T, int kRows, int kWidth, int kThreads, int kTiles, bool kSkip>
+struct Tiles {
   static constexpr int kIn = Pieces<T>::kIn;
-  static constexpr int kBlocks = kRows / 4 * (kWidth / 4);
-  static constexpr int kIts = (kBlocks + kThreads - 1) / kThreads;
-  using Word = std::conditional_t<sizeof(T) == 2, u32x2, u32x4>;
+  // fp16 rows, which are cut into pieces on the way, go by 8 bytes: more threads
+  // take part (70,001 x 6 x 40 x 71 with gradient 1,114 us, 1,183 by 16); bf16 rows,
+  // which are stored as they are, by 16 (64 x 2998 x 8 x 64 259 us, 271 by 8)
+  static constexpr int kCols = std::is_same_v<T, f16_t> ? 4 : 16 / (int)sizeof(T);
+  static constexpr int kDwords = kCols * (int)sizeof(T) / 4;   // of a block's row
+  using Row = std::conditional_t<kDwords == 4, u32x4, u32x2>;
+  static constexpr int kWide = kWidth / kCols, kBlocks = kRows / 4 * kWide;   // of a tile
+  static constexpr int kIts = (kTiles * kBlocks + kThreads - 1) / kThreads;
+  static_assert(kBlocks % 64 == 0);
+
+  // The first block of this wavefront: kTiles * kBlocks and more where it has none.
+  static __device__ __forceinline__ int first(int it) {
+    return (int)(__builtin_amdgcn_readfirstlane(threadIdx.x) % kThreads & ~63) + kThreads * it;
+  }
+  static __device__ __forceinline__ bool second(int it) {
+    if (kTiles == 1) return false;
+    return kBlocks % kThreads == 0 ? it >= kBlocks / kThreads : first(it) >= kBlocks;
+  }
+  static __device__ __forceinline__ bool on(int it) {
+    return (kTiles * kBlocks % kThreads == 0 || first(it) < kTiles * kBlocks) &&
+           !(kSkip && !second(it));
+  }
+  static __device__ __forceinline__ void at(int tid, int it, int& rb, int& cb) {
+    constexpr int kSide = kWide < 8 ? kWide : 8, kDown = 64 / kSide;
+    const int i = (tid % kThreads + kThreads * it) % kBlocks, rest = i >> 6;
+    cb = i % kSide + kSide * (rest % (kWide / kSide));
+    rb = (i & 63) / kSide + kDown * (rest / (kWide / kSide));
+  }
+
   // Where this lane's blocks lie: in memory from the tile's lowest row on (from
-  // its first row upwards, from its last row downwards), and in LDS. 2-byte values
-  // are read in blocks that do not pass the row's end (a word that does would be 0
-  // at the buffer's), so that the last ones are shifted back.
-  static constexpr bool back_from_end() { return sizeof(T) == 2; }
+  // its first row upwards, from its last row downwards), and in LDS. Blocks do not
+  // pass the row's end (of 2-byte values a word that does would be 0 at the
+  // buffer's): the last ones are shifted back.
   struct Places {
-    uint32_t from[kIts], row[kIts], col[kIts];
-    __device__ __forceinline__ Places(uint32_t pitch, bool up, int width, bool rows_placed,
-                                      bool cols_placed) {
+    uint32_t from[kIts], row[kIts], col[kIts], col2[kIts];
+    __device__ __forceinline__ Places(const TileAt<T>& x, const TileAt<T>& y, bool up,
+                                      bool placed_second) {
 #pragma unroll
       for (int it = 0; it < kIts; ++it) {
         int rb, cb;
         at(threadIdx.x, it, rb, cb);
-        const uint32_t down = (uint32_t)(4 * rb) * pitch;
-        const int c = back_from_end() && 4 * cb > width - 4 ? width - 4 : 4 * cb;
+        const TileAt<T>& t = second(it) ? y : x;
+        const bool placed = second(it) && placed_second;
+        const uint32_t down = (uint32_t)(4 * rb) * t.pitch;
+        const int c = kCols * cb > t.width - kCols ? t.width - kCols : kCols * cb;
         from[it] = (up ? down : 0u - down) + (uint32_t)c * (uint32_t)sizeof(T);
-        row[it] = half_at<kWidth / 8, false>(rows_placed ? place(rb) : 4 * rb, cb);
-        col[it] = half_at<kRows / 8, true>(cols_placed ? place(cb) : 4 * cb, rb);
+        row[it] = kCols == 8
+                      ? 16 * unit_at<kWidth / 8, false>(placed ? place(rb) : 4 * rb, cb)
+                      : half_at<kWidth / 8, false>(placed ? place(rb) : 4 * rb, cb);
+        // columns four at a time: the block's first four, and the others
+        const int c4 = kCols / 4 * cb;
+        col[it] = half_at<kRows / 8, true>(placed ? place(c4) : 4 * c4, rb);
+        col2[it] = half_at<kRows / 8, true>(placed ? place(c4 + 1) : 4 * c4 + 4, rb);
       }
     }
   };
 
-  Word v[kIts][4];
+  Row v[kIts][4];
 
-  // For a wavefront as a whole: blocks come in 64s.
-  static __device__ __forceinline__ bool on(int it) {
-    static_assert(kBlocks % 64 == 0);
-    if (kBlocks % kThreads == 0) return true;
-    const int first = __builtin_amdgcn_readfirstlane(
-        ((int)threadIdx.x % kThreads + kThreads - kFirst) % kThreads & ~63);
-    return first + kThreads * it < kBlocks;
-  }
-  static __device__ __forceinline__ void at(int tid, int it, int& rb, int& cb) {
-    const int i = (tid % kThreads + kThreads - kFirst) % kThreads + kThreads * it, rest = i >> 6;
-    constexpr int kWide = kWidth / 32;
-    cb = (i & 7) + 8 * (rest % kWide);
-    rb = ((i >> 3) & 7) + 8 * (rest / kWide);
-  }
-
-  // base: the tile's lowest row; up: whether that is its first; held: the rows
-  // there are, which may be none. Rows from held on lie behind the buffer (or,
-  // their offsets being negative, far behind it) and are 0; `settle` sees to the
-  // channels.
-  __device__ __forceinline__ void load(const Places& k, const T* base, uint32_t pitch, bool up,
-                                       int held, int width) {
-    const auto buffer = buffer_of(
-        base, held > 0 ? (uint32_t)(held - 1) * pitch + (uint32_t)width * (uint32_t)sizeof(T) : 0u);
-    const uint32_t step = up ? pitch : 0u - pitch;
-    const uint32_t first = up ? 0u : (uint32_t)(held - 1) * pitch;
+  // up: whether the lowest row is the first; held: the rows there are, which may
+  // be none. Rows from held on lie behind the buffer (or, their offsets being
+  // negative, far behind it) and are 0; `settle` sees to the channels.
+  __device__ __forceinline__ void load(const Places& k, const TileAt<T>& x, const TileAt<T>& y,
+                                       bool up, int held) {
 #pragma unroll
     for (int it = 0; it < kIts; ++it) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[it][r] = Word{};
+      for (int r = 0; r < 4; ++r) v[it][r] = Row{};
       if (!on(it)) continue;
-      uint32_t to = k.from[it] + first;
+      const T* base = second(it) ? y.base : x.base;
+      const uint32_t pitch = second(it) ? y.pitch : x.pitch;
+      const int width = second(it) ? y.width : x.width;
+      const auto buffer = buffer_of(
+          base, held > 0 ? (uint32_t)(held - 1) * pitch + (uint32_t)width * (uint32_t)sizeof(T) : 0u);
+      uint32_t to = k.from[it] + (up ? 0u : (uint32_t)(held - 1) * pitch);
+      const uint32_t step = up ? pitch : 0u - pitch;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        if constexpr (sizeof(T) == 2)
-          v[it][r] = __builtin_amdgcn_raw_buffer_load_b64(buffer, to, 0, 0);
-        else
+        if constexpr (kDwords == 4)
           v[it][r] = __builtin_amdgcn_raw_buffer_load_b128(buffer, to, 0, 0);
+        else
+          v[it][r] = __builtin_amdgcn_raw_buffer_load_b64(buffer, to, 0, 0);
         to += step;
       }
     }
   }
 
-  // 0 in channels from width on, in whose place stands what lies there, and the
-  // last ones where they belong.
+  // 0 in channels from the width on, and the last ones where they belong.
   __device__ __forceinline__ void settle(int width) {
     const int tid = fresh(threadIdx.x);
 #pragma unroll
     for (int it = 0; it < kIts; ++it) {
       int rb, cb;
       at(tid, it, rb, cb);
-      const int left = width - 4 * cb;
-      if constexpr (sizeof(T) == 2) {
-        const int by = left >= 4 ? 0 : left > 0 ? 16 * (4 - left) : 0;
+      const int left = width - kCols * cb;   // channels of the block that there are
+      const int by = left >= kCols || left <= 0 ? 0 : kCols - left;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint64_t x = left > 0 ? __builtin_bit_cast(uint64_t, v[it][r]) >> by : 0;
-          v[it][r] = __builtin_bit_cast(Word, x);
+      for (int r = 0; r < 4; ++r) {
+        if constexpr (kDwords == 2) {
+          const uint64_t x = left > 0 ? __builtin_bit_cast(uint64_t, v[it][r]) >> (16 * by) : 0;
+          v[it][r] = __builtin_bit_cast(Row, x);
+          continue;
         }
-      } else {
+        Row x = v[it][r];
+        constexpr int kHalf = sizeof(T) == 2, kN = kDwords;   // words are two values
+        if constexpr (kHalf) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t keep = left > j ? ~0u : 0u;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) v[it][r][j] &= keep;
+          for (int j = 0; j < kN; ++j) {
+            const uint32_t next = j + 1 < kN ? x[(j + 1) % kN] : 0u;
+            x[j] = by & 1 ? __builtin_amdgcn_alignbit(next, x[j], 16) : x[j];
+          }
         }
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          x[j] = by >> kHalf & 1 ? (j + 1 < kN ? x[(j + 1) % kN] : 0u) : x[j];
+#pragma unroll
+        for (int j = 0; j < kN; ++j)
+          x[j] = by >> kHalf & 2 ? (j + 2 < kN ? x[(j + 2) % kN] : 0u) : x[j];
+        if (left <= 0) x = Row{};
+        v[it][r] = x;
       }
     }
   }
 
-  // Whether a value is not finite: the largest of the words without signs is.
-  __device__ __forceinline__ bool any_bad() const {
-    if constexpr (sizeof(T) == 2) {
-      using u16x2 = __attribute__((ext_vector_type(2))) uint16_t;
-      constexpr uint16_t kInf = std::is_same_v<T, bf16_t> ? 0x7f80 : 0x7c00;
-      u16x2 m = {0, 0};
+  // Whether a value of the tile `which` is not finite: the largest of the words
+  // without signs is.
+  __device__ __forceinline__ bool any_bad(bool which) const {
+    bool bad = false;
 #pragma unroll
-      for (int it = 0; it < kIts; ++it)
+    for (int it = 0; it < kIts; ++it) {
+      if (second(it) != which) continue;
+      if constexpr (sizeof(T) == 2) {
+        using u16x2 = __attribute__((ext_vector_type(2))) uint16_t;
+        constexpr uint16_t kInf = std::is_same_v<T, bf16_t> ? 0x7f80 : 0x7c00;
+        u16x2 m = {0, 0};
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < kDwords; ++j)
             m = __builtin_elementwise_max(
                 m, __builtin_bit_cast(u16x2, (uint32_t)(v[it][r][j] & 0x7fff7fffu)));
-      return m[0] >= kInf || m[1] >= kInf;
-    } else {
-      uint32_t m = 0;
-#pragma unroll
-      for (int it = 0; it < kIts; ++it)
+        bad |= m[0] >= kInf || m[1] >= kInf;
+      } else {
+        uint32_t m = 0;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < kDwords; ++j) {
             const uint32_t w = v[it][r][j] & 0x7fffffffu;
             m = m > w ? m : w;
           }
-      return m >= 0x7f800000u;
+        bad |= m >= 0x7f800000u;
+      }
     }
+    return bad;
   }
 
-  // The first row with a value that is not finite, or kRows.
-  __device__ __forceinline__ int first_bad() const {
+  // The first row of it with a value that is not finite, or kRows.
+  __device__ __forceinline__ int first_bad(bool which) const {
     const int tid = fresh(threadIdx.x);
-    int first = kRows;
+    int found = kRows;
 #pragma unroll
     for (int it = 0; it < kIts; ++it) {
+      if (second(it) != which || !on(it)) continue;
       int rb, cb;
       at(tid, it, rb, cb);
 #pragma unroll
       for (int r = 3; r >= 0; --r) {
-        const auto x = __builtin_bit_cast(Packed<T, 4>, v[it][r]);
+        const auto x = __builtin_bit_cast(Packed<T, kCols>, v[it][r]);
         bool bad = false;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) bad |= !__builtin_isfinite((float)x.v[j]);
-        first = bad && on(it) && 4 * rb + r < first ? 4 * rb + r : first;
+        for (int j = 0; j < kCols; ++j) bad |= !__builtin_isfinite((float)x.v[j]);
+        found = bad && 4 * rb + r < found ? 4 * rb + r : found;
       }
     }
-    return first;
+    return found;
   }
 
   // Into LDS: rows [kIn][kRows][kWidth] and columns [kIn][kWidth][kRows],
-  // whichever is not null.
-  __device__ __forceinline__ void store(const Places& k, uint16_t* rows, uint16_t* cols) const {
+  // whichever there are.
+  __device__ __forceinline__ void store(const Places& k, const TileAt<T>& x,
+                                        const TileAt<T>& y) const {
+    constexpr int kBytes = kRows * kWidth * 2;   // of a piece's tile
+    constexpr int kWords = kCols / 2;
 #pragma unroll
     for (int it = 0; it < kIts; ++it) {
       if (!on(it)) continue;
-      uint32_t w[4][kIn][2];
+      uint32_t w[4][kIn][kWords];
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         if constexpr (kIn == 1) {
-          w[r][0][0] = v[it][r][0], w[r][0][1] = v[it][r][1];
-        } else {
-          const auto y = __builtin_bit_cast(Packed<T, 4>, v[it][r]);
-          float x[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = (float)y.v[j];
-          cut<kIn, 4>(x, w[r]);
+          for (int j = 0; j < kWords; ++j) w[r][0][j] = v[it][r][j];
+        } else {
+          const auto z = __builtin_bit_cast(Packed<T, kCols>, v[it][r]);
+          float f[kCols];
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) f[j] = (float)z.v[j];
+          cut<kIn, kCols>(f, w[r]);
         }
       }
-      constexpr int kBytes = kRows * kWidth * 2;   // of a piece's tile
-      const uint32_t row = fresh(k.row[it]), col = fresh(k.col[it]);
+      uint16_t* rows = second(it) ? y.rows : x.rows;
+      uint16_t* cols = kTiles == 2 ? y.cols : x.cols;
+      if (kTiles == 2 && !kSkip) {
+        const uint32_t row = fresh(k.row[it]);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        char* to = reinterpret_cast<char*>(rows) + half_below<kWidth / 8>(row, r);
+        for (int r = 0; r < 4; ++r) {
+          char* to = reinterpret_cast<char*>(rows) + half_below<kWidth / 8>(row, r);
 #pragma unroll
-        for (int n = 0; n < kIn; ++n)
-          if (rows) *reinterpret_cast<u32x2*>(to + n * kBytes) = u32x2{w[r][n][0], w[r][n][1]};
+          for (int n = 0; n < kIn; ++n) {
+            if constexpr (kCols == 8)
+              *reinterpret_cast<u32x4*>(to + n * kBytes) =
+                  u32x4{w[r][n][0], w[r][n][1], w[r][n][2], w[r][n][3]};
+            else
+              *reinterpret_cast<u32x2*>(to + n * kBytes) = u32x2{w[r][n][0], w[r][n][1]};
+          }
+        }
       }
+      if (kTiles == 1 || second(it)) {
+        const uint32_t col = fresh(k.col[it]), col2 = fresh(k.col2[it]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        char* to = reinterpret_cast<char*>(cols) + half_below<kRows / 8>(col, c);
-        const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
+        for (int c = 0; c < kCols; ++c) {
+          char* to = reinterpret_cast<char*>(cols) + half_below<kRows / 8>(c < 4 ? col : col2, c & 3);
+          const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
 #pragma unroll
-        for (int n = 0; n < kIn; ++n)
-          if (cols)
+          for (int n = 0; n < kIn; ++n)
             *reinterpret_cast<u32x2*>(to + n * kBytes) =
                 u32x2{__builtin_amdgcn_perm(w[1][n][c / 2], w[0][n][c / 2], sel),
                       __builtin_amdgcn_perm(w[3][n][c / 2], w[2][n][c / 2], sel)};
+        }
       }
     }
   }
@@ -609,9 +668,10 @@ __global__ __launch_bounds__(128 * kWaves, 4) void logmel_attn_chunk_kernel(Attn
   constexpr int kThreads = 64 * kWaves, kWide = 16 * kWaves;   // of each half
   constexpr int kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid, kState = Pieces<T>::kState;
   constexpr int C = kChunk<T, DA, kWaves>, kI = C / 16, kT = C / 32, kS = DA / 32, kU = DA / 16;
-  using TileA = Tile<T, C, DA, kThreads, 0>;
-  using TileB = Tile<T, C, DA, kThreads, TileA::kBlocks % kThreads>;
-  using TileC = Tile<T, C, kWide, kThreads, 0>;
+  // of the scores' half (a is not brought where only the state is wanted), and of
+  // the state's
+  using TilesAB = Tiles<T, C, DA, kThreads, 2, !kOut>;
+  using TileC = Tiles<T, C, kWide, kThreads, 1, false>;
   __shared__ __attribute__((aligned(16))) ChunkLds<T, DA, kWide, C> lds;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % kWaves;
@@ -719,8 +779,9 @@ __global__ __launch_bounds__(128 * kWaves, 4) void logmel_attn_chunk_kernel(Attn
       const T* pa = p.a + (int64_t)(h / p.share_a) * p.da;
       const T* pb = p.b + (int64_t)(h / p.share_b) * p.da;
       const uint32_t sa = (uint32_t)(p.as * sizeof(T)), sb = (uint32_t)(p.bs * sizeof(T));
-      const typename TileA::Places la(sa, !p.back, p.da, false, false);
-      const typename TileB::Places lb(sb, !p.back, p.da, true, true);
+      TileAt<T> a{pa, sa, p.da, lds.a[0], nullptr};
+      TileAt<T> b{pb, sb, p.da, lds.b[0], lds.bt[0]};
+      const typename TilesAB::Places places(a, b, !p.back, true);
       // this lane's weights of the scores: block (rows 16 bi, columns 32 t and half);
       // of eight wavefronts the first four take the blocks on the diagonal
       constexpr int kMine = C == 64 ? 3 : 1;
@@ -741,28 +802,20 @@ __global__ __launch_bounds__(128 * kWaves, 4) void logmel_attn_chunk_kernel(Attn
           }
         }
       }
-      TileA ta;
-      TileB tb;
+      TilesAB tiles;
       bf16x8 fc[kT][kIn];
 
       auto bring = [&](int64_t row, int held) __attribute__((always_inline)) {
-        if constexpr (kOut) ta.load(la, pa + row * p.as, sa, !p.back, held, p.da);
-        tb.load(lb, pb + row * p.bs, sb, !p.back, held, p.da);
+        a.base = pa + row * p.as;
+        b.base = pb + row * p.bs;
+        tiles.load(places, a, b, !p.back, held);
       };
       auto put = [&]() __attribute__((always_inline)) {
-        if (p.da < DA) {
-          if constexpr (kOut) ta.settle(p.da);
-          tb.settle(p.da);
-        }
-        if constexpr (kOut) {
-          ta.store(la, lds.a[0], nullptr);
-          tb.store(lb, lds.b[0], lds.bt[0]);
-        } else {
-          tb.store(lb, nullptr, lds.bt[0]);
-        }
+        if (p.da < DA) tiles.settle(p.da);
+        tiles.store(places, a, b);
       };
       auto bad = [&]() __attribute__((always_inline)) {
-        return __any(tb.any_bad()) ? tb.first_bad() : C;
+        return __any(tiles.any_bad(true)) ? tiles.first_bad(true) : C;
       };
       auto scores = [&](int, bool) __attribute__((always_inline)) {
         if constexpr (kOut) {
@@ -871,7 +924,8 @@ __global__ __launch_bounds__(128 * kWaves, 4) void logmel_attn_chunk_kernel(Attn
     } else {
       const T* pc = p.c + (int64_t)(h / p.share_c) * p.dc;
       const uint32_t sc = (uint32_t)(p.cs * sizeof(T));
-      const typename TileC::Places lc(sc, !p.back, wide, false, false);
+      TileAt<T> c{pc, sc, wide, nullptr, lds.ct[0]};
+      const typename TileC::Places places(c, c, !p.back, false);
       float enter[kI];
       if constexpr (kOut) {
 #pragma unroll
@@ -914,14 +968,15 @@ __global__ __launch_bounds__(128 * kWaves, 4) void logmel_attn_chunk_kernel(Attn
       bool undecayed = false;   // the state behind the segment's last row is wanted so
 
       auto bring = [&](int64_t row, int held) __attribute__((always_inline)) {
-        tc.load(lc, pc + row * p.cs, sc, !p.back, held, wide);
+        c.base = pc + row * p.cs;
+        tc.load(places, c, c, !p.back, held);
       };
       auto put = [&]() __attribute__((always_inline)) {
         if (wide < kWide) tc.settle(wide);
-        tc.store(lc, nullptr, lds.ct[0]);
+        tc.store(places, c, c);
       };
       auto bad = [&]() __attribute__((always_inline)) {
-        return __any(tc.any_bad()) ? tc.first_bad() : C;
+        return __any(tc.any_bad(false)) ? tc.first_bad(false) : C;
       };
       auto update = [&](int held, bool end) __attribute__((always_inline)) {
         if (!works) return;
@@ -1002,8 +1057,8 @@ __global__ __launch_bounds__(128 * kWaves, 4) void logmel_attn_chunk_kernel(Attn
         float* out = p.state_out ? p.state_out + of_seq : nullptr;
         if (kOut && lo >= hi) {   // an empty sequence
           if (starts && ends && out)
-            cells_of([&](int, int, int c) __attribute__((always_inline)) {
-              out[c] = in ? in[c] : 0.0f;
+            cells_of([&](int, int, int i) __attribute__((always_inline)) {
+              out[i] = in ? in[i] : 0.0f;
             });
           return;
         }
@@ -1093,8 +1148,10 @@ AttnSplit split_of(const logmel_attention_input& in, int64_t dc, int64_t widest,
   const int64_t longest =
       in.max_frames && in.max_frames < in.rows ? in.max_frames : in.rows;
   // a chunk's rows are addressed by 32 bits from its lowest one
-  // in blocks of four values
-  if (longest <= kShort || widest >= (int64_t)1 << 22 || in.head_dk < 4 || in.head_dv < 4) {
+  // in blocks of so many values
+  const int64_t block = in.type == LOGMEL_BF16 ? 8 : 4;
+  if (longest <= kShort || widest >= (int64_t)1 << 22 || in.head_dk < block ||
+      in.head_dv < block) {
     s.how = AttnSplit::kRows;
     return s;
   }
