@@ -200,11 +200,10 @@ __global__ __launch_bounds__(256) void logmel_attn_rows_kernel(AttnJob<T> p, int
 // row meets it,
 //   o_i = beta (gamma sum_{j<=i} lambda^(i-j) (a_i . b_j) c_j + lambda^i a_i E)
 //   E'  = lambda^n E + gamma sum_j lambda^(n-j) b_j c_j^T,
-// four products on the matrix cores. A workgroup of four wavefronts walks the
-// chunks of a sequence's rows and holds 64 columns of E, 16 per wavefront, in
-// its accumulators. The scores of a chunk are formed by the wavefronts
-// together, a few blocks of 16 x 16 each, and exchanged through LDS; every
-// other product is a wavefront's own. The scores come out of the matrix cores
+// four products on the matrix cores. A workgroup walks the chunks of a sequence's
+// rows; half of its wavefronts hold the state, 16 columns each in their
+// accumulators, and the other half form the scores, a few blocks of 16 x 16 each,
+// which they exchange through LDS. The scores come out of the matrix cores
 // with a row i per lane and four neighbouring j in its registers, the state with
 // a column per lane and four neighbouring rows: both are fed back as operands
 // just so, as the order of the summed index is free, if rows of b are taken in
@@ -297,7 +296,9 @@ __device__ __forceinline__ void mma(f32x4& acc, const bf16x8 (&a)[NA], const bf1
 
 // Where the block of four rows (columns) 4 i .. 4 i + 3 stands in a tile whose
 // 16-blocks are read as operands of results that are operands again.
-__device__ __forceinline__ int place(int i) { return 32 * (i >> 3) + 16 * (i & 1) + 4 * ((i >> 1) & 3); }
+__device__ __forceinline__ int place(int i) {
+  return 32 * (i >> 3) + 16 * (i & 1) + 4 * ((i >> 1) & 3);
+}
 
 // Where a tile of rows of kUnits 16-byte units holds unit u of row r: the units
 // of a 128-byte line change places with the row, so that eight lanes that read
@@ -438,8 +439,8 @@ struct Tiles {
       const T* base = second(it) ? y.base : x.base;
       const uint32_t pitch = second(it) ? y.pitch : x.pitch;
       const int width = second(it) ? y.width : x.width;
-      const auto buffer = buffer_of(
-          base, held > 0 ? (uint32_t)(held - 1) * pitch + (uint32_t)width * (uint32_t)sizeof(T) : 0u);
+      const uint32_t row = (uint32_t)width * (uint32_t)sizeof(T);
+      const auto buffer = buffer_of(base, held > 0 ? (uint32_t)(held - 1) * pitch + row : 0u);
       uint32_t to = k.from[it] + (up ? 0u : (uint32_t)(held - 1) * pitch);
       const uint32_t step = up ? pitch : 0u - pitch;
 #pragma unroll
@@ -588,7 +589,8 @@ struct Tiles {
         const uint32_t col = fresh(k.col[it]), col2 = fresh(k.col2[it]);
 #pragma unroll
         for (int c = 0; c < kCols; ++c) {
-          char* to = reinterpret_cast<char*>(cols) + half_below<kRows / 8>(c < 4 ? col : col2, c & 3);
+          char* to =
+              reinterpret_cast<char*>(cols) + half_below<kRows / 8>(c < 4 ? col : col2, c & 3);
           const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
 #pragma unroll
           for (int n = 0; n < kIn; ++n)
@@ -615,10 +617,10 @@ struct Walk {
   int64_t items;
 };
 
-// The sequence that holds rows on both sides of `row`: -1 if there is none.
+// The first offset at or behind row: n_seq + 1 if there is none.
 template <typename T>
 __device__ __forceinline__ int64_t first_from(const AttnJob<T>& p, int64_t row) {
-  int64_t lo = 0, hi = p.n_seq + 1;   // the first offset at or behind row
+  int64_t lo = 0, hi = p.n_seq + 1;
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
     if (p.off[mid] < row)
@@ -628,6 +630,7 @@ __device__ __forceinline__ int64_t first_from(const AttnJob<T>& p, int64_t row) 
   }
   return lo;
 }
+// The sequence that holds rows on both sides of `row`: -1 if there is none.
 template <typename T>
 __device__ __forceinline__ int64_t across(const AttnJob<T>& p, int64_t row) {
   const int64_t i = first_from(p, row);
@@ -654,6 +657,14 @@ template <typename T, int DA, int kWaves>
 constexpr int kChunk =
     sizeof(ChunkLds<T, DA, 16 * kWaves, 64>) <= (kWaves == 4 ? 80 : 160) * 1024 ? 64 : 32;
 
+// Wavefronts that a SIMD holds at a time as LDS has it, four at most.
+template <typename T, int DA, int kWaves>
+constexpr int kHeld = [] {
+  const int lds = (int)sizeof(ChunkLds<T, DA, 16 * kWaves, kChunk<T, DA, kWaves>>);
+  const int held = 160 * 1024 / lds * 2 * kWaves / 4;
+  return held < 4 ? held : 4;
+}();
+
 // A workgroup is kWaves wavefronts that see to the scores and kWaves that hold
 // the state, 16 columns of it each; a wavefront alone waits for half of its time,
 // for LDS and for the other wavefronts. Of a chunk
@@ -663,8 +674,8 @@ constexpr int kChunk =
 // Two barriers: the tiles are written; the scores and the state's part are
 // written and the tiles read.
 template <typename T, int DA, int kWaves, bool kOut>
-__global__ __launch_bounds__(128 * kWaves, 4) void logmel_attn_chunk_kernel(AttnJob<T> p,
-                                                                            Walk walk) {
+__global__ __launch_bounds__(128 * kWaves, (kHeld<T, DA, kWaves>)) void
+logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
   constexpr int kThreads = 64 * kWaves, kWide = 16 * kWaves;   // of each half
   constexpr int kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid, kState = Pieces<T>::kState;
   constexpr int C = kChunk<T, DA, kWaves>, kI = C / 16, kT = C / 32, kS = DA / 32, kU = DA / 16;
@@ -1147,8 +1158,8 @@ AttnSplit split_of(const logmel_attention_input& in, int64_t dc, int64_t widest,
   AttnSplit s{AttnSplit::kSequences, 0, 0};
   const int64_t longest =
       in.max_frames && in.max_frames < in.rows ? in.max_frames : in.rows;
-  // a chunk's rows are addressed by 32 bits from its lowest one
-  // in blocks of so many values
+  // a chunk's rows are addressed by 32 bits from its lowest one, in blocks of so
+  // many values
   const int64_t block = in.type == LOGMEL_BF16 ? 8 : 4;
   if (longest <= kShort || widest >= (int64_t)1 << 22 || in.head_dk < block ||
       in.head_dv < block) {
@@ -1196,7 +1207,8 @@ struct PartSpace {
 template <typename T, int DA, int kWaves>
 hipError_t launch_chunks(const AttnJob<T>& p, const AttnSplit& s, Walk k, bool between,
                          hipStream_t stream) {
-  auto grid = [](int64_t items) { return (unsigned)(items < (1 << 22) ? items : 1 << 22); };
+  // of up to 1024 threads, of which a launch takes fewer than 2^32
+  auto grid = [](int64_t items) { return (unsigned)(items < (1 << 20) ? items : 1 << 20); };
   if (s.how == AttnSplit::kParts) {
     k.part_rows = s.part_rows;
     k.parts = s.parts;
@@ -1314,7 +1326,8 @@ hipError_t launch_attention_backward(const logmel_attention_input& in,
     const int64_t n = in.rows * in.qk_heads * dk;
     const int64_t blocks = (n + 255) / 256;
     if (n)
-      logmel_attn_share_kernel<T><<<(unsigned)(blocks < cus * 8 ? blocks : cus * 8), 256, 0, stream>>>(
+      logmel_attn_share_kernel<T>
+          <<<(unsigned)(blocks < cus * 8 ? blocks : cus * 8), 256, 0, stream>>>(
           part, in.rows, (int)in.qk_heads, share, dk, in.d_seq_offsets, in.n_seq,
           static_cast<T*>(out), stride);
     return hipGetLastError();

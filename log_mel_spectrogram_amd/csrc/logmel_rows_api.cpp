@@ -239,6 +239,8 @@ Operands group_operands(const logmel_group_norm_input& in) {
   o.floats(in.d_bias, 1, false);
   // the workspace's count, for rows by themselves
   if (!o.status() && in.rows > INT64_MAX / 64 / in.channels) o.fault(LOGMEL_ERR_INPUT_TOO_LONG);
+  // and over sequences
+  if (!o.status() && in.n_seq > INT64_MAX / 64 / in.groups) o.fault(LOGMEL_ERR_INPUT_TOO_LONG);
   return o;
 }
 
@@ -381,6 +383,7 @@ int logmel_linear_attention(const logmel_plan* plan, const logmel_attention_inpu
                             int64_t workspace_bytes, void* hip_stream) {
   if (!plan || !in) return LOGMEL_ERR_INVALID_ARGUMENT;
   Operands o = attention_operands(*in);
+  if (o.status()) return o.status();
   o.floats(in->d_state, in->n_seq, head_state(*in), false, -1);
   if (o.status()) return o.status();
   const int state = o.at(in->d_state);
@@ -406,6 +409,7 @@ int logmel_linear_attention_backward(const logmel_plan* plan, const logmel_atten
                                      int64_t workspace_bytes, void* hip_stream) {
   if (!plan || !in || !grad) return LOGMEL_ERR_INVALID_ARGUMENT;
   Operands o = attention_operands(*in);
+  if (o.status()) return o.status();
   o.floats(in->d_state, in->n_seq, head_state(*in), false, -1);
   if (o.status()) return o.status();
   const int64_t need = logmel_attention_workspace(*in, 1, cus_of(plan));

@@ -239,6 +239,22 @@ def test_group_norm_backward_refuses(lm):
     assert _group_back(lm, inp, ws=0x310000) == bad                        # workspace in dx
 
 
+def test_group_norm_refuses_counts_that_overflow(lm):
+    """Sequences whose statistics' count, and the workspace's, pass 64 bits."""
+    inp = _group_in(lm, n_seq=1 << 58)
+    assert _group(lm, inp) == lm.LOGMEL_ERR_INPUT_TOO_LONG
+    assert _group_back(lm, inp) == lm.LOGMEL_ERR_INPUT_TOO_LONG
+    assert lm._group_norm_workspace(FAKE, inp, 0) == -1
+
+
+def test_attention_refuses_counts_that_overflow(lm):
+    """A state whose size passes 64 bits is refused before it is multiplied out."""
+    for kw in (dict(heads=1 << 40, head_dk=1 << 40), dict(head_dk=1 << 62, head_dv=1 << 62)):
+        inp = _attn_in(lm, **kw)
+        assert _attn(lm, inp) != lm.LOGMEL_OK
+        assert lm._linear_attention_workspace(FAKE, inp, 1) == -1
+
+
 def test_binding_refuses_host_tensors(lm):
     import torch
 
