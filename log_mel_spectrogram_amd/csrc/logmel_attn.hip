@@ -637,30 +637,31 @@ __device__ __forceinline__ int64_t across(const AttnJob<T>& p, int64_t row) {
   return i > 0 && i <= p.n_seq && p.off[i] > row ? i - 1 : -1;
 }
 
-template <typename T, int DA, int kWide, int C>
+template <typename T, int DA, int kWide, int C, bool kOut>
 struct ChunkLds {
   static constexpr int kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid;
   static constexpr int kScores = C == 64 ? 6 : 2;
-  uint16_t a[kIn][C * DA];
-  uint16_t b[kIn][C * DA];       // rows as `place` has them
   uint16_t bt[kIn][DA * C];      // columns as `place` has them
   uint16_t ct[kIn][kWide * C];
-  uint16_t p[kMid][kScores][64][8];
-  float from_state[kWide / 16][C / 16][64][4];
   float weight[kWide / 16][C];   // of a chunk's rows as they enter the state, a copy per wavefront
+  uint16_t a[kIn][kOut ? C * DA : 8];
+  uint16_t b[kIn][kOut ? C * DA : 8];   // rows as `place` has them
+  uint16_t p[kMid][kOut ? kScores : 1][kOut ? 64 : 1][8];
+  float from_state[kOut ? kWide / 16 : 1][C / 16][kOut ? 64 : 1][4];
   int bad;
 };
 
 // Rows of a chunk: 64 where a compute unit's LDS holds 16 wavefronts' tiles so
-// (two workgroups of four columns' wavefronts, one of eight), else 32.
-template <typename T, int DA, int kWaves>
+// (two workgroups of four columns' wavefronts, one of eight), else 32. Where only
+// the state is formed that is always so.
+template <typename T, int DA, int kWaves, bool kOut>
 constexpr int kChunk =
-    sizeof(ChunkLds<T, DA, 16 * kWaves, 64>) <= (kWaves == 4 ? 80 : 160) * 1024 ? 64 : 32;
+    sizeof(ChunkLds<T, DA, 16 * kWaves, 64, kOut>) <= (kWaves == 4 ? 80 : 160) * 1024 ? 64 : 32;
 
 // Wavefronts that a SIMD holds at a time as LDS has it, four at most.
-template <typename T, int DA, int kWaves>
+template <typename T, int DA, int kWaves, bool kOut>
 constexpr int kHeld = [] {
-  const int lds = (int)sizeof(ChunkLds<T, DA, 16 * kWaves, kChunk<T, DA, kWaves>>);
+  const int lds = (int)sizeof(ChunkLds<T, DA, 16 * kWaves, kChunk<T, DA, kWaves, kOut>, kOut>);
   const int held = 160 * 1024 / lds * 2 * kWaves / 4;
   return held < 4 ? held : 4;
 }();
@@ -674,16 +675,16 @@ constexpr int kHeld = [] {
 // Two barriers: the tiles are written; the scores and the state's part are
 // written and the tiles read.
 template <typename T, int DA, int kWaves, bool kOut>
-__global__ __launch_bounds__(128 * kWaves, (kHeld<T, DA, kWaves>)) void
+__global__ __launch_bounds__(128 * kWaves, (kHeld<T, DA, kWaves, kOut>)) void
 logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
   constexpr int kThreads = 64 * kWaves, kWide = 16 * kWaves;   // of each half
   constexpr int kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid, kState = Pieces<T>::kState;
-  constexpr int C = kChunk<T, DA, kWaves>, kI = C / 16, kT = C / 32, kS = DA / 32, kU = DA / 16;
+  constexpr int C = kChunk<T, DA, kWaves, kOut>, kI = C / 16, kT = C / 32, kS = DA / 32, kU = DA / 16;
   // of the scores' half (a is not brought where only the state is wanted), and of
   // the state's
   using TilesAB = Tiles<T, C, DA, kThreads, 2, !kOut>;
   using TileC = Tiles<T, C, kWide, kThreads, 1, false>;
-  __shared__ __attribute__((aligned(16))) ChunkLds<T, DA, kWide, C> lds;
+  __shared__ __attribute__((aligned(16))) ChunkLds<T, DA, kWide, C, kOut> lds;
   const int tid = threadIdx.x, lane = tid & 63, n = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % kWaves;
   const bool of_scores = __builtin_amdgcn_readfirstlane(tid >> 6) < kWaves;
@@ -1096,33 +1097,61 @@ logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
 
 // The states between the parts, from those that each part makes: in order (from
 // the last, backwards), the state that enters a part decays through it where
-// its sequence does not end in it. A lane per cell; 32 places are read at a time.
+// its sequence does not end in it. A lane per cell; up to kRun places in a row are
+// a wavefront's, read at once: 16 wavefronts go through theirs from 0, join what
+// leaves them, and go through theirs again from what enters (254 places of 2 x 64 x
+// 64 cells 12.5 us, 62 one after the other by one wavefront).
 template <typename T>
-__global__ __launch_bounds__(64) void logmel_attn_between_kernel(AttnJob<T> p, Walk walk) {
-  constexpr int kBatch = 32;
+__global__ __launch_bounds__(1024) void logmel_attn_between_kernel(AttnJob<T> p, Walk walk) {
+  constexpr int kWaves = 16, kRun = 16;
+  __shared__ float left[kWaves][64];
+  __shared__ int goes[kWaves];   // whether what enters a wavefront's places leaves them
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t cells = (int64_t)p.da * p.dc, all = cells * p.heads;
-  const int64_t x = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (x >= all) return;
-  const Decay whole = decay_of(p.log_decay[x / cells], (float)walk.part_rows);
+  const int64_t x0 = (int64_t)blockIdx.x * 64 + lane, x = x0 < all ? x0 : all - 1;
   const int64_t count = walk.parts - 1;
-  float e = 0.0f;
-  for (int64_t k0 = 0; k0 < count; k0 += kBatch) {
-    float u[kBatch];
-    int how[kBatch];
+  const int run = count >= kWaves * kRun ? kRun : (int)((count + kWaves - 1) / kWaves);
+  const float decay = p.log_decay[x / cells];
+  const Decay whole = decay_of(decay, (float)walk.part_rows);
+  const Decay through = decay_of(decay, (float)(walk.part_rows * run));
+  float enters = 0.0f;   // the state before place k0
+  for (int64_t k0 = 0; k0 < count; k0 += kWaves * run) {
+    float u[kRun];
+    int how[kRun];   // 0 as well where there is no place
+    auto place = [&](int m) {
+      const int64_t k = k0 + wave * run + m;
+      return p.back ? count - 1 - k : k;
+    };
 #pragma unroll
-    for (int m = 0; m < kBatch; ++m) {
-      const int64_t k = k0 + m < count ? k0 + m : count - 1, b = p.back ? count - 1 - k : k;
-      how[m] = walk.through[b];
-      u[m] = walk.between[b * all + x];   // what it holds is used where a sequence lies across
+    for (int m = 0; m < kRun; ++m) {
+      const bool on = m < run && k0 + wave * run + m < count;
+      how[m] = on ? walk.through[place(m)] : 0;
+      u[m] = on ? walk.between[place(m) * all + x] : 0.0f;
     }
+    auto go = [&](float e, auto f) {
 #pragma unroll
-    for (int m = 0; m < kBatch; ++m) {
-      const int64_t k = k0 + m, b = p.back ? count - 1 - k : k;
-      if (k >= count) break;
-      if (how[m] == 0) continue;
-      e = how[m] == 2 ? u[m] + decayed(whole, e) : u[m];
-      walk.between[b * all + x] = e;
+      for (int m = 0; m < kRun; ++m) {
+        if (how[m] == 0) continue;   // what its place holds is not used
+        e = how[m] == 2 ? u[m] + decayed(whole, e) : u[m];
+        f(m, e);
+      }
+      return e;
+    };
+    bool kept = true;
+#pragma unroll
+    for (int m = 0; m < kRun; ++m) kept = kept && (m >= run || how[m] == 2);
+    left[wave][lane] = go(0.0f, [](int, float) {});
+    if (lane == 0) goes[wave] = kept;
+    __syncthreads();
+    float e = enters;
+    for (int w = 0; w < kWaves; ++w) {
+      if (w == wave) go(e, [&](int m, float y) {
+        if (x0 < all) walk.between[place(m) * all + x] = y;
+      });
+      e = goes[w] ? left[w][lane] + decayed(through, e) : left[w][lane];
     }
+    enters = e;
+    __syncthreads();   // for the next places
   }
 }
 
@@ -1153,7 +1182,8 @@ struct AttnSplit {
   int64_t part_rows, parts;
 };
 
-// dc: the widest c of the call's jobs; widest: the longest row stride.
+// dc: the narrowest c of the jobs that share the split; widest: the longest row
+// stride.
 AttnSplit split_of(const logmel_attention_input& in, int64_t dc, int64_t widest, int cus) {
   AttnSplit s{AttnSplit::kSequences, 0, 0};
   const int64_t longest =
@@ -1167,20 +1197,23 @@ AttnSplit split_of(const logmel_attention_input& in, int64_t dc, int64_t widest,
     return s;
   }
   const int64_t chunk = in.type == LOGMEL_BF16 ? 64 : 32;
-  const int64_t lanes = in.heads;                          // workgroups side by side
-  const int64_t slots = 2 * (int64_t)cus;                  // (of eight wavefronts half as many
-                                                           // are resident, which take turns)
-  // in chunks one after the other
+  const int64_t lanes = in.heads;   // workgroups side by side
+  // those that are resident: of four columns' wavefronts two on a compute unit, of
+  // eight one (70,001 x 6 x 40 x 71 fp16 287 us with one part for each, 336 with two
+  // parts that take turns)
+  const int64_t slots = (dc > 64 ? 1 : 2) * (int64_t)cus;
+  // times in chunks one after the other
   const int64_t by_seq = ceil_div(longest, chunk);
-  const int64_t seq_all = ceil_div(in.rows, chunk) * lanes / slots * (dc > 64 ? 2 : 1);
+  const int64_t seq_all = ceil_div(in.rows, chunk) * lanes / slots;
   const double seq_time = (double)(by_seq > seq_all ? by_seq : seq_all);
   const int64_t most = slots / lanes;   // parts in one round of workgroups
   int64_t rows = ceil_div(ceil_div(in.rows, most < 1 ? 1 : most), chunk) * chunk;
   rows = rows < 4 * chunk ? 4 * chunk : rows;
   const int64_t parts = ceil_div(in.rows, rows);
+  // the states between parts are formed in a pass of their own, of about half the
+  // time, and joined
   const double part_time =
-      1.6 * (double)(rows / chunk) * (double)ceil_div(parts * lanes, slots) * (dc > 64 ? 2 : 1) +
-      0.1 * parts + 4.0;
+      1.5 * (double)(rows / chunk) * (double)ceil_div(parts * lanes, slots) + 4.0;
   if (parts > 1 && part_time < seq_time) {
     s.how = AttnSplit::kParts;
     s.part_rows = rows;
@@ -1217,7 +1250,7 @@ hipError_t launch_chunks(const AttnJob<T>& p, const AttnSplit& s, Walk k, bool b
       logmel_attn_chunk_kernel<T, DA, kWaves, false>
           <<<grid(k.items), 128 * kWaves, 0, stream>>>(p, k);
       logmel_attn_between_kernel<T>
-          <<<(unsigned)ceil_div((int64_t)p.heads * p.da * p.dc, 64), 64, 0, stream>>>(p, k);
+          <<<(unsigned)ceil_div((int64_t)p.heads * p.da * p.dc, 64), 1024, 0, stream>>>(p, k);
     }
   } else {
     k.items = p.n_seq * p.heads;
@@ -1307,21 +1340,20 @@ hipError_t launch_attention_backward(const logmel_attention_input& in,
   const T* v = static_cast<const T*>(in.d_v);
   const T* d = static_cast<const T*>(g.d_do);
   const int dk = (int)in.head_dk, dv = (int)in.head_dv;
-  const AttnSplit s =
-      split_of(in, dk > dv ? dk : dv,
-               longest_of({in.q_stride, in.k_stride, in.v_stride, g.do_stride, g.dq_stride,
-                           g.dk_stride, g.dv_stride, share > 1 ? in.heads * dk : 0}),
-               cus);
-  const PartSpace space(s, in, false);
+  const int64_t widest =
+      longest_of({in.q_stride, in.k_stride, in.v_stride, g.do_stride, g.dq_stride, g.dk_stride,
+                  g.dv_stride, share > 1 ? in.heads * dk : 0});
+  const AttnSplit of_q = split_of(in, dk, widest, cus);
+  const AttnSplit of_kv = split_of(in, dk < dv ? dk : dv, widest, cus);   // they share the states
   // the shared heads' parts first, then the splits'
   float* part = share > 1 ? static_cast<float*>(ws) : nullptr;
   float* between = static_cast<float*>(ws) + (part ? in.rows * in.heads * dk : 0);
   // a gradient of q or k: its own rows, or each head's first and then their sums
-  auto shared = [&](AttnJob<T>& p, void* out, int64_t stride) {
+  auto shared = [&](AttnJob<T>& p, const AttnSplit& s, void* out, int64_t stride) {
     p.o = static_cast<T*>(out);
     p.of = part;
     p.os = part ? in.heads * dk : stride;
-    hipError_t e = launch_job(p, s, space, between, true, stream);
+    hipError_t e = launch_job(p, s, PartSpace(s, in, false), between, true, stream);
     if (e != hipSuccess || !part) return e;
     const int64_t n = in.rows * in.qk_heads * dk;
     const int64_t blocks = (n + 255) / 256;
@@ -1341,7 +1373,7 @@ hipError_t launch_attention_backward(const logmel_attention_input& in,
   p.state = in.d_state;
   p.transposed = true;
   p.beta = in.scale, p.gamma = 1.0f;
-  hipError_t e = shared(p, g.d_dq, g.dq_stride);
+  hipError_t e = shared(p, of_q, g.d_dq, g.dq_stride);
   if (e != hipSuccess) return e;
   p.back = true;                  // dk
   p.a = v, p.as = in.v_stride;
@@ -1349,7 +1381,7 @@ hipError_t launch_attention_backward(const logmel_attention_input& in,
   p.c = q, p.cs = in.q_stride;
   p.state = g.d_dstate_out;
   p.beta = 1.0f, p.gamma = in.scale;
-  e = shared(p, g.d_dk, g.dk_stride);
+  e = shared(p, of_kv, g.d_dk, g.dk_stride);
   if (e != hipSuccess) return e;
   p.a = k, p.as = in.k_stride;    // dv, and the initial state's gradient
   p.b = q, p.bs = in.q_stride;
@@ -1362,7 +1394,8 @@ hipError_t launch_attention_backward(const logmel_attention_input& in,
   p.of = nullptr;
   p.o = static_cast<T*>(g.d_dv);
   p.os = g.dv_stride;
-  return launch_job(p, s, space, between, false, stream);   // its states are those of dk
+  // its states are those of dk
+  return launch_job(p, of_kv, PartSpace(of_kv, in, false), between, false, stream);
 }
 
 }  // namespace
@@ -1372,10 +1405,13 @@ int64_t logmel_attention_workspace(const logmel_attention_input& in, int backwar
   using namespace logmel;
   if (!in.n_seq) return 0;
   const int64_t dk = in.head_dk, dv = in.head_dv;
-  const AttnSplit s = split_of(in, backward && dk > dv ? dk : dv, 0, cus);
-  const int64_t share =
-      backward && in.heads > in.qk_heads ? in.rows * in.heads * in.head_dk : 0;
-  return (share + PartSpace(s, in, !backward && in.d_state).all()) * 4;
+  auto parts = [&](int64_t dc) {
+    return PartSpace(split_of(in, dc, 0, cus), in, !backward && in.d_state).all();
+  };
+  if (!backward) return parts(dv) * 4;
+  const int64_t share = in.heads > in.qk_heads ? in.rows * in.heads * dk : 0;
+  const int64_t of_q = parts(dk), of_kv = parts(dk < dv ? dk : dv);
+  return (share + (of_q > of_kv ? of_q : of_kv)) * 4;
 }
 
 hipError_t logmel_launch_attention(const logmel_attention_input& in, void* o, int64_t o_stride,
