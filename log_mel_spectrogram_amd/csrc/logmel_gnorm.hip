@@ -484,23 +484,43 @@ __device__ __forceinline__ void for_pieces(const GroupArgs<T>& p, int64_t i, F&&
 template <int V>
 __device__ __forceinline__ void group_sums(const Columns<V>& k, double (&red)[kWork][2], double& a,
                                            double& b) {
-  red[threadIdx.x][0] = a;
-  red[threadIdx.x][1] = b;
+  const int tid = threadIdx.x;
+  red[tid][0] = a;
+  red[tid][1] = b;
+  __syncthreads();
+  // up to 16 threads a group take every so many-th, then one theirs
+  const int room = k.groups ? kWork / k.groups : 1, per = room < 16 ? room : 16;
+  const int across = k.vecs <= kWork ? k.vg : kWork;
+  a = b = 0.0;
+  if (tid < k.groups * per)
+    for (int e = tid % per; e < k.lanes * across; e += per) {
+      const int t = e / across * k.vecs + tid / per * k.vg + e % across;
+      a += red[t][0];
+      b += red[t][1];
+    }
+  __syncthreads();
+  red[tid][0] = a;
+  red[tid][1] = b;
   __syncthreads();
   a = b = 0.0;
-  if ((int)threadIdx.x < k.groups) {
-    const int across = k.vecs <= kWork ? k.vg : kWork;
-    for (int l = 0; l < k.lanes; ++l)
-      for (int v = 0; v < across; ++v) {
-        const int t = l * k.vecs + threadIdx.x * k.vg + v;
-        a += red[t][0];
-        b += red[t][1];
-      }
-  }
+  if (tid < k.groups)
+    for (int j = 0; j < per; ++j) {
+      a += red[tid * per + j][0];
+      b += red[tid * per + j][1];
+    }
   __syncthreads();
 }
 
 constexpr int kBatch = 8;   // rows of a lane on their way at a time
+
+// f(row, whole) for a lane's rows first, first + step, .. below to, kN at a time:
+// whole (a compile-time constant): all of them are there.
+template <int kN, typename F>
+__device__ __forceinline__ void in_batches(int64_t first, int64_t to, int step, F&& f) {
+  int64_t r = first;
+  for (; r + (kN - 1) * step < to; r += kN * step) f(r, std::true_type{});
+  if (r < to) f(r, std::false_type{});
+}
 
 // Each piece's sum and sum of squares: a lane's kBatch rows at a time are
 // centred on their mean, summed again (what the mean's rounding left) and squared
@@ -518,14 +538,15 @@ __global__ __launch_bounds__(kWork) void logmel_group_stats_kernel(GroupArgs<T> 
     if (lane < k.lanes)
       for (int v = vec; v < k.vecs; v += kWork) {
         const T* x = p.x + ((int64_t)k.g0 * p.width + (int64_t)v * V);
-        for (int64_t r = from + lane; r < to; r += kBatch * k.lanes) {
+        in_batches<kBatch>(from + lane, to, k.lanes, [&](int64_t r, auto whole) {
           Packed<T, V> q[kBatch];
+          const T* xr = x + r * p.xs;
           int n = 0;
 #pragma unroll
           for (int m = 0; m < kBatch; ++m) {
-            const int64_t row = r + m * k.lanes;
-            q[m] = row_load<T, V>(x + (row < to ? row : r) * p.xs);
-            n += row < to;
+            const bool on = whole || r + m * k.lanes < to;
+            q[m] = row_load<T, V>(xr + (on ? m * k.lanes * p.xs : 0));
+            n += on;
           }
           float sum = 0.0f;
 #pragma unroll
@@ -545,7 +566,7 @@ __global__ __launch_bounds__(kWork) void logmel_group_stats_kernel(GroupArgs<T> 
           const double all = (double)(n * V) * (double)mean;
           s += all + (double)rest;
           ss += (double)sq + (all + 2.0 * (double)rest) * (double)mean;
-        }
+        });
       }
     group_sums(k, red, s, ss);
     if ((int)threadIdx.x < k.groups) {
@@ -637,18 +658,20 @@ __global__ __launch_bounds__(kWork) void logmel_group_apply_kernel(GroupArgs<T> 
     for_pieces(p, i0, [&](int64_t i, int64_t from, int64_t to, bool, bool) {
       const float mean = p.stats[(i * p.groups + g) * 2];
       const float root = p.stats[(i * p.groups + g) * 2 + 1];
-      for (int64_t r = from + lane; r < to; r += kRows * k.lanes) {
+      in_batches<kRows>(from + lane, to, k.lanes, [&](int64_t r, auto whole) {
         Packed<T, V> x[kRows], o[kRows];
+        const T* xr = p.x + r * p.xs + c;
+        const T* gr = kGate ? p.gate + r * p.gs + c : nullptr;
+        T* yr = p.y + r * p.ys + c;
 #pragma unroll
         for (int m = 0; m < kRows; ++m) {
-          const int64_t row = r + m * k.lanes < to ? r + m * k.lanes : r;
-          x[m] = row_load<T, V>(p.x + row * p.xs + c);
-          if constexpr (kGate) o[m] = row_load<T, V>(p.gate + row * p.gs + c);
+          const int64_t by = whole || r + m * k.lanes < to ? m * k.lanes : 0;
+          x[m] = row_load<T, V>(xr + by * p.xs);
+          if constexpr (kGate) o[m] = row_load<T, V>(gr + by * p.gs);
         }
 #pragma unroll
         for (int m = 0; m < kRows; ++m) {
-          const int64_t row = r + m * k.lanes;
-          if (row >= to) break;
+          if (!whole && r + m * k.lanes >= to) break;
           float y[V];
 #pragma unroll
           for (int j = 0; j < V; ++j) {
@@ -659,9 +682,9 @@ __global__ __launch_bounds__(kWork) void logmel_group_apply_kernel(GroupArgs<T> 
               y[j] *= gt * Gate<T>::sigmoid(gt);
             }
           }
-          row_store(p.y + row * p.ys + c, y);
+          row_store(yr + m * k.lanes * p.ys, y);
         }
-      }
+      });
     });
   }
 }
@@ -733,14 +756,17 @@ __global__ __launch_bounds__(kWork) void logmel_group_back_sums_kernel(GroupArgs
       double d1[V], d2[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) d1[j] = d2[j] = 0.0;
-      for (int64_t r = from + lane; r < to; r += kRows * k.lanes) {
+      in_batches<kRows>(from + lane, to, k.lanes, [&](int64_t r, auto whole) {
         Packed<T, V> x[kRows], o[kRows], d[kRows];
+        const T* xr = p.x + r * p.xs + c;
+        const T* dr = p.dy + r * p.dys + c;
+        const T* gr = kGate ? p.gate + r * p.gs + c : nullptr;
 #pragma unroll
         for (int m = 0; m < kRows; ++m) {
-          const int64_t row = r + m * k.lanes < to ? r + m * k.lanes : r;
-          x[m] = row_load<T, V>(p.x + row * p.xs + c);
-          d[m] = row_load<T, V>(p.dy + row * p.dys + c);
-          if constexpr (kGate) o[m] = row_load<T, V>(p.gate + row * p.gs + c);
+          const int64_t by = whole || r + m * k.lanes < to ? m * k.lanes : 0;
+          x[m] = row_load<T, V>(xr + by * p.xs);
+          d[m] = row_load<T, V>(dr + by * p.dys);
+          if constexpr (kGate) o[m] = row_load<T, V>(gr + by * p.gs);
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -749,14 +775,14 @@ __global__ __launch_bounds__(kWork) void logmel_group_back_sums_kernel(GroupArgs
           for (int m = 0; m < kRows; ++m) {
             const Back<T, kGate> t((float)x[m].v[j], kGate ? (float)o[m].v[j] : 0.0f,
                                    (float)d[m].v[j], mean, root, w[j], b[j], p.silu);
-            const bool on = r + m * k.lanes < to;
+            const bool on = whole || r + m * k.lanes < to;
             a1 = on ? __builtin_fmaf(t.dn, t.xh, a1) : a1;
             a2 = on ? a2 + t.dn : a2;
           }
           d1[j] += (double)a1;
           d2[j] += (double)a2;
         }
-      }
+      });
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         s1 += (double)w[j] * d2[j];   // of q
@@ -830,19 +856,21 @@ __global__ __launch_bounds__(kWork) void logmel_group_dx_kernel(GroupArgs<T> p) 
       const int64_t at = (i * p.groups + g) * 2;
       const float mean = p.stats[at], root = p.stats[at + 1];
       const float m1 = p.sums[at], m2 = p.sums[at + 1];
-      for (int64_t r = from + lane; r < to; r += kRows * k.lanes) {
+      in_batches<kRows>(from + lane, to, k.lanes, [&](int64_t r, auto whole) {
         Packed<T, V> x[kRows], o[kRows], d[kRows];
+        const T* xr = p.x + r * p.xs + c;
+        const T* dr = p.dy + r * p.dys + c;
+        const T* gr = kGate ? p.gate + r * p.gs + c : nullptr;
 #pragma unroll
         for (int m = 0; m < kRows; ++m) {
-          const int64_t row = r + m * k.lanes < to ? r + m * k.lanes : r;
-          x[m] = row_load<T, V>(p.x + row * p.xs + c);
-          d[m] = row_load<T, V>(p.dy + row * p.dys + c);
-          if constexpr (kGate) o[m] = row_load<T, V>(p.gate + row * p.gs + c);
+          const int64_t by = whole || r + m * k.lanes < to ? m * k.lanes : 0;
+          x[m] = row_load<T, V>(xr + by * p.xs);
+          d[m] = row_load<T, V>(dr + by * p.dys);
+          if constexpr (kGate) o[m] = row_load<T, V>(gr + by * p.gs);
         }
 #pragma unroll
         for (int m = 0; m < kRows; ++m) {
-          const int64_t row = r + m * k.lanes;
-          if (row >= to) break;
+          if (!whole && r + m * k.lanes >= to) break;
           float dx[V], dg[V];
 #pragma unroll
           for (int j = 0; j < V; ++j) {
@@ -851,10 +879,10 @@ __global__ __launch_bounds__(kWork) void logmel_group_dx_kernel(GroupArgs<T> p) 
             dx[j] = root * __builtin_fmaf(-t.xh, m2, __builtin_fmaf(t.dn, w[j], -m1));
             dg[j] = t.dgate;
           }
-          row_store(p.dx + row * p.dxs + c, dx);
-          if constexpr (kGate) row_store(p.dgate + row * p.dgs + c, dg);
+          row_store(p.dx + r * p.dxs + c + m * k.lanes * p.dxs, dx);
+          if constexpr (kGate) row_store(p.dgate + r * p.dgs + c + m * k.lanes * p.dgs, dg);
         }
-      }
+      });
     });
   }
 }
