@@ -679,7 +679,8 @@ __global__ __launch_bounds__(128 * kWaves, (kHeld<T, DA, kWaves, kOut>)) void
 logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
   constexpr int kThreads = 64 * kWaves, kWide = 16 * kWaves;   // of each half
   constexpr int kIn = Pieces<T>::kIn, kMid = Pieces<T>::kMid, kState = Pieces<T>::kState;
-  constexpr int C = kChunk<T, DA, kWaves, kOut>, kI = C / 16, kT = C / 32, kS = DA / 32, kU = DA / 16;
+  constexpr int C = kChunk<T, DA, kWaves, kOut>;
+  constexpr int kI = C / 16, kT = C / 32, kS = DA / 32, kU = DA / 16;
   // of the scores' half (a is not brought where only the state is wanted), and of
   // the state's
   using TilesAB = Tiles<T, C, DA, kThreads, 2, !kOut>;
