@@ -10,8 +10,8 @@ of 2, the products it enters). The products are summed over dk values, over the
 64 rows of a chunk and over dk values again: that many additions, and 8 for the
 scale and the sums' joins. Products on the matrix cores take their operands in
 bf16 pieces. Rows of 16 bits: what is not a row operand itself (a weighted row,
-a score, the state) is two pieces, which leave 2^-18 of it, 64 units of 2^-24,
-for each of the three such roundings that a term meets; an fp16 row is two
+a score, the state) is two pieces or three, which leave up to 2^-18 of it, 64
+units of 2^-24, for each of the three such roundings that a term meets; an fp16 row is two
 pieces too, and the product of two second pieces is left out, 64 more for each
 of the three products. fp32 rows: three pieces each, which leave 2^-26 and drop
 products below 2^-25: a unit for each of six.
