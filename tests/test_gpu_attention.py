@@ -342,3 +342,53 @@ def test_attention_refusals_of_the_binding(env):
                dict(v=torch.zeros((4, 16), device=dev, requires_grad=True))):
         with pytest.raises((ValueError, TypeError, RuntimeError)):
             call(**kw)
+
+
+def chain(a, b, c, off, g, scale):
+    """o_i = scale a_i S_i of one head row by row in fp64, with its bound: the
+    formula over absolute values A, 8 + 2 DK + 64 + 6 roundings for the sums and
+    pieces, and 6 + 2 |g| for each of a term's i - j + 1 steps, whose sum over the
+    terms is that of the state R_i = lambda R_{i-1} + |S|_i."""
+    u, lam = 2.0 ** -24, np.exp(g)
+    out, tol, last = np.zeros_like(c), np.zeros_like(c), []
+    for lo, hi in zip(off[:-1], off[1:]):
+        s = np.zeros((a.shape[1], c.shape[1]))
+        p, r = s.copy(), s.copy()
+        for t in range(lo, hi):
+            x = np.outer(b[t], c[t])
+            s = lam * s + x
+            p = lam * p + np.abs(x)
+            r = lam * r + p
+            out[t] = scale * (a[t] @ s)
+            m = np.abs(a[t])
+            tol[t] = scale * u * ((78 + 2 * a.shape[1]) * (m @ p) + (6 + 2 * abs(g)) * (m @ r))
+        last.append(s)
+    return out, tol + u * np.abs(out), np.stack(last)
+
+
+def test_more_places_between_parts_than_one_pass_takes(env):
+    """One head and few long sequences: several hundred parts."""
+    lm, plan, torch = env
+    off = np.array([0, 41000, 41000, 70001], np.int64)
+    rng = np.random.default_rng(5)
+    q, k, v, do = (rng.normal(size=(70001, 8)).astype(np.float32) for _ in range(4))
+    g = np.float32(-2.0 ** -9)
+    scale = 0.25
+    dev = torch.device("cuda", 0)
+    tq, tk, tv, td, tg, to = (torch.from_numpy(np.asarray(x)).to(dev)
+                              for x in (q, k, v, do, g.reshape(1), off))
+    o = torch.empty_like(tv)
+    end = torch.empty(3, 1, 8, 8, device=dev)
+    lm.logmel_linear_attention(plan, tq, tk, tv, tg, to, scale=scale, out=o, state_out=end)
+    _, _, dv, _ = lm.logmel_linear_attention_backward(plan, td, tq, tk, tv, tg, to, scale=scale)
+    f = [x.astype(np.float64) for x in (q, k, v, do)]
+    want, tol, last = chain(*f[:3], off, float(g), scale)
+    got = o.cpu().numpy()
+    assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / tol)
+    assert (end[1] == 0).all()
+    # 512 steps of memory, 6 + 2 |g| and less than 2 more roundings for each
+    np.testing.assert_allclose(end[:, 0].cpu().numpy(), last, rtol=0, atol=float(
+        2.0 ** -24 * 8 * 512 * np.abs(last).max()))
+    want, tol, _ = chain(f[1][::-1], f[0][::-1], f[3][::-1], 70001 - off[::-1], float(g), scale)
+    got = dv.cpu().numpy()[::-1]
+    assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / tol)
