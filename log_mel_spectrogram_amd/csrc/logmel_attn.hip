@@ -693,7 +693,10 @@ logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) % kWaves;
   const bool of_scores = __builtin_amdgcn_readfirstlane(tid >> 6) < kWaves;
   const int64_t cells = (int64_t)p.da * p.dc;
-  if (tid == 0) lds.bad = C;
+  if constexpr (kOut) {
+    if (tid == 0) lds.bad = C;
+    __syncthreads();   // before another wavefront marks a row in it
+  }
 
   // A lane's operand: unit 4 s + g of row 16 i + n of a tile of rows, or of columns
   const uint32_t row_base = 16 * unit_at<DA / 8, false>(n, g);

@@ -392,3 +392,41 @@ def test_more_places_between_parts_than_one_pass_takes(env):
     want, tol, _ = chain(f[1][::-1], f[0][::-1], f[3][::-1], 70001 - off[::-1], float(g), scale)
     got = dv.cpu().numpy()[::-1]
     assert (np.abs(got - want) <= tol).all(), np.max(np.abs(got - want) / tol)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("dk,dv", [(32, 64), (64, 128)])
+def test_attention_first_chunk_marks_of_every_wavefront(env, dtype, dk, dv):
+    """A value that is not finite in a workgroup's very first chunk, in the
+    columns that each wavefront brings in turn: the rows before it keep every
+    bit. Each sequence is a workgroup's and has one such value."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say(f"attention first chunk {dtype} {dk} x {dv}")
+    dt = getattr(torch, dtype)
+    n, length = 512, 40
+    gen = torch.Generator(device=dev).manual_seed(21)
+    q, k = (torch.randn((n * length, dk), generator=gen, device=dev).to(dt) for _ in range(2))
+    v = torch.randn((n * length, dv), generator=gen, device=dev).to(dt)
+    off = torch.arange(n + 1, device=dev) * length
+    g = torch.tensor([-0.1], device=dev)
+
+    def call():
+        return lm.logmel_linear_attention(plan, q, k, v, g, off, max_frames=length)
+
+    whole = call()
+    seq = torch.arange(n, device=dev)
+    at = 1 + seq % (length - 1)                     # the row in its sequence
+    row = seq * length + at
+    before = (torch.arange(length, device=dev) < at[:, None]).reshape(-1)
+    for x, wide in ((k, dk), (v, dv)):
+        col = (seq * 5) % wide                      # every column, in every block of rows
+        keep = x[row, col].clone()
+        x[row, col] = float("nan")
+        got = call()
+        x[row, col] = keep
+        assert torch.equal(got[before], whole[before])
+        behind = got[~before] if x is k else got[torch.arange(n * length, device=dev)[~before],
+                                                 col.repeat_interleave(length)[~before]]
+        assert torch.isnan(behind).all()
+    assert torch.equal(call(), whole)
