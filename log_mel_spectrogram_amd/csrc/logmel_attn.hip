@@ -618,6 +618,16 @@ struct Walk {
   int64_t items;
 };
 
+// Rows of a chunk of most C, of the `left` that there are: none where left is
+// below 0, as far below as offsets that decrease make it.
+template <int C>
+__host__ __device__ constexpr int held_of(int64_t left) {
+  return (int)(left < 0 ? 0 : left < C ? left : C);
+}
+static_assert(held_of<64>(-((int64_t)1 << 32) + 5) == 0 && held_of<64>(-((int64_t)1 << 40)) == 0);
+static_assert(held_of<64>(0) == 0 && held_of<64>(5) == 5 && held_of<64>(64) == 64 &&
+              held_of<64>(((int64_t)1 << 32) + 5) == 64);
+
 // The first offset at or behind row: n_seq + 1 if there is none.
 template <typename T>
 __device__ __forceinline__ int64_t first_from(const AttnJob<T>& p, int64_t row) {
@@ -717,9 +727,7 @@ logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
     auto lowest = [&](int64_t at, int held) {
       return held <= 0 ? lo : p.back ? hi - at - held : lo + at;
     };
-    auto held_at = [&](int64_t at) {   // not above 0 behind the last
-      return (int)(rows - at < C ? rows - at : C);
-    };
+    auto held_at = [&](int64_t at) { return held_of<C>(rows - at); };   // 0 behind the last
     bring(lowest(0, held_at(0)), held_at(0));
     for (int64_t at = 0; at < rows;) {
       int held = held_at(at);
