@@ -218,6 +218,11 @@ __global__ __launch_bounds__(256) void logmel_attn_rows_kernel(AttnJob<T> p, int
 // which is fp32 for every type. Products of pieces whose places sum to the
 // count are left out: 2^-18 or 2^-26 of the whole as well.
 //
+// bf16 rounds the largest fp32 values to infinity. The state is held at half its
+// size, which keeps it and the rows that enter it below that at no cost; the pieces of
+// fp32 rows and of their scores are held below it one by one (`cut`). Scores of 2-byte
+// rows are not: a result of fp32 may be lost where one is within 2^-9 of overflow.
+//
 // Causality is exact, for NaN and infinities too: a score above the diagonal is
 // left out by a select, and a chunk with a value of b or c that is not finite
 // is cut short before its row, which starts a chunk of its own.
@@ -260,14 +265,19 @@ __device__ __forceinline__ float high(uint32_t v) {
   return __builtin_bit_cast(float, v & 0xffff0000u);
 }
 
-// M values as N pieces each, packed in pairs; x keeps the rest.
-template <int N, int M>
+// M values as N pieces each, packed in pairs; x keeps the rest. kLarge: values from
+// 0x1.ffp127 on, which bf16 rounds to infinity, are there too: their first piece is
+// bf16's largest, with which three pieces hold them exactly as well.
+template <bool kLarge, int N, int M>
 __device__ __forceinline__ void cut(float (&x)[M], uint32_t (&piece)[N][M / 2]) {
+  static_assert(!kLarge || N > 1);
+  auto held = [](float v) { return __builtin_amdgcn_fmed3f(v, -0x1.fep127f, 0x1.fep127f); };
 #pragma unroll
   for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int i = 0; i < M / 2; ++i) {
-      piece[n][i] = pack(x[2 * i], x[2 * i + 1]);
+      piece[n][i] = kLarge && n == 0 ? pack(held(x[2 * i]), held(x[2 * i + 1]))
+                                     : pack(x[2 * i], x[2 * i + 1]);
       if (n + 1 < N) {
         x[2 * i] -= low(piece[n][i]);
         x[2 * i + 1] -= high(piece[n][i]);
@@ -566,7 +576,7 @@ struct Tiles {
           float f[kCols];
 #pragma unroll
           for (int j = 0; j < kCols; ++j) f[j] = (float)z.v[j];
-          cut<kIn, kCols>(f, w[r]);
+          cut<sizeof(T) == 4, kIn, kCols>(f, w[r]);
         }
       }
       uint16_t* rows = second(it) ? y.rows : x.rows;
@@ -608,7 +618,8 @@ struct Tiles {
 // part_rows packed rows each, whatever sequences they hold. Between parts b and
 // b + 1 stands state b of `between`, as the next row of the sequence there meets
 // it; kept: the initial state of the sequence that starts in part b and leaves
-// it, where state_out may overwrite it.
+// it, as its first row meets it, where state_out may overwrite it. Both at the size at
+// which the chunks hold them.
 struct Walk {
   int64_t part_rows, parts;
   float* between;
@@ -871,7 +882,7 @@ logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
               if (m != 1) x[r] = after + r <= 0 ? x[r] : 0.0f;
             }
             uint32_t piece[kMid][2];
-            cut<kMid, 4>(x, piece);
+            cut<sizeof(T) == 4, kMid, 4>(x, piece);
             const int f = bi < 2 ? bi : 2 * bi - 2 + t;
 #pragma unroll
             for (int k = 0; k < kMid; ++k)
@@ -953,10 +964,13 @@ logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
       const uint32_t sc = (uint32_t)(p.cs * sizeof(T));
       TileAt<T> c{pc, sc, wide, nullptr, lds.ct[0]};
       const typename TileC::Places places(c, c, !p.back, false);
+      // the state's part that is held: half of it (a scale that would pass fp32 when
+      // doubled takes all of it)
+      const float part = __builtin_fabsf(p.beta) < 1e38f ? 0.5f : 1.0f, whole_of = 1.0f / part;
       float enter[kI];
       if constexpr (kOut) {
 #pragma unroll
-        for (int i = 0; i < kI; ++i) enter[i] = p.beta * power(16 * i + n);
+        for (int i = 0; i < kI; ++i) enter[i] = p.beta * whole_of * power(16 * i + n);
       }
       // of the rows that enter the state, `left` rows before the next chunk's first
       Decay whole;
@@ -965,7 +979,8 @@ logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
         if (to == left) return;
         left = to;
         whole = decay_of(decay, (float)to);
-        if (lane < C) lds.weight[wave][lane] = lane <= to ? p.gamma * power(to - lane) : 0.0f;
+        if (lane < C)
+          lds.weight[wave][lane] = lane <= to ? p.gamma * (part * power(to - lane)) : 0.0f;
       };
 
       f32x4 w[kU];
@@ -988,8 +1003,8 @@ logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
             w[u][r] = decayed(d, s[i]);
           });
       };
-      auto store_state = [&](float* s) __attribute__((always_inline)) {
-        cells_of([&](int u, int r, int i) __attribute__((always_inline)) { s[i] = w[u][r]; });
+      auto store_state = [&](float* s, float by) __attribute__((always_inline)) {
+        cells_of([&](int u, int r, int i) __attribute__((always_inline)) { s[i] = w[u][r] * by; });
       };
       TileC tc;
       bool undecayed = false;   // the state behind the segment's last row is wanted so
@@ -1019,7 +1034,7 @@ logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = w[2 * s + e / 4][e & 3];
             uint32_t piece[kMid][4];
-            cut<kMid, 8>(x, piece);
+            cut<false, kMid, 8>(x, piece);
             bf16x8 fw[kMid];
 #pragma unroll
             for (int k = 0; k < kMid; ++k) fw[k] = frag(piece[k]);
@@ -1062,7 +1077,7 @@ logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
             x[e] *= e < 4 ? w0[e & 3] : w1[e & 3];
           }
           uint32_t piece[kState][4];
-          cut<kState, 8>(x, piece);
+          cut<false, kState, 8>(x, piece);
           bf16x8 fw[kState];
 #pragma unroll
           for (int k = 0; k < kState; ++k) fw[k] = frag(piece[k]);
@@ -1076,7 +1091,9 @@ logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
           }
         }
       };
-      const Decay one = {1.0f, 0.0f}, lambda = decay_of(decay, 1.0f);
+      // of a sequence's own initial state, before its first row and undecayed
+      const Decay lambda = decay_of(decay, 1.0f);
+      const Decay first = {part * lambda.hi, part * lambda.lo}, last = {part, 0.0f};
       each([&](int64_t i, int64_t lo, int64_t hi, bool starts, bool ends)
                __attribute__((always_inline)) {
         const int64_t of_seq = (i * p.heads + h) * cells;
@@ -1097,14 +1114,14 @@ logmel_attn_chunk_kernel(AttnJob<T> p, Walk walk) {
         const float* from = own ? (put_by ? slot(walk.kept, which) : in)
                             : kOut ? slot(walk.between, p.back ? which : which - 1)
                                    : nullptr;
-        load_state(from, own && !put_by && !p.back ? lambda : one);
-        if (!kOut && own && walk.kept) store_state(slot(walk.kept, which));
+        load_state(from, !own || put_by ? Decay{1.0f, 0.0f} : p.back ? last : first);
+        if (!kOut && own && walk.kept) store_state(slot(walk.kept, which), 1.0f);
         undecayed = kOut && !p.back && ends;
         chunks(lo, hi, bring, put, bad, update, [](int64_t, int) {});
         if constexpr (!kOut)
-          store_state(slot(walk.between, p.back ? which - 1 : which));
+          store_state(slot(walk.between, p.back ? which - 1 : which), 1.0f);
         else if ((p.back ? starts : ends) && out)
-          store_state(out);
+          store_state(out, whole_of);
       });
     }
   }

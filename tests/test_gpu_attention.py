@@ -430,3 +430,76 @@ def test_attention_first_chunk_marks_of_every_wavefront(env, dtype, dk, dv):
                                                  col.repeat_interleave(length)[~before]]
         assert torch.isnan(behind).all()
     assert torch.equal(call(), whole)
+
+
+LARGEST = float(np.finfo(np.float32).max)
+NEAR = [(k, "float32") for k in ("q", "k", "v", "do", "score")]
+NEAR += [(k, d) for k in ("state", "dstate_out") for d in DTYPES if (k, d) != ("dstate_out", "float16")]
+
+
+@pytest.mark.parametrize("lens,max_frames", [([11, 0, 9], 11), ([150, 0, 77], 150),
+                                             ([1300, 0, 900], 0)])
+@pytest.mark.parametrize("dk,dv", [(32, 48), (72, 80)])
+@pytest.mark.parametrize("kind,dtype", NEAR)
+def test_attention_values_near_the_largest(env, kind, dtype, dk, dv, lens, max_frames):
+    """fp32's largest values, and its lowest as masks have it, are values like
+    others: in a row operand, in a score, and in a state of rows of any type.
+    The rest is small, so that results are finite, and rows before a large one
+    keep every bit."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say(f"attention near the largest {kind} {dtype} {dk} x {dv} {lens}")
+    dt = getattr(torch, dtype)
+    heads, rows, n = 2, sum(lens), len(lens)
+    rng = np.random.default_rng(22)
+    off = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+
+    def small(*shape):
+        return torch.from_numpy(rng.normal(size=shape) / 64).to(dev)
+
+    t = dict(q=small(rows, heads * dk), k=small(rows, heads * dk), v=small(rows, heads * dv),
+             do=small(rows, heads * dv))
+    t = {name: x.to(dt) for name, x in t.items()}
+    state, dso = (small(n, heads, dk, dv).float() for _ in range(2))
+    g = torch.tensor([0.0, -0.05], device=dev)
+    # a 2-byte result of such a state is finite where the scale makes it so
+    scale = 1.0 if dtype == "float32" else 2.0 ** -120
+    args = dict(qk_heads=heads, scale=scale, max_frames=max_frames)
+    off_d = torch.from_numpy(off).to(dev)
+
+    def call():
+        so = torch.empty_like(state)
+        o = lm.logmel_linear_attention(plan, t["q"], t["k"], t["v"], g, off_d, state=state,
+                                       state_out=so, **args)
+        dq, dkk, dvv, ds = lm.logmel_linear_attention_backward(
+            plan, t["do"], t["q"], t["k"], t["v"], g, off_d, state=state, dstate_out=dso, **args)
+        return dict(o=o, state_out=so, dq=dq, dk=dkk, dv=dvv, dstate=ds)
+
+    first = call()
+    at = [lens[0] - 6, rows - 3]   # a row of each sequence, others before and behind it
+    if kind in ("state", "dstate_out"):
+        x = state if kind == "state" else dso
+        x[..., ::2] = -LARGEST
+        x[..., 1::2] = LARGEST
+    elif kind == "score":
+        t["q"][at], t["k"][:, 5] = 0.0, 1.0
+        t["q"][at, 5] = -LARGEST
+    else:
+        t[kind][at, : t[kind].shape[1] // 2] = -LARGEST
+        t[kind][at, -1] = LARGEST
+    got = call()
+    val, tol = attn_ref.attention(*(host(t[x]) for x in ("q", "k", "v")), host(g), off, heads,
+                                  scale, host(state), host(t["do"]), host(dso), dtype=dtype)
+    # fp32 sums may overflow on the way, in any order, where the terms' absolute
+    # values add up to more than fp32 has (of the scores, those of 1300 rows do)
+    most, _ = attn_ref.attention(*(np.abs(host(t[x])) for x in ("q", "k", "v")), host(g), off,
+                                 heads, scale, np.abs(host(state)), np.abs(host(t["do"])),
+                                 np.abs(host(dso)), dtype=dtype)
+    for name, x in got.items():
+        with np.errstate(over="ignore"):
+            fits = np.isfinite(most[name].astype(np.float32))
+        assert fits.mean() > 0.5, name
+        check(x[torch.from_numpy(fits).to(dev)], val[name][fits], tol[name][fits], name)
+    if kind == "v":
+        for lo, hi in ((0, at[0]), (lens[0], at[1])):
+            assert torch.equal(got["o"][lo:hi], first["o"][lo:hi])
