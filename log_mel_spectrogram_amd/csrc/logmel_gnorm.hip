@@ -46,6 +46,8 @@ struct GroupArgs {
   // over sequences
   double* pieces;       // [parts][2][groups][2]: of the sequence that enters a part, of the one
                         // that starts in it and leaves it
+  double* wide;         // [parts][2][channels]: `part` while its pieces are added, of groups
+                        // of more vectors than a workgroup has lanes
   int64_t part_rows, parts;
 };
 
@@ -723,31 +725,35 @@ struct Back {
 };
 
 // Each part's sums of dn xh and dn, channel by channel, and weighted those of
-// its pieces' groups. A lane's rows are summed in fp32 eight at a time, then in
-// fp64.
-template <typename T, bool kGate, int V>
+// its pieces' groups. A lane's rows are summed in fp32 four at a time, then in
+// fp64. kWide: of groups of more vectors than a workgroup has lanes, which go through
+// theirs 256 at a time; the sums over a part's pieces, which may be as many as its
+// rows, are in memory, unless one piece is the whole part.
+template <typename T, bool kGate, int V, bool kWide>
 __global__ __launch_bounds__(kWork) void logmel_group_back_sums_kernel(GroupArgs<T> p) {
   constexpr int kRows = 4;
   __shared__ double red[kWork][2];
   const Columns<V> k(p.groups, p.width);
   const int64_t i0 = first_piece(p);
-  const bool wide = k.vecs > kWork;
   const int vec = threadIdx.x % (k.vecs < kWork && k.vecs ? k.vecs : kWork);
   const int lane = k.vecs < kWork && k.vecs ? threadIdx.x / k.vecs : 0;
-  // wide groups: their vectors 256 at a time, whose parts go to memory by pieces
-  const int rounds = wide ? (k.vecs + kWork - 1) / kWork : 1;
-  double p1[V], p2[V];   // over the part
+  const int rounds = kWide ? (k.vecs + kWork - 1) / kWork : 1;
+  double p1[V], p2[V];   // over the part, if not wide
+  bool some = false, alone = false;   // pieces before; one that is the whole part
 #pragma unroll
   for (int j = 0; j < V; ++j) p1[j] = p2[j] = 0.0;
   auto part_at = [&](int which, int v) {
     return p.part + (((int64_t)blockIdx.x * 2 + which) * p.channels +
                      (int64_t)k.g0 * p.width + (int64_t)v * V);
   };
-  if (p.part && wide)
-    for (int v = vec; v < k.vecs; v += kWork)
-      for (int j = 0; j < V; ++j) part_at(0, v)[j] = part_at(1, v)[j] = 0.0f;
+  auto wide_at = [&](int which, int v) {
+    return p.wide + (((int64_t)blockIdx.x * 2 + which) * p.channels +
+                     (int64_t)k.g0 * p.width + (int64_t)v * V);
+  };
   for_pieces(p, i0, [&](int64_t i, int64_t from, int64_t to, bool starts, bool ends) {
     double s1 = 0.0, s2 = 0.0;
+    if (kWide)
+      alone = to - from == p.part_rows || (from == (int64_t)blockIdx.x * p.part_rows && to == p.rows);
     for (int round = 0; round < rounds; ++round) {
       const int v = vec + round * kWork;
       if (lane >= k.lanes || v >= k.vecs) continue;
@@ -802,14 +808,19 @@ __global__ __launch_bounds__(kWork) void logmel_group_back_sums_kernel(GroupArgs
       for (int j = 0; j < V; ++j) {
         s1 += (double)w[j] * d2[j];   // of q
         s2 += (double)w[j] * d1[j];   // of q xh
-        if (wide && p.part) {
-          part_at(0, v)[j] += (float)d1[j];
-          part_at(1, v)[j] += (float)d2[j];
+        if (!kWide) {
+          p1[j] += d1[j];
+          p2[j] += d2[j];
+        } else if (p.part && alone) {
+          part_at(0, v)[j] = (float)d1[j];
+          part_at(1, v)[j] = (float)d2[j];
+        } else if (p.part) {
+          wide_at(0, v)[j] = some ? wide_at(0, v)[j] + d1[j] : d1[j];
+          wide_at(1, v)[j] = some ? wide_at(1, v)[j] + d2[j] : d2[j];
         }
-        p1[j] += d1[j];
-        p2[j] += d2[j];
       }
     }
+    some = true;
     group_sums(k, red, s1, s2);
     if ((int)threadIdx.x < k.groups) {
       const int g = k.g0 + threadIdx.x;
@@ -825,7 +836,15 @@ __global__ __launch_bounds__(kWork) void logmel_group_back_sums_kernel(GroupArgs
       }
     }
   });
-  if (!p.part || wide) return;
+  if (!p.part) return;
+  if constexpr (kWide) {
+    for (int v = vec; v < k.vecs && !alone; v += kWork)
+      for (int which = 0; which < 2; ++which)
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          part_at(which, v)[j] = some ? (float)wide_at(which, v)[j] : 0.0f;
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     __syncthreads();
@@ -1003,6 +1022,9 @@ int seq_values(const logmel_group_norm_input& in) {
   const int v = in.type == LOGMEL_F32 ? 4 : 8;
   return in.channels / in.groups % v ? 1 : v;
 }
+bool seq_wide(const logmel_group_norm_input& in) {
+  return in.channels / in.groups / seq_values(in) > kWork;
+}
 int64_t part_rows_of(const logmel_group_norm_input& in, int cus) {
   const int64_t sets =
       group_sets((int)in.groups, (int)(in.channels / in.groups), seq_values(in));
@@ -1010,17 +1032,19 @@ int64_t part_rows_of(const logmel_group_norm_input& in, int cus) {
   return rows < 64 ? 64 : rows;
 }
 
-// Where a call over sequences has what in its workspace: pieces first.
+// Where a call over sequences has what in its workspace: pieces first, then in this
+// order.
 struct SeqSpace {
-  int64_t parts, pieces, stats, part, bytes;
+  int64_t parts, pieces, stats, wide, part, bytes;
 };
 SeqSpace seq_space(const logmel_group_norm_input& in, bool backward, int cus) {
   SeqSpace s{};
   s.parts = ceil_div(in.rows, part_rows_of(in, cus));
   s.pieces = s.parts * in.groups * 32;
   s.stats = in.n_seq * in.groups * 8;   // forward: statistics nobody asked for; backward: sums
+  s.wide = backward && seq_wide(in) ? s.parts * in.channels * 16 : 0;
   s.part = backward ? s.parts * in.channels * 8 : 0;
-  s.bytes = s.pieces + s.stats + s.part;
+  s.bytes = s.pieces + s.stats + s.wide + s.part;
   return s;
 }
 
@@ -1124,7 +1148,7 @@ hipError_t logmel_launch_group_backward(const logmel_group_norm_input& in, const
   } else if (in.n_seq) {
     const SeqSpace s = seq_space(in, true, cus);
     char* at = static_cast<char*>(ws);
-    part = reinterpret_cast<float*>(at + s.pieces + s.stats);
+    part = reinterpret_cast<float*>(at + s.pieces + s.stats + s.wide);
     parts = s.parts;
     if (parts)
       seq_dispatch(in, [&](auto zero, auto gate, auto values) {
@@ -1134,11 +1158,16 @@ hipError_t logmel_launch_group_backward(const logmel_group_norm_input& in, const
         p.pieces = reinterpret_cast<double*>(at);
         p.sums = reinterpret_cast<float*>(at + s.pieces);
         p.part = params ? part : nullptr;
+        p.wide = reinterpret_cast<double*>(at + s.pieces + s.stats);
         p.part_rows = part_rows_of(in, cus);
         p.parts = s.parts;
         const dim3 grid((unsigned)s.parts, (unsigned)group_sets(p.groups, p.width, values.value));
-        logmel_group_back_sums_kernel<T, gate.value, values.value>
-            <<<grid, kWork, 0, stream>>>(p);
+        if (seq_wide(in))
+          logmel_group_back_sums_kernel<T, gate.value, values.value, true>
+              <<<grid, kWork, 0, stream>>>(p);
+        else
+          logmel_group_back_sums_kernel<T, gate.value, values.value, false>
+              <<<grid, kWork, 0, stream>>>(p);
         logmel_group_join_kernel<T, true><<<join_grid(in), 256, 0, stream>>>(p);
         logmel_group_dx_kernel<T, gate.value, values.value><<<grid, kWork, 0, stream>>>(p);
       });

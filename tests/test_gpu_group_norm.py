@@ -304,3 +304,36 @@ def test_layer_along_streams(env):
     # 128-term products of values to 4 (the norm) and 1/3: sums to about 4, off
     # by up to 128 roundings of 2^-24 times 20; then as above, 2^-10 in all
     assert (got - whole).abs().max().item() <= 2.0 ** -10 * whole.abs().max().item()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("groups,width", [(1, 4096), (2, 257), (1, 8192)])
+def test_group_norm_wide_groups_of_many_sequences(env, dtype, groups, width):
+    say(f"group norm wide, many sequences {dtype} {groups} x {width}")
+    norm_case(env, dtype, groups, width, lens=[1, 0, 2] * 100, behind=2, silu=True, seed=31)
+
+
+def test_group_norm_parameter_sums_do_not_grow_with_sequences(env):
+    """Half a million sequences of one row, of a group too wide to be summed in
+    registers: parts of 512 sequences. Every row is the same, so a parameter's
+    sum is the count times one value; its parts are rounded once (2^-24), as the
+    result is, and dn xh once before (dn itself is dy)."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say("group norm parameter sums of 2^19 sequences")
+    rows, width = 1 << 19, 257
+    x = torch.ones((rows, width), device=dev)
+    x[:, ::2] = -1.0
+    dy = torch.full((rows, width), 1.0 + 0.4 * 2.0 ** -16, device=dev)
+    off = torch.arange(rows + 1, device=dev)
+    w, b = torch.ones(width, device=dev), torch.zeros(width, device=dev)
+    more = dict(weight=w, bias=b, seq_offsets=off, max_frames=1)
+    st = torch.empty((rows, 1, 2), device=dev)
+    y = lm.logmel_group_norm(plan, x, 1, stats=st, **more)
+    assert (y == y[0]).all()                      # xh, as weight is 1 and bias 0
+    g = lm.logmel_group_norm_backward(plan, dy, x, 1, stats=st, **more)
+    u = 2.0 ** -24
+    want = host(dy[0]) * rows
+    assert (np.abs(host(g["dbias"]) - want) <= 2 * u * want).all()
+    want = host(dy[0]) * host(y[0]) * rows
+    assert (np.abs(host(g["dweight"]) - want) <= 3 * u * np.abs(want)).all()
