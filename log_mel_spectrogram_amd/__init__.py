@@ -1030,7 +1030,7 @@ def _attention_input(plan, q, k, v, log_decay, seq_offsets, qk_heads, scale, sta
     torch = _torch()
     _on_device(q, "q", plan)
     ty = _row_type(q.dtype)
-    if type(log_decay) is not torch.Tensor or log_decay.dim() != 1 or log_decay.numel() == 0:
+    if not isinstance(log_decay, torch.Tensor) or log_decay.dim() != 1 or not log_decay.numel():
         raise ValueError("log_decay must be a tensor [heads]")
     heads = log_decay.shape[0]
     pg = _params(log_decay, "log_decay", (heads,), plan)

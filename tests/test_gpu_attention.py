@@ -503,3 +503,25 @@ def test_attention_values_near_the_largest(env, kind, dtype, dk, dv, lens, max_f
     if kind == "v":
         for lo, hi in ((0, at[0]), (lens[0], at[1])):
             assert torch.equal(got["o"][lo:hi], first["o"][lo:hi])
+
+
+def test_attention_takes_a_module_s_parameters(env):
+    """Every operand may be a torch.nn.Parameter where no graph is recorded,
+    the decays too; where one is, it is refused as other tensors are."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say("attention of parameters")
+    gen = torch.Generator(device=dev).manual_seed(23)
+    x = torch.randn((9, 16), generator=gen, device=dev)
+    g = torch.tensor([-0.1, -0.2], device=dev)
+    s = torch.randn((2, 2, 8, 8), generator=gen, device=dev)
+    off = torch.tensor([0, 5, 9], device=dev)
+    px, pg, ps = (torch.nn.Parameter(t.clone()) for t in (x, g, s))
+    o = lm.logmel_linear_attention(plan, x, x, x, g, off, state=s)
+    with torch.no_grad():
+        assert torch.equal(lm.logmel_linear_attention(plan, px, px, px, pg, off, state=ps), o)
+        grads = lm.logmel_linear_attention_backward(plan, x, px, px, px, pg, off, state=ps)
+    for a, b in zip(grads, lm.logmel_linear_attention_backward(plan, x, x, x, x, g, off, state=s)):
+        assert torch.equal(a, b)
+    with pytest.raises(RuntimeError):
+        lm.logmel_linear_attention(plan, x, x, x, pg, off)
