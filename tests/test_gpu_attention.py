@@ -525,3 +525,79 @@ def test_attention_takes_a_module_s_parameters(env):
         assert torch.equal(a, b)
     with pytest.raises(RuntimeError):
         lm.logmel_linear_attention(plan, x, x, x, pg, off)
+
+
+# lengths that are split by parts at each of the widths below: 1603 rows are 7 parts
+# of bf16 rows and 13 of others
+SPLIT = [900, 0, 700, 3]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("heads,qk", [(6, 2), (3, 3)])
+@pytest.mark.parametrize("dk,dv", [(40, 71), (71, 40), (128, 128), (16, 64), (64, 16), (128, 33)])
+def test_attention_parts_of_every_shape(env, dtype, heads, qk, dk, dv):
+    """Parts with shared heads (whose sums lie before the states in the
+    workspace), of unequal widths (dv reads the states that dk formed), and of
+    either number of wavefronts."""
+    say(f"attention parts {dtype} {heads} heads, {qk} of q and k, {dk} x {dv}")
+    attn_case(env, dtype, SPLIT, heads=heads, qk=qk, dk=dk, dv=dv, behind=5, seed=24,
+              layout="odd" if dk == 40 else "dense", state=dk != 16)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_attention_parts_state_in_place(env, dtype):
+    say(f"attention parts in place {dtype}")
+    attn_case(env, dtype, SPLIT, heads=6, qk=2, dk=40, dv=71, train=False, in_place=True, seed=25)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_attention_not_finite_across_parts(env, dtype):
+    """In the first, a middle and the last part of a sequence: earlier rows,
+    other sequences and other heads keep every bit, and the states between the
+    parts carry it to the last row. In the gradient as the formulas have it: of
+    do to dk and dv of its row and earlier ones and dq of its row, of k to dq of
+    its row and later ones and dv of its row, of v to dq and dk so."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say(f"attention not finite across parts {dtype}")
+    dt = getattr(torch, dtype)
+    lens, heads, d, e = [500, 1700, 300], 2, 32, 72
+    rows, lo, hi = sum(lens), 500, 2200
+    gen = torch.Generator(device=dev).manual_seed(26)
+    q, k = (torch.randn((rows, heads * d), generator=gen, device=dev).to(dt) for _ in range(2))
+    v, do = (torch.randn((rows, heads * e), generator=gen, device=dev).to(dt) for _ in range(2))
+    off = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), device=dev)
+    g = torch.tensor([-0.001, -0.002], device=dev)
+
+    def call():
+        o = lm.logmel_linear_attention(plan, q, k, v, g, off)
+        grads = lm.logmel_linear_attention_backward(plan, do, q, k, v, g, off)
+        return dict(zip(("o", "dq", "dk", "dv"), (o, *grads)))
+
+    first = call()
+    wide = dict(o=e, dq=d, dk=d, dv=e)
+    # of each operand the rows of each result that it reaches, from its own
+    later, earlier, own, none = (0, hi), (lo, 1), (0, 1), None
+    reach = dict(q=dict(o=own, dq=none, dk=earlier, dv=earlier),
+                 k=dict(o=later, dq=later, dk=none, dv=own),
+                 v=dict(o=later, dq=later, dk=own, dv=none),
+                 do=dict(o=none, dq=own, dk=earlier, dv=earlier))
+    for name, x in dict(q=q, k=k, v=v, do=do).items():
+        for row, head in ((lo + 3, 0), (lo + 850, 1), (hi - 2, 0)):
+            col = head * (x.shape[1] // heads) + 7
+            for bad in (float("nan"), float("inf")):
+                keep = x[row, col].clone()
+                x[row, col] = bad
+                got = call()
+                x[row, col] = keep
+                for key, to in reach[name].items():
+                    same = torch.ones_like(first[key], dtype=torch.bool)
+                    cols = slice(head * wide[key], (head + 1) * wide[key])
+                    if to is not none:
+                        a, b = {later: (row, hi), earlier: (lo, row + 1), own: (row, row + 1)}[to]
+                        same[a:b, cols] = False
+                        for far in (a, b - 1):
+                            assert not torch.isfinite(got[key][far, cols]).all(), (name, key, row)
+                    assert torch.equal(got[key][same], first[key][same]), (name, key, row, bad)
+    again = call()
+    assert all(torch.equal(again[key], first[key]) for key in first)
