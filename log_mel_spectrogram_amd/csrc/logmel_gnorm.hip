@@ -48,7 +48,7 @@ struct GroupArgs {
                         // that starts in it and leaves it
   double* wide;         // [parts][2][channels]: `part` while its pieces are added, of groups
                         // of more vectors than a workgroup has lanes
-  int64_t part_rows, parts;
+  int64_t part_rows;
 };
 
 // n of a centred value, and what follows from it. T: whose sigmoid. Over sequences
@@ -206,11 +206,6 @@ struct Piece {
     }
   }
   __device__ __forceinline__ float at(int j, int i) const { return (float)v[j].v[i]; }
-  __device__ __forceinline__ void unpack_anew() {
-    if constexpr (sizeof(T) == 2)
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) repack(v[j]);
-  }
 };
 
 template <typename T, int kLanes, int kVecs, int V>
@@ -1105,7 +1100,6 @@ hipError_t logmel_launch_group(const logmel_group_norm_input& in, void* y, int64
     p.pieces = static_cast<double*>(ws);
     p.stats = stats ? stats : reinterpret_cast<float*>(static_cast<char*>(ws) + s.pieces);
     p.part_rows = part_rows_of(in, cus);
-    p.parts = s.parts;
     const dim3 grid((unsigned)s.parts, (unsigned)group_sets(p.groups, p.width, values.value));
     if (s.parts) logmel_group_stats_kernel<T, values.value><<<grid, kWork, 0, stream>>>(p);
     logmel_group_join_kernel<T, false><<<join_grid(in), 256, 0, stream>>>(p);
@@ -1160,7 +1154,6 @@ hipError_t logmel_launch_group_backward(const logmel_group_norm_input& in, const
         p.part = params ? part : nullptr;
         p.wide = reinterpret_cast<double*>(at + s.pieces + s.stats);
         p.part_rows = part_rows_of(in, cus);
-        p.parts = s.parts;
         const dim3 grid((unsigned)s.parts, (unsigned)group_sets(p.groups, p.width, values.value));
         if (seq_wide(in))
           logmel_group_back_sums_kernel<T, gate.value, values.value, true>
