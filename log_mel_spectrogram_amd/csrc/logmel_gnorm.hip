@@ -70,42 +70,6 @@ struct Act {
   }
 };
 
-// 1 / sqrt(m) to an ulp: the hardware's estimate and a Newton step; a subnormal
-// m, which the estimate takes for 0, is scaled before. Infinity gives 0.
-__device__ __forceinline__ float inv_root(float m) {
-  const bool small = m < 0x1p-64f;
-  m = small ? m * 0x1p64f : m;
-  const float r = __builtin_amdgcn_rsqf(m);
-  const float e = __builtin_fmaf(-m * r, r, 1.0f);
-  const float root = m < __builtin_inff() ? __builtin_fmaf(0.5f * r, e, r) : r;
-  return small ? root * 0x1p32f : root;
-}
-
-// Sums over kLanes lanes (a power of two up to 64), in every one of them.
-template <int kLanes>
-__device__ __forceinline__ float lane_sum(float v) {
-  auto dpp = [&](auto pattern) {
-    return v + __builtin_bit_cast(
-                   float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v),
-                                                      decltype(pattern)::value, 0xf, 0xf, true));
-  };
-  if constexpr (kLanes >= 2) v = dpp(std::integral_constant<int, 0xB1>{});    // quad_perm 1 0 3 2
-  if constexpr (kLanes >= 4) v = dpp(std::integral_constant<int, 0x4E>{});    // quad_perm 2 3 0 1
-  if constexpr (kLanes >= 8) v = dpp(std::integral_constant<int, 0x141>{});   // row_half_mirror
-  if constexpr (kLanes >= 16) v = dpp(std::integral_constant<int, 0x140>{});  // row_mirror
-  if constexpr (kLanes >= 32) {
-    const unsigned b = __builtin_bit_cast(unsigned, v);
-    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-    v = __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
-  }
-  if constexpr (kLanes >= 64) {
-    const unsigned c = __builtin_bit_cast(unsigned, v);
-    const auto s = __builtin_amdgcn_permlane32_swap(c, c, false, false);
-    v = __builtin_bit_cast(float, (unsigned)s[0]) + __builtin_bit_cast(float, (unsigned)s[1]);
-  }
-  return v;
-}
-
 // ------------------------------------------------------------ row by row
 //
 // Memory bounds both directions: 64 x 2998 x 8 x 64 bf16 with its gate 116 us (589 MB,
@@ -523,6 +487,24 @@ __device__ __forceinline__ void group_sums(const Columns<V>& k, double (&red)[kW
   __syncthreads();
 }
 
+// Weight and bias of V channels from c on, 1 and 0 where they are absent.
+template <typename T, int V>
+__device__ __forceinline__ void affine_at(const GroupArgs<T>& p, int64_t c, float (&w)[V],
+                                          float (&b)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) w[j] = 1.0f, b[j] = 0.0f;
+  if (p.weight) {
+    const auto t = row_load<float, V>(p.weight + c);
+#pragma unroll
+    for (int j = 0; j < V; ++j) w[j] = t.v[j];
+  }
+  if (p.bias) {
+    const auto t = row_load<float, V>(p.bias + c);
+#pragma unroll
+    for (int j = 0; j < V; ++j) b[j] = t.v[j];
+  }
+}
+
 constexpr int kBatch = 8;   // rows of a lane on their way at a time
 
 // f(row, whole) for a lane's rows first, first + step, .. below to, kN at a time:
@@ -655,18 +637,7 @@ __global__ __launch_bounds__(kWork) void logmel_group_apply_kernel(GroupArgs<T> 
     const int64_t c = (int64_t)k.g0 * p.width + (int64_t)v * V;
     const int g = k.g0 + v / k.vg;
     float w[V], b[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) w[j] = 1.0f, b[j] = 0.0f;
-    if (p.weight) {
-      const auto t = row_load<float, V>(p.weight + c);
-#pragma unroll
-      for (int j = 0; j < V; ++j) w[j] = t.v[j];
-    }
-    if (p.bias) {
-      const auto t = row_load<float, V>(p.bias + c);
-#pragma unroll
-      for (int j = 0; j < V; ++j) b[j] = t.v[j];
-    }
+    affine_at(p, c, w, b);
     for_pieces(p, i0, [&](int64_t i, int64_t from, int64_t to, bool, bool) {
       const float mean = p.stats[(i * p.groups + g) * 2];
       const float root = p.stats[(i * p.groups + g) * 2 + 1];
@@ -757,18 +728,7 @@ __global__ __launch_bounds__(kWork) void logmel_group_back_sums_kernel(GroupArgs
       const float mean = p.stats[(i * p.groups + g) * 2];
       const float root = p.stats[(i * p.groups + g) * 2 + 1];
       float w[V], b[V];
-#pragma unroll
-      for (int j = 0; j < V; ++j) w[j] = 1.0f, b[j] = 0.0f;
-      if (p.weight) {
-        const auto t = row_load<float, V>(p.weight + c);
-#pragma unroll
-        for (int j = 0; j < V; ++j) w[j] = t.v[j];
-      }
-      if (p.bias) {
-        const auto t = row_load<float, V>(p.bias + c);
-#pragma unroll
-        for (int j = 0; j < V; ++j) b[j] = t.v[j];
-      }
+      affine_at(p, c, w, b);
       double d1[V], d2[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) d1[j] = d2[j] = 0.0;
@@ -869,18 +829,7 @@ __global__ __launch_bounds__(kWork) void logmel_group_dx_kernel(GroupArgs<T> p) 
     const int64_t c = (int64_t)k.g0 * p.width + (int64_t)v * V;
     const int g = k.g0 + v / k.vg;
     float w[V], b[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) w[j] = 1.0f, b[j] = 0.0f;
-    if (p.weight) {
-      const auto t = row_load<float, V>(p.weight + c);
-#pragma unroll
-      for (int j = 0; j < V; ++j) w[j] = t.v[j];
-    }
-    if (p.bias) {
-      const auto t = row_load<float, V>(p.bias + c);
-#pragma unroll
-      for (int j = 0; j < V; ++j) b[j] = t.v[j];
-    }
+    affine_at(p, c, w, b);
     for_pieces(p, i0, [&](int64_t i, int64_t from, int64_t to, bool, bool) {
       const int64_t at = (i * p.groups + g) * 2;
       const float mean = p.stats[at], root = p.stats[at + 1];

@@ -62,50 +62,8 @@ struct NormGradArgs {
   float* part;   // [workgroups][2][channels]: sums of G n act and of dz y / rms(y); or null
 };
 
-// 1 / sqrt(m): the hardware's estimate (one ulp) and one Newton step, a third
-// of the instructions of a square root and a division, which two or three
-// times a row are as many as four of its values take. The estimate takes a
-// subnormal m for 0, so a small one is scaled by 2^64 before and the root by
-// 2^32 after (five instructions a root, at most 0.4 % of a call). Infinity gives 0.
-__device__ __forceinline__ float inv_root(float m) {
-  const bool small = m < 0x1p-64f;
-  m = small ? m * 0x1p64f : m;
-  const float r = __builtin_amdgcn_rsqf(m);
-  const float e = __builtin_fmaf(-m * r, r, 1.0f);
-  const float root = m < __builtin_inff() ? __builtin_fmaf(0.5f * r, e, r) : r;
-  return small ? root * 0x1p32f : root;
-}
-
 // What stands between res and y.
 enum Parts { kNone, kNorm, kGated };
-
-template <int kPattern>
-__device__ __forceinline__ float dpp_add(float v) {
-  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
-                                           0, __builtin_bit_cast(int, v), kPattern, 0xf, 0xf, true));
-}
-
-// Sum over 16, 32 or 64 lanes, in every one of them: neighbours, pairs, then
-// the mirrored half rows and rows of 16, which hold one value each by then;
-// rows and halves of the wavefront by the lane swaps.
-template <int kLanes>
-__device__ __forceinline__ float lane_sum(float v) {
-  v = dpp_add<0xB1>(v);    // quad_perm 1 0 3 2
-  v = dpp_add<0x4E>(v);    // quad_perm 2 3 0 1
-  v = dpp_add<0x141>(v);   // row_half_mirror
-  v = dpp_add<0x140>(v);   // row_mirror
-  if constexpr (kLanes >= 32) {
-    const unsigned b = __builtin_bit_cast(unsigned, v);
-    const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
-    v = __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
-  }
-  if constexpr (kLanes >= 64) {
-    const unsigned c = __builtin_bit_cast(unsigned, v);
-    const auto s = __builtin_amdgcn_permlane32_swap(c, c, false, false);
-    v = __builtin_bit_cast(float, (unsigned)s[0]) + __builtin_bit_cast(float, (unsigned)s[1]);
-  }
-  return v;
-}
 
 // Wavefronts per SIMD that the kernels leave room for: the gradient holds eight
 // values of five operands per lane within the 128 registers of four.
