@@ -368,9 +368,9 @@ int logmel_resample(const logmel_resampler* r, const void* d_samples, int sample
 /* ---------------------------------------------------------------------------
  * Operators over packed rows, for the layers that take the front end's rows:
  * a gated recurrence and linear attention along each sequence, the norms
- * around a block, and the group norm. The rows are those of logmel_compute (clip i's frames are rows
- * [frame_offsets[i], frame_offsets[i+1])) or of a push (stream j's new frames
- * are rows [fo[j], fo[j+1])), of any width.
+ * around a block, and the group norm. The rows are those of logmel_compute
+ * (clip i's frames are rows [frame_offsets[i], frame_offsets[i+1])) or of a
+ * push (stream j's new frames are rows [fo[j], fo[j+1])), of any width.
  *
  * Conventions beside those above:
  *  - A row operand is [rows][channels] of `type` (LOGMEL_F32, LOGMEL_F16 or
@@ -378,7 +378,8 @@ int logmel_resample(const logmel_resampler* r, const void* d_samples, int sample
  *    contiguous, row r at element r * stride of its pointer (stride >=
  *    channels, so the column slices of one wider product are operands as
  *    they are). Any element alignment is accepted. Arithmetic, sums and
- *    states are fp32; a row output is rounded once, to nearest even.
+ *    states are fp32 (but for the factors of linear attention's matrix
+ *    products, see there); a row output is rounded once, to nearest even.
  *  - Parameters, states and their gradients are contiguous fp32.
  *  - An output may not overlap another operand (INVALID_ARGUMENT), except
  *    where a call says so.
@@ -540,8 +541,16 @@ int logmel_block_norm_backward(const logmel_plan* plan, const logmel_norm_input*
  * A row operand holds its heads side by side: head h of q is columns
  * [h head_dk, (h + 1) head_dk).
  * A NaN or infinity in q stays in its row and head; one in k or v stays in its
- * sequence and in the heads that read it, from its row on, where an infinity
- * may come out as NaN. */
+ * sequence and in the heads that read it, from its row on; one in d_state in
+ * its sequence, head and column of head_dv; an infinity may come out as NaN.
+ * Sequences of more than 16 rows are matrix products, whose factors are sums of
+ * bf16 pieces and whose sums are fp32. An fp32 row is three pieces and an fp16
+ * row two, which hold it exactly; of their products those below 2^-25 and 2^-18
+ * of the largest are left out. What products make, the scores q k^T and the state
+ * that meets q, is three pieces for fp32 rows and two for others: 2^-18 of it is
+ * left out, where the output keeps 2^-9 or 2^-12. What enters the state is three
+ * pieces in every type. A score of 2-byte rows from 0x1.ffp127 on counts as
+ * infinite. */
 #define LOGMEL_ATTENTION_MAX_HEAD_DIM 128
 typedef struct logmel_attention_input {
   int32_t type;
@@ -549,10 +558,15 @@ typedef struct logmel_attention_input {
   int64_t heads;                /* of v, of o, of the decays and of the states */
   int64_t qk_heads;             /* of q and k; divides heads (INVALID_ARGUMENT where not): heads
                                    h heads / qk_heads on read the same q and k */
-  int64_t head_dk, head_dv;     /* 1..LOGMEL_ATTENTION_MAX_HEAD_DIM (UNSUPPORTED beyond) */
+  int64_t head_dk, head_dv;     /* 1..LOGMEL_ATTENTION_MAX_HEAD_DIM (UNSUPPORTED beyond). Below 8
+                                   (bf16) or 4 the rows are worked one after the other: 64 x 2998
+                                   x 8 heads of 7 bf16 channels 1.7 ms, of 8 0.16 */
   int64_t n_seq;                /* sequences, offsets and hint as logmel_scan_input's */
   const int64_t* d_seq_offsets;
-  int64_t max_frames;
+  int64_t max_frames;           /* but that its lack costs more: rows of one sequence, as 0 says,
+                                   are worked in few parts, sequence after sequence. 512 streams x
+                                   8 heads x 64 bf16, of 8 rows each 331 us instead of 42, of 1 row
+                                   113 instead of 27 (fp32 1,260) */
   const void* d_q;              /* [rows][qk_heads head_dk], as k */
   int64_t q_stride;
   const void* d_k;
@@ -608,7 +622,12 @@ int logmel_linear_attention_backward(const logmel_plan* plan, const logmel_atten
  *     n = (x - mean) / sqrt(var + eps) * weight + bias
  *     y = act(n) * silu(gate),    silu(g) = g sigmoid(g),
  * var the mean square of x - mean. d_weight NULL: 1. d_bias NULL: 0. d_gate
- * NULL: no silu factor. A NaN or infinity in x reaches what its mean does. */
+ * NULL: no silu factor. A NaN or infinity in x reaches what its mean does.
+ * Squares are fp32: a group whose variance plus eps is 0 gives NaN, one whose
+ * squares overflow act(bias) in place of act(n), one whose sums do NaN. Over sequences the mean is one fp32: y and the
+ * gradients are those of x - mean with a mean that is up to 2^-24 of itself
+ * off, of rows at a level 10^4 times their spread 6e-4 of that spread (rows by
+ * themselves keep what its rounding takes). */
 #define LOGMEL_ACT_NONE 0
 #define LOGMEL_ACT_SILU 1
 typedef struct logmel_group_norm_input {

@@ -1059,7 +1059,8 @@ def logmel_linear_attention(plan: Plan, q, k, v, log_decay, seq_offsets, qk_head
     dk and dv at most ATTENTION_MAX_HEAD_DIM. log_decay: fp32 [heads], at most 0;
     it has no gradient. qk_heads (default: heads) divides heads; heads / qk_heads
     neighbouring heads read the same q and k. seq_offsets and max_frames as in
-    logmel_gated_scan; rows from the last offset on stay as they are in out.
+    logmel_gated_scan (give max_frames in pushes: without it 512 streams of 8 rows
+    take eight times as long); rows from the last offset on stay as they are in out.
     state (S before each sequence, default 0) and state_out (S after it; may be
     state): fp32 [n_seq, heads, dk, dv]."""
     _check_stream(stream, plan)

@@ -79,11 +79,13 @@ __device__ __forceinline__ float decayed(Decay d, float x) {
 // sixteenth row. Eight rows at a time are laid out in LDS, worked one after the
 // other, and their products with the state joined at the end. Right for any
 // length; the form for single rows and short pushes, whose time is that of
-// reading and writing the states (512 x 8 x 8 x 64 bf16, 134 MB of states: 44 us;
-// a tenth more with the eight rows worked as a chunk, which goes over them twice).
+// reading and writing the states (512 x 8 x 8 x 64 bf16, 134 MB of states: 43 us).
 constexpr int kStepRows = 8;
 constexpr int kSlab = 64;
-constexpr int kShort = 16;   // rows of the longest sequence that this form is taken for
+// Rows of the longest sequence that this form is taken for: 64 sequences x 16 x 8 x 64
+// bf16 15.1 us, 17.5 in chunks, x 24 19.1 and 18.7, x 48 32 and 20; 512 sequences x 16
+// 63 and 117, x 32 102 and 119, x 48 145 and 122 (fp32 within a tenth).
+constexpr int kShort = 16;
 
 template <typename T, int DA>
 __global__ __launch_bounds__(256) void logmel_attn_rows_kernel(AttnJob<T> p, int slabs,
@@ -1216,6 +1218,18 @@ struct AttnSplit {
 
 // dc: the narrowest c of the jobs that share the split; widest: the longest row
 // stride.
+//
+// The times are counted in chunks that one workgroup works one after the other. Both
+// ways measured, us of n sequences of 2998 rows, 8 heads x 64 (bf16; fp32), parts and a
+// workgroup per sequence:
+//   n = 8     92, 158   (121, 278)
+//   n = 16   122, 157   (195, 279)
+//   n = 24   161, 159   (266, 280)
+//   n = 32   197, 160   (331, 283)
+//   n = 48   265, 211   (476, 408)
+// of which parts are taken to n = 32, a fifth too long at its end. One sequence of 8
+// heads: 384 rows bf16 50, 28 (taken), 1024 rows 53 (taken), 58; fp32 384 rows 51
+// (taken), 43, 512 rows 52 (taken), 55.
 AttnSplit split_of(const logmel_attention_input& in, int64_t dc, int64_t widest, int cus) {
   AttnSplit s{AttnSplit::kSequences, 0, 0};
   const int64_t longest =
@@ -1228,7 +1242,7 @@ AttnSplit split_of(const logmel_attention_input& in, int64_t dc, int64_t widest,
     s.how = AttnSplit::kRows;
     return s;
   }
-  const int64_t chunk = in.type == LOGMEL_BF16 ? 64 : 32;
+  const int64_t chunk = in.type == LOGMEL_BF16 ? 64 : 32;   // the output's at most widths
   const int64_t lanes = in.heads;   // workgroups side by side
   // those that are resident: of four columns' wavefronts two on a compute unit, of
   // eight one (70,001 x 6 x 40 x 71 fp16 287 us with one part for each, 336 with two
@@ -1242,8 +1256,9 @@ AttnSplit split_of(const logmel_attention_input& in, int64_t dc, int64_t widest,
   int64_t rows = ceil_div(ceil_div(in.rows, most < 1 ? 1 : most), chunk) * chunk;
   rows = rows < 4 * chunk ? 4 * chunk : rows;
   const int64_t parts = ceil_div(in.rows, rows);
-  // the states between parts are formed in a pass of their own, of about half the
-  // time, and joined
+  // the states between parts are formed in a pass of their own, counted as half of the
+  // output's (0.38 of it for 521,998 x 2 x 64 fp32), and joined by a launch, counted
+  // as four chunks
   const double part_time =
       1.5 * (double)(rows / chunk) * (double)ceil_div(parts * lanes, slots) + 4.0;
   if (parts > 1 && part_time < seq_time) {

@@ -601,3 +601,39 @@ def test_attention_not_finite_across_parts(env, dtype):
                     assert torch.equal(got[key][same], first[key][same]), (name, key, row, bad)
     again = call()
     assert all(torch.equal(again[key], first[key]) for key in first)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lens,max_frames", [([8, 0, 3], 8), ([150, 90], 150), ([1300, 700], 0)])
+def test_attention_state_not_finite_stays_in_its_column(env, dtype, lens, max_frames):
+    """A NaN or infinity in an initial state reaches its column of the outputs
+    and of the state behind them, in its sequence and head."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say(f"attention state not finite {dtype} {lens}")
+    dt = getattr(torch, dtype)
+    heads, d, e, n = 2, 32, 48, len(lens)
+    gen = torch.Generator(device=dev).manual_seed(27)
+    q, k = (torch.randn((sum(lens), heads * d), generator=gen, device=dev).to(dt)
+            for _ in range(2))
+    v = torch.randn((sum(lens), heads * e), generator=gen, device=dev).to(dt)
+    s = torch.randn((n, heads, d, e), generator=gen, device=dev)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), device=dev)
+    g = torch.tensor([-0.001, 0.0], device=dev)
+
+    def call():
+        so = torch.empty_like(s)
+        o = lm.logmel_linear_attention(plan, q, k, v, g, off, state=s, state_out=so,
+                                       max_frames=max_frames)
+        return o, so
+
+    first = call()
+    for bad in (float("nan"), float("inf")):
+        s[0, 1, 5, 40] = bad
+        o, so = call()
+        s[0, 1, 5, 40] = 1.0
+        same, same_s = (torch.ones_like(t, dtype=torch.bool) for t in first)
+        same[:lens[0], e + 40] = False
+        same_s[0, 1, :, 40] = False
+        assert torch.equal(o[same], first[0][same]) and torch.equal(so[same_s], first[1][same_s])
+        assert not torch.isfinite(o[lens[0] - 1, e + 40]) and not torch.isfinite(so[0, 1, 5, 40])

@@ -337,3 +337,30 @@ def test_group_norm_parameter_sums_do_not_grow_with_sequences(env):
     assert (np.abs(host(g["dbias"]) - want) <= 2 * u * want).all()
     want = host(dy[0]) * host(y[0]) * rows
     assert (np.abs(host(g["dweight"]) - want) <= 3 * u * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("over", ["row", "clip"])
+def test_group_norm_squares_that_overflow(env, dtype, over):
+    """A group whose squares pass fp32 is normed to 0: y is that of a constant
+    group; other groups keep every bit. Where the sums pass it too, NaN."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say(f"group norm of squares that overflow {dtype} {over}")
+    gen = torch.Generator(device=dev).manual_seed(32)
+    x = torch.randn((40, 64), generator=gen, device=dev).to(getattr(torch, dtype))
+    b = torch.randn(64, generator=gen, device=dev)
+    off = torch.tensor([0, 25, 40], device=dev) if over == "clip" else None
+
+    def call(t):
+        return lm.logmel_group_norm(plan, t, 4, bias=b, activation="silu", seq_offsets=off)
+
+    y, flat = call(x), call(torch.full_like(x, 2.0))
+    big = x.clone()
+    big[:, 16:32] *= 1e25
+    got = call(big)
+    assert torch.equal(got[:, 16:32], flat[:, 16:32])
+    big[:, 16:32] = 3e38
+    assert torch.isnan(call(big)[:, 16:32]).all()
+    for lo, hi in ((0, 16), (32, 64)):
+        assert torch.equal(got[:, lo:hi], y[:, lo:hi])
