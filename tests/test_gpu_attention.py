@@ -637,3 +637,30 @@ def test_attention_state_not_finite_stays_in_its_column(env, dtype, lens, max_fr
         same_s[0, 1, :, 40] = False
         assert torch.equal(o[same], first[0][same]) and torch.equal(so[same_s], first[1][same_s])
         assert not torch.isfinite(o[lens[0] - 1, e + 40]) and not torch.isfinite(so[0, 1, 5, 40])
+
+
+@pytest.mark.parametrize("length,max_frames", [(17, 17), (4, 4)])
+def test_attention_more_sequences_than_a_launch_has_workgroups(env, length, max_frames):
+    """Workgroups that take several sequences: the first, the last and others
+    between against the fp64 form, the states too."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    heads, d = 4, 8
+    n = 300_000 if length > 16 else 1_100_000     # items past 2^20 and 2^22
+    say(f"attention of {n} sequences x {length}")
+    gen = torch.Generator(device=dev).manual_seed(28)
+    q, k, v = (torch.randn((n * length, heads * d), generator=gen, device=dev).to(torch.bfloat16)
+               for _ in range(3))
+    s = torch.randn((n, heads, d, d), generator=gen, device=dev)
+    so = torch.empty_like(s)
+    g = torch.tensor([-0.1, -0.5, 0.0, -2.0], device=dev)
+    off = torch.arange(n + 1, device=dev) * length
+    o = lm.logmel_linear_attention(plan, q, k, v, g, off, state=s, state_out=so,
+                                   max_frames=max_frames)
+    for at in (0, n // 2 - 1, (1 << 20) // heads - 1, (1 << 20) // heads, n - 2):
+        rows = slice(at * length, (at + 2) * length)
+        val, tol = attn_ref.attention(*(host(x[rows]) for x in (q, k, v)), host(g),
+                                      np.arange(3) * length, heads, 1.0, host(s[at:at + 2]),
+                                      dtype="bfloat16")
+        check(o[rows], val["o"], tol["o"], "o")
+        check(so[at:at + 2], val["state_out"], tol["state_out"], "state_out")

@@ -364,3 +364,25 @@ def test_group_norm_squares_that_overflow(env, dtype, over):
     assert torch.isnan(call(big)[:, 16:32]).all()
     for lo, hi in ((0, 16), (32, 64)):
         assert torch.equal(got[:, lo:hi], y[:, lo:hi])
+
+
+def test_group_norm_more_sequences_than_a_launch_has_wavefronts(env):
+    """Half a million sequences of two rows and 16 groups: those across parts
+    are joined by wavefronts that take several."""
+    lm, plan, torch = env
+    dev = torch.device("cuda", 0)
+    say("group norm of 2^19 sequences x 16 groups")
+    n, groups, width = 1 << 19, 16, 4
+    gen = torch.Generator(device=dev).manual_seed(33)
+    x, dy = (torch.randn((2 * n - 1, groups * width), generator=gen, device=dev) for _ in range(2))
+    off = torch.arange(n + 1, device=dev) * 2 - 1
+    off[0] = 0                                      # parts begin inside sequences
+    st = torch.empty((n, groups, 2), device=dev)
+    y = lm.logmel_group_norm(plan, x, groups, seq_offsets=off, stats=st, max_frames=2)
+    g = lm.logmel_group_norm_backward(plan, dy, x, groups, seq_offsets=off, stats=st, max_frames=2)
+    for at in (1, 2 * (n // 3) - 1, 2 * n - 1 - 4000):
+        rows = slice(at, at + 4000)
+        val, tol = attn_ref.group_norm(host(x[rows]), groups, off=np.arange(2001) * 2,
+                                       dy=host(dy[rows]))
+        check(y[rows], val["y"], tol["y"], "y")
+        check(g["dx"][rows], val["dx"], tol["dx"], "dx")
