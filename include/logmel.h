@@ -543,8 +543,9 @@ int logmel_block_norm_backward(const logmel_plan* plan, const logmel_norm_input*
  * A NaN or infinity in q stays in its row and head; one in k or v stays in its
  * sequence and in the heads that read it, from its row on; one in d_state in
  * its sequence, head and column of head_dv; an infinity may come out as NaN.
- * Sequences of more than 16 rows are matrix products, whose factors are sums of
- * bf16 pieces and whose sums are fp32. An fp32 row is three pieces and an fp16
+ * Calls whose longest sequence is not known to have at most 16 rows are worked as
+ * matrix products, whose factors are sums of bf16 pieces and whose sums are fp32
+ * (others, and rows and heads that the products do not take, in fp32). An fp32 row is three pieces and an fp16
  * row two, which hold it exactly; of their products those below 2^-25 and 2^-18
  * of the largest are left out. What products make, the scores q k^T and the state
  * that meets q, is three pieces for fp32 rows and two for others: 2^-18 of it is
