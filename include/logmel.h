@@ -545,12 +545,13 @@ int logmel_block_norm_backward(const logmel_plan* plan, const logmel_norm_input*
  * its sequence, head and column of head_dv; an infinity may come out as NaN.
  * Calls whose longest sequence is not known to have at most 16 rows are worked as
  * matrix products, whose factors are sums of bf16 pieces and whose sums are fp32
- * (others, and rows and heads that the products do not take, in fp32). An fp32 row is three pieces and an fp16
- * row two, which hold it exactly; of their products those below 2^-25 and 2^-18
- * of the largest are left out. What products make, the scores q k^T and the state
- * that meets q, is three pieces for fp32 rows and two for others: 2^-18 of it is
- * left out, where the output keeps 2^-9 or 2^-12. What enters the state is three
- * pieces in every type. A score of 2-byte rows from 0x1.ffp127 on counts as
+ * (others, and rows and heads that the products do not take, in fp32). An fp32
+ * row is three pieces and an fp16 row two, which hold it exactly; of their
+ * products those below 2^-25 and 2^-18 of the largest are left out. What products
+ * make, the scores q k^T and the state that meets q, is three pieces for fp32 rows
+ * and two for others: 2^-18 of it is left out, where the output keeps 2^-9 or
+ * 2^-12. What enters the state is three pieces in every type. A score of 2-byte
+ * rows from 0x1.ffp127 on counts as
  * infinite. */
 #define LOGMEL_ATTENTION_MAX_HEAD_DIM 128
 typedef struct logmel_attention_input {
